@@ -87,7 +87,9 @@ typedef enum {
     LA_OP_PREFIX = 3,
     LA_OP_DECODE = 4,
     LA_OP_NONCAUSAL_BWD = 5,  /* la_noncausal_backward */
-    LA_OP_CAUSAL_BWD = 6      /* la_causal_backward */
+    LA_OP_CAUSAL_BWD = 6,     /* la_causal_backward */
+    LA_OP_GATED_CAUSAL = 8,     /* la_gated_causal (7 is not used) */
+    LA_OP_GATED_CAUSAL_BWD = 9  /* la_gated_causal_backward */
 } la_op;
 
 /* Problem description. d is both d_k and d_v. */
@@ -101,8 +103,9 @@ typedef struct {
 /* Bytes of workspace `op` needs for `desc` (chunk is used by LA_OP_CAUSAL and
  * LA_OP_PREFIX only; it must be 64 or 128 for those and is ignored
  * otherwise). Returns 0 when the request is invalid or unsupported, and for
- * ops that need none (LA_OP_DECODE). A valid request that needs a workspace
- * always gets a non-zero size. Host function; launches nothing. The work is
+ * requests that need none (LA_OP_DECODE; LA_OP_GATED_CAUSAL when every head is
+ * one block, that is for short rows or many heads). A valid request that
+ * needs a workspace always gets a non-zero size. Host function; launches nothing. The work is
  * split to fill the SMs of the current device, so the size is for that
  * device (with no CUDA device, for a 148-SM B200): a workspace sized on one
  * device can be too small for another, which the call then rejects with
@@ -197,6 +200,100 @@ LA_API la_status la_prefix_mask(const la_desc* desc, int32_t chunk, const void* 
 LA_API la_status la_decode_step(const la_desc* desc, const void* q, const void* k,
                          const void* v, float* S, float* z, void* out,
                          void* stream);
+
+/* ---- gated linear attention ------------------------------------------------
+ * The causal form with a decay: each token scales what the head has kept
+ * before it adds its own key and value,
+ *   S_t = a_t S_{t-1} + phi(k_t) (x) v_t,   z_t = a_t z_{t-1} + phi(k_t),
+ *   out_t = phi(q_t) S_t / (phi(q_t) . z_t)   (or the numerator alone),
+ * with one gate a_t = exp(g_t) per head and token. g: [B,H,N] log-gates in the
+ * element type. g = 0 keeps everything (la_causal_chunked); g = -inf, or any g
+ * below -9700, closes the gate: nothing before the token reaches it or a later
+ * one, so rows of several documents carry g = -inf at each document's first
+ * token. A positive g amplifies, within what fp32 can hold; a NaN gate makes
+ * NaN of its head from there on. */
+
+/* Every output of a row, and optionally the state around it.
+ * q, k, v: [B,H,N,d] inputs, g: [B,H,N] input; out: [B,H,N,d] output.
+ * S_in, z_in: float32 state in front of the first token ([B,H,d,d], [B,H,d]),
+ * both or neither (NULL: an empty one): a prompt can be given in pieces.
+ * S_out, z_out: float32 state after the last token, both or neither (NULL: not
+ * wanted), ready for la_gated_decode_step. They may be S_in, z_in.
+ * ws: op LA_OP_GATED_CAUSAL; may be NULL when la_workspace_size is 0. */
+LA_API la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, const void* v,
+                                 const void* g, const float* S_in, const float* z_in, void* out,
+                                 float* S_out, float* z_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of la_gated_causal from an empty state: dq, dk, dv ([B,H,N,d]) and
+ * dg ([B,H,N]), element type, overwritten, for dout = dL/dout. With S_i, z_i
+ * the state that query i reads, gn and gden as for la_causal_backward and
+ *   G_j = phi(q_j) gn_j^T + a_{j+1} G_{j+1},  h_j = phi(q_j) gden_j + a_{j+1} h_{j+1}:
+ *   dq_i = phi'(q_i) * (S_i gn_i + z_i gden_i)
+ *   dk_j = phi'(k_j) * (G_j v_j + h_j),  dv_j = G_j^T phi(k_j)
+ *   dg_t = a_t (<S_{t-1}, G_t> + z_{t-1} . h_t)     (exactly 0 for a closed gate)
+ * Sums are fp32; bf16 rounds the operands of its products once. ws: op
+ * LA_OP_GATED_CAUSAL_BWD (it holds a state per chunk of 64, or in fp32 with
+ * d >= 64 of 32, tokens: d d elements and d floats). */
+LA_API la_status la_gated_causal_backward(const la_desc* desc, const void* q, const void* k,
+                                          const void* v, const void* g, const void* dout, void* dq,
+                                          void* dk, void* dv, void* dg, void* ws, size_t ws_bytes,
+                                          void* stream);
+
+/* One token for every (b, h) on a cached state: q, k, v [B,H,1,d], g [B,H,1]
+ * (desc->N is ignored), S and z float32 as above. S_out, z_out receive the new
+ * state; they are S, z for a step in place, or other buffers to keep the old
+ * one (a draft that may be taken back). Needs no workspace. */
+LA_API la_status la_gated_decode_step(const la_desc* desc, const void* q, const void* k,
+                                      const void* v, const void* g, const float* S, const float* z,
+                                      float* S_out, float* z_out, void* out, void* stream);
+
+/* ---- queries and keys out of a projection -------------------------------------
+ * Norm of each query and key row and the rotation by its position, in one pass,
+ * into the [B,H,N,d] layout that the attention entry points take:
+ *   u = x (mean(x^2) + eps)^(-1/2) w,   y = R(position) u.
+ * R turns the first `rot` channels: the pairs (i, i + rot/2), or with
+ * interleaved = 1 the pairs (2i, 2i + 1), i < rot/2, by the angle whose cosine
+ * and sine are cos[position][i] and sin[position][i]:
+ *   y_1 = u_1 cos - u_2 sin,  y_2 = u_2 cos + u_1 sin.
+ * The other channels are not turned. Norm and rotation run in fp32. */
+typedef struct {
+    int32_t B, N, Hq, Hk, d;  /* d in {16, 32, 64, 128}; Hq and Hk may differ */
+    int32_t rot;              /* rotated channels: 0 (norm only) or a multiple of 16, at most d */
+    int32_t dtype;            /* la_dtype of q, k and the outputs */
+    int32_t interleaved;      /* 0: halves, 1: neighbours */
+    int32_t table_rows;       /* rows of cos and sin */
+    float eps;                /* >= 0 */
+} la_rope_desc;
+
+/* Element strides of a [B,N,H,d] view whose rows of d are contiguous: multiples
+ * of 16 bytes, not negative (0 repeats an input; the strides of a dimension of
+ * size 1 are not used). */
+typedef struct { int64_t b, n, h; } la_strides;
+
+/* q [B,N,Hq,d], k [B,N,Hk,d] by strides; q_out [B,Hq,N,d], k_out [B,Hk,N,d]
+ * contiguous. wq, wk: float32 [d], or both NULL (ones). cos, sin: float32
+ * [table_rows, rot/2], both NULL when rot = 0. positions: int32 [B,N], or NULL:
+ * token n of every sequence stands at position n (then table_rows >= N). A
+ * position outside the tables makes NaN of the token's rows. */
+LA_API la_status la_qk_norm_rope(const la_rope_desc* desc, const void* q, const la_strides* q_strides,
+                                 const void* k, const la_strides* k_strides, const float* wq,
+                                 const float* wk, const float* cos, const float* sin,
+                                 const int32_t* positions, void* q_out, void* k_out, void* stream);
+
+/* Gradients: dq, dk by strides (they may lie in one packed buffer; different
+ * rows must not overlap) for dq_out, dk_out = dL/dq_out, dL/dk_out (contiguous),
+ * and dwq, dwk float32 [d] (both NULL: not wanted), all overwritten.
+ * ws: la_qk_norm_rope_workspace_size bytes. */
+LA_API la_status la_qk_norm_rope_backward(const la_rope_desc* desc, const void* q,
+                                          const la_strides* q_strides, const void* k,
+                                          const la_strides* k_strides, const float* wq, const float* wk,
+                                          const float* cos, const float* sin, const int32_t* positions,
+                                          const void* dq_out, const void* dk_out, void* dq,
+                                          const la_strides* dq_strides, void* dk,
+                                          const la_strides* dk_strides, float* dwq, float* dwk, void* ws,
+                                          size_t ws_bytes, void* stream);
+/* 0 for an invalid or unsupported request. */
+LA_API size_t la_qk_norm_rope_workspace_size(const la_rope_desc* desc);
 
 /* la_kv_summary without a caller workspace, for callers that cannot allocate
  * device memory: code that runs where cudaMalloc is off limits (inside a

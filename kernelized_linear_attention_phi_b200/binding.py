@@ -28,7 +28,7 @@ STATUS_NAMES = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED",
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 PHIS = {"relu1": 0, "identity": 1, "elu1": 2}
 OPS = {"kv_summary": 0, "noncausal": 1, "causal": 2, "prefix": 3, "decode": 4, "noncausal_bwd": 5,
-       "causal_bwd": 6}
+       "causal_bwd": 6, "gated_causal": 8, "gated_causal_bwd": 9}
 
 
 class LaError(RuntimeError):
@@ -43,9 +43,20 @@ class la_desc(ctypes.Structure):
                 ("normalize", ctypes.c_int32)]
 
 
+class la_rope_desc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("table_rows", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class la_strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("n", ctypes.c_int64), ("h", ctypes.c_int64)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
+_ROPE = [ctypes.POINTER(la_rope_desc), _P, ctypes.POINTER(la_strides), _P, ctypes.POINTER(la_strides), _P, _P, _P, _P, _P]
 _SIGS = {
     "la_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(la_desc), ctypes.c_int32, ctypes.c_int32]),
     "la_kv_summary": (ctypes.c_int, [ctypes.POINTER(la_desc), _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
@@ -62,6 +73,13 @@ _SIGS = {
     "la_prefix_mask": (ctypes.c_int, [ctypes.POINTER(la_desc), ctypes.c_int32, _P, _P, _P, _P, _P,
                                       _P, ctypes.c_size_t, _P]),
     "la_decode_step": (ctypes.c_int, [ctypes.POINTER(la_desc), _P, _P, _P, _P, _P, _P, _P]),
+    "la_gated_causal": (ctypes.c_int, [ctypes.POINTER(la_desc)] + [_P] * 10 + [ctypes.c_size_t, _P]),
+    "la_gated_causal_backward": (ctypes.c_int, [ctypes.POINTER(la_desc)] + [_P] * 10 + [ctypes.c_size_t, _P]),
+    "la_gated_decode_step": (ctypes.c_int, [ctypes.POINTER(la_desc)] + [_P] * 10),
+    "la_qk_norm_rope": (ctypes.c_int, _ROPE + [_P, _P, _P]),
+    "la_qk_norm_rope_backward": (ctypes.c_int, _ROPE + [_P, _P, _P, ctypes.POINTER(la_strides), _P,
+                                                        ctypes.POINTER(la_strides), _P, _P, _P, ctypes.c_size_t, _P]),
+    "la_qk_norm_rope_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(la_rope_desc)]),
     "la_kv_summary_static": (ctypes.c_int, [ctypes.POINTER(la_desc), _P, _P, _P, _P, _P]),
     "la_last_error": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "la_timing_enable": (ctypes.c_int, [ctypes.c_int32]),
@@ -164,9 +182,11 @@ def la_workspace_size(desc: la_desc, op, chunk: int = 64) -> int:
 def workspace(desc: la_desc, op, chunk: int = 64, device="cuda") -> torch.Tensor:
     """A device buffer big enough for ``op`` on ``desc``, with its error word
     zeroed (the library only sets bits in it; la_last_error reads and
-    clears)."""
+    clears). The rest needs no initialization."""
     n = la_workspace_size(desc, op, chunk)
-    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
 
 
 def la_kv_summary(k, v, S_out=None, z_out=None, phi="relu1", ws=None, stream=None):
@@ -331,3 +351,205 @@ def la_causal_backward(q, k, v, dout, dq=None, dk=None, dv=None, phi="relu1", no
                        stream=None):
     """Gradients (dq, dk, dv) of causal attention for upstream dout."""
     return _backward("la_causal_backward", "causal_bwd", q, k, v, dout, dq, dk, dv, phi, normalize, ws, stream)
+
+
+class _on:
+    """The device of ``ref`` and ``stream`` (torch's current one there when
+    None) made current: what a call allocates and clears is then ordered with
+    its kernels, whatever device and stream the caller was on."""
+
+    def __init__(self, ref, stream):
+        if not ref.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        self.device = torch.cuda.device(ref.device) if ref.device.index != torch.cuda.current_device() else None
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=ref.device)
+        self.stream = torch.cuda.stream(stream) if stream is not None else None
+        self.ref = ref
+
+    def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self.ref.device).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
+
+
+def _gates(g, ref):
+    B, H, N, _ = ref.shape
+    if g.dtype != ref.dtype or tuple(g.shape) != (B, H, N) or g.device != ref.device:
+        raise ValueError(f"g must be {ref.dtype} [{B}, {H}, {N}] on {ref.device}")
+
+
+def la_gated_causal(q, k, v, g, S_in=None, z_in=None, out=None, S_out=None, z_out=None, phi="relu1", normalize=True,
+                    ws=None, stream=None):
+    """Causal attention with a decay exp(g) per head and token (g: [B, H, N]
+    log-gates, -inf starts anew). S_in, z_in: the state in front of the first
+    token; S_out, z_out (may be the same) receive the one after the last.
+    Returns out."""
+    desc = _desc_of(q, phi, normalize)
+    _gates(g, q)
+    for a, b in ((S_in, z_in), (S_out, z_out)):
+        if (a is None) != (b is None):
+            raise ValueError("give both S and z of a state, or neither")
+        if a is not None:
+            _state(a, b, q)
+    with _on(q, stream) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        _same(q, k, v, out)
+        if ws is None:
+            ws = workspace(desc, "gated_causal", device=q.device) if la_workspace_size(desc, "gated_causal") else None
+        else:
+            _ws(ws, q)
+        _check("la_gated_causal", lib().la_gated_causal(
+            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S_in), _ptr(z_in), _ptr(out), _ptr(S_out),
+            _ptr(z_out), _ptr(ws), 0 if ws is None else ws.numel(), st))
+    return out
+
+
+def la_gated_causal_backward(q, k, v, g, dout, dq=None, dk=None, dv=None, dg=None, phi="relu1", normalize=True, ws=None,
+                             stream=None):
+    """Gradients (dq, dk, dv, dg) of la_gated_causal, from an empty state, for
+    upstream dout."""
+    desc = _desc_of(q, phi, normalize)
+    _gates(g, q)
+    with _on(q, stream) as st:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        dg = torch.empty_like(g) if dg is None else dg
+        _same(q, k, v, dout, dq, dk, dv)
+        _gates(dg, q)
+        ws = workspace(desc, "gated_causal_bwd", device=q.device) if ws is None else _ws(ws, q)
+        _check("la_gated_causal_backward", lib().la_gated_causal_backward(
+            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+            _ptr(ws), ws.numel(), st))
+    return dq, dk, dv, dg
+
+
+def la_gated_decode_step(q, k, v, g, S, z, S_out=None, z_out=None, out=None, phi="relu1", normalize=True, stream=None):
+    """One token on the state (S, z): q, k, v [B, H, 1, d], g [B, H, 1]. The new
+    state goes to S_out, z_out, or in place when they are not given. Returns out."""
+    desc = _desc_of(q, phi, normalize)
+    if q.shape[2] != 1:
+        raise ValueError("a step takes one token: [B, H, 1, d]")
+    _gates(g, q)
+    if (S_out is None) != (z_out is None):
+        raise ValueError("give both S and z of a state, or neither")
+    _state(S, z, q)
+    if S_out is None:
+        S_out, z_out = S, z
+    else:
+        _state(S_out, z_out, q)
+    with _on(q, stream) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        _same(q, k, v, out)
+        _check("la_gated_decode_step", lib().la_gated_decode_step(
+            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(z), _ptr(S_out), _ptr(z_out), _ptr(out),
+            st))
+    return out
+
+
+def _rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    """The descriptor and the pointers of the inputs both directions share."""
+    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+        raise ValueError(f"expected q [B, N, Hq, d] and k [B, N, Hk, d], got {tuple(q.shape)} and {tuple(k.shape)}")
+    if q.dtype not in DTYPES or k.dtype != q.dtype or k.device != q.device:
+        raise ValueError("q and k must share a device and a dtype (float32 or bfloat16)")
+    B, N, Hq, d = q.shape
+    if (cos is None) != (sin is None) or (q_weight is None) != (k_weight is None):
+        raise ValueError("give both cos and sin, and both weights, or neither")
+    rot = rows = 0
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [rows, rot / 2] tables")
+        rows, rot = cos.shape[0], 2 * cos.shape[1]
+        if rows >= 1 << 31 or rot > d:
+            raise ValueError(f"the tables turn {rot} of {d} channels and have {rows} rows")
+    for t in (q_weight, k_weight):
+        if t is not None and tuple(t.shape) != (d,):
+            raise ValueError(f"weights must be [{d}]")
+    for t in (q_weight, k_weight, cos, sin):
+        if t is not None and (t.dtype != torch.float32 or t.device != q.device):
+            raise ValueError(f"weights and tables must be float32 on {q.device}")
+    if positions is not None and (positions.dtype != torch.int32 or tuple(positions.shape) != (B, N) or
+                                  positions.device != q.device):
+        raise ValueError(f"positions must be int32 [{B}, {N}] on {q.device}")
+    desc = la_rope_desc(B, N, Hq, k.shape[2], d, rot, DTYPES[q.dtype], int(bool(interleaved)), rows, float(eps))
+    return desc, [_ptr(t) for t in (q_weight, k_weight, cos, sin, positions)]
+
+
+def _rows(t):
+    """Pointer and strides of a [B, N, H, d] view with contiguous rows."""
+    if t.stride(3) != 1:
+        raise ValueError("the rows of q and k must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), ctypes.byref(la_strides(*t.stride()[:3]))
+
+
+def la_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, interleaved=False, q_out=None,
+                    k_out=None, stream=None):
+    """Norm of each query and key row (float32 weights [d] or None) and the
+    rotation of its first 2 * cos.shape[1] channels by its position's row of
+    the tables (float32 [rows, rot / 2]; None: norm only). q [B, N, Hq, d] and
+    k [B, N, Hk, d] may be views into one projection; positions int32 [B, N],
+    or None for 0 .. N - 1. Returns contiguous (q_out [B, Hq, N, d], k_out
+    [B, Hk, N, d])."""
+    desc, small = _rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    B, N, Hq, d = q.shape
+    with _on(q, stream) as st:
+        q_out = torch.empty(B, Hq, N, d, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        k_out = torch.empty(B, desc.Hk, N, d, dtype=q.dtype, device=q.device) if k_out is None else k_out
+        _outputs(q, (q_out, Hq), (k_out, desc.Hk))
+        _check("la_qk_norm_rope", lib().la_qk_norm_rope(
+            ctypes.byref(desc), *_rows(q), *_rows(k), *small, _ptr(q_out), _ptr(k_out), st))
+    return q_out, k_out
+
+
+def _outputs(q, *pairs):
+    B, N, _, d = q.shape
+    for t, H in pairs:
+        if t.dtype != q.dtype or tuple(t.shape) != (B, H, N, d) or t.device != q.device:
+            raise ValueError(f"expected {q.dtype} [{B}, {H}, {N}, {d}] on {q.device}, got {t.dtype} {tuple(t.shape)}")
+
+
+def la_qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, dq_out, dk_out, positions=None, eps=1e-6,
+                             interleaved=False, dq=None, dk=None, dq_weight=None, dk_weight=None, ws=None, stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of la_qk_norm_rope for upstream
+    dq_out [B, Hq, N, d], dk_out [B, Hk, N, d]. dq, dk may be given as views
+    like q, k (of one packed gradient, say). Without weights the last two are
+    None."""
+    desc, small = _rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    d = q.shape[3]
+    _outputs(q, (dq_out, desc.Hq), (dk_out, desc.Hk))
+    with _on(q, stream) as st:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+        for t, like in ((dq, q), (dk, k)):
+            if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
+                raise ValueError("dq and dk must have the shape, dtype and device of q and k")
+        if q_weight is None:
+            if dq_weight is not None or dk_weight is not None:
+                raise ValueError("there are no weights to differentiate")
+        else:
+            dq_weight = torch.empty_like(q_weight) if dq_weight is None else dq_weight
+            dk_weight = torch.empty_like(k_weight) if dk_weight is None else dk_weight
+            for t in (dq_weight, dk_weight):
+                if t.dtype != torch.float32 or tuple(t.shape) != (d,) or t.device != q.device:
+                    raise ValueError(f"weight gradients must be float32 [{d}] on {q.device}")
+        n = int(lib().la_qk_norm_rope_workspace_size(ctypes.byref(desc)))
+        if ws is None:
+            ws = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+        else:
+            _ws(ws, q)
+        _check("la_qk_norm_rope_backward", lib().la_qk_norm_rope_backward(
+            ctypes.byref(desc), *_rows(q), *_rows(k), *small, _ptr(dq_out), _ptr(dk_out), *_rows(dq), *_rows(dk),
+            _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), ws.numel(), st))
+    return dq, dk, dq_weight, dk_weight

@@ -1,0 +1,701 @@
+// Gradients of gated linear attention. With S_i, z_i the state query i reads,
+// up_i = 1 / den_i, delta_i = out_i . dout_i, col_i = -delta_i (unnormalized:
+// up = 1, col = 0) and G_j, h_j = sum_{i >= j} e^{b_i - b_j} up_i phi(q_i) [dout_i, col_i]:
+//   dq_i = phi'(q_i) * up_i (S_i dout_i + col_i z_i)
+//   dk_j = phi'(k_j) * (G_j v_j + h_j),   dv_j = G_j^T phi(k_j)
+//   dg_t = a_t (<S_{t-1}, G_t> + <z_{t-1}, h_t>)
+// dg over a chunk, from the state S in front of it and G behind it, with
+// W_ij = e^{b_i - b_j} (phi(q_i).phi(k_j)) up_i (dout_i.v_j + col_i):
+//   dg_t = sum_{i >= t} (sum_j W_ij) - sum_{j >= t} (sum_i W_ij)     pairs inside the chunk
+//        + sum_{i >= t} e^{b_i} up_i phi(q_i) (S dout_i + col_i z)   queries with earlier keys
+//        + sum_{j < t} e^{b_last - b_j} phi(k_j) (G v_j + h)         keys with later queries
+//        + e^{b_last} (<S, G> + <z, h>)                              keys and queries outside
+// No term sums over more than a chunk, so dg keeps its accuracy at any length
+// (the difference of the running sums of q dq and k dk would lose it), and
+// W is formed in fp32 from unrounded products.
+//
+// Two sweeps: chunks in order for dq (S in registers; the state in front of
+// each chunk is written out for the last term), then chunks in reverse for
+// dk, dv, dg (G in registers).
+#pragma once
+
+#include "gated.h"
+#include "gated_common.cuh"
+#include "launch_util.h"
+
+namespace la {
+namespace gated {
+
+// PARTS: operands of the state (2: rounded and remainder); COPIES of them.
+template <typename T, int D, int PARTS, int COPIES> struct BwdSmem {
+    using SH = Shape<T, D>;
+    T tiles[2][4][SH::TILE];  // q, k, v, dout of two chunks
+    T sop[COPIES][PARTS][SH::SOP];
+    float zs[COPIES][D];
+    Gates<SH::C> gates[2];
+    float row[2][SH::CG][SH::C];     // per token sums for dg
+    float cols[2][SH::RG][SH::C];    // column sums of W per row group
+    float part[SH::CG][SH::C];
+    float dot[2][SH::NW];
+};
+
+// The first sweep subtracts delta_i z from S dout_i; with features that are
+// positive (relu + 1, elu + 1) both are dominated by the part that all
+// channels share, and what is left would carry the rounding of the whole: S
+// goes in as two bf16 parts there (relative error of dq at 2 x 8 x 4096 x 64,
+// relu + 1: 6.1e-3 with one part).
+template <typename T, int D, int PHI> struct BwdQ {
+    static constexpr int PARTS = sizeof(T) == 2 && shifted<PHI> ? 2 : 1;
+    static constexpr int COPIES = D == 128 && PARTS == 2 ? 1 : Shape<T, D>::SB;
+    using Smem = BwdSmem<T, D, PARTS, COPIES>;
+};
+template <typename T, int D> using BwdKvSmem = BwdSmem<T, D, 1, Shape<T, D>::SB>;
+
+// State records between the sweeps: per chunk, the fragments of S in the
+// element type in thread order (both sweeps hold S and G in the same lanes),
+// then z in fp32.
+template <typename T, int D> struct ChunkState {
+    using SH = Shape<T, D>;
+    static constexpr int OWN = SH::SRT * SH::SCG * 32;             // threads that hold S
+    static constexpr int VEC = SH::SN * 4 / 8 * sizeof(T) / 16;    // 16-byte vectors per thread
+    static constexpr size_t BYTES = (size_t)D * D * sizeof(T) + D * sizeof(float);
+    static_assert((size_t)OWN * VEC * 16 == (size_t)D * D * sizeof(T), "record");
+
+    __device__ __forceinline__ static void write(uint8_t* rec, const State<T, D>& st, const float* zs) {
+        if ((int)threadIdx.x < OWN) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                uint4 u;
+                if constexpr (SH::F32) {
+                    u = make_uint4(__float_as_uint(st.S[v][0]), __float_as_uint(st.S[v][1]), __float_as_uint(st.S[v][2]),
+                                   __float_as_uint(st.S[v][3]));
+                } else {
+                    u = make_uint4(pack_bf16(st.S[2 * v][0], st.S[2 * v][1]), pack_bf16(st.S[2 * v][2], st.S[2 * v][3]),
+                                   pack_bf16(st.S[2 * v + 1][0], st.S[2 * v + 1][1]),
+                                   pack_bf16(st.S[2 * v + 1][2], st.S[2 * v + 1][3]));
+                }
+                reinterpret_cast<uint4*>(rec)[v * OWN + threadIdx.x] = u;
+            }
+        }
+        float* z = reinterpret_cast<float*>(rec + (size_t)D * D * sizeof(T));
+        for (int a = threadIdx.x; a < D; a += SH::THREADS) z[a] = zs[a];
+    }
+    // this thread's part of <S, G> + <z, h>
+    __device__ __forceinline__ static float product(const uint8_t* rec, const State<T, D>& st, const float* zs) {
+        float sum = 0.f;
+        if ((int)threadIdx.x < OWN) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const uint4 u = ldg_stream(reinterpret_cast<const uint4*>(rec) + v * OWN + threadIdx.x);
+                if constexpr (SH::F32) {
+                    sum += __uint_as_float(u.x) * st.S[v][0] + __uint_as_float(u.y) * st.S[v][1] +
+                           __uint_as_float(u.z) * st.S[v][2] + __uint_as_float(u.w) * st.S[v][3];
+                } else {
+                    sum += bf16_lo(u.x) * st.S[2 * v][0] + bf16_hi(u.x) * st.S[2 * v][1] + bf16_lo(u.y) * st.S[2 * v][2] +
+                           bf16_hi(u.y) * st.S[2 * v][3];
+                    sum += bf16_lo(u.z) * st.S[2 * v + 1][0] + bf16_hi(u.z) * st.S[2 * v + 1][1] +
+                           bf16_lo(u.w) * st.S[2 * v + 1][2] + bf16_hi(u.w) * st.S[2 * v + 1][3];
+                }
+            }
+        }
+        const float* z = reinterpret_cast<const float*>(rec + (size_t)D * D * sizeof(T));
+        for (int a = threadIdx.x; a < D; a += SH::THREADS) sum += z[a] * zs[a];
+        return sum;
+    }
+};
+
+template <typename T> __device__ __forceinline__ void load_pair(const T* p, float& a, float& b);
+template <> __device__ __forceinline__ void load_pair<float>(const float* p, float& a, float& b) {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    a = x.x;
+    b = x.y;
+}
+template <> __device__ __forceinline__ void load_pair<__nv_bfloat16>(const __nv_bfloat16* p, float& a, float& b) {
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+    a = bf16_lo(x);
+    b = bf16_hi(x);
+}
+__device__ __forceinline__ void store_pair(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16(a, b);
+}
+
+template <typename T, int D, int PHI>
+__global__ void __launch_bounds__(Shape<T, D>::THREADS)
+gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
+                   const T* __restrict__ dout, const float* prefix, int N, int block_tokens, int nblk, int normalize,
+                   T* __restrict__ dq, float* __restrict__ up, float* __restrict__ col, float* __restrict__ dgp,
+                   uint8_t* __restrict__ chunk_state) {
+    using SH = Shape<T, D>;
+    using BQ = BwdQ<T, D, PHI>;
+    constexpr int C = SH::C, LD = SH::LD, NT = SH::NCOL / 8;
+    constexpr bool LO = BQ::PARTS == 2;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    auto& sm = *reinterpret_cast<typename BQ::Smem*>(smem_raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
+    const int blk = blockIdx.x, bh = blockIdx.y;
+    const int first = blk * block_tokens, end = min(N, first + block_tokens);
+    const int nch = (end - first + C - 1) / C;
+    const size_t off = (size_t)bh * N * D, toff = (size_t)bh * N;
+    q += off; k += off; v += off; dout += off; dq += off;
+    gate += toff;
+    dgp += toff;
+    uint8_t* states = chunk_state + ((size_t)bh * ((N + C - 1) / C) + first / C) * ChunkState<T, D>::BYTES;
+    pdl_wait();
+
+    auto fetch = [&](int c) {
+        const int row0 = first + c * C;
+        load_tile<SH, T, D>(sm.tiles[c & 1][0], q, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c & 1][1], k, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c & 1][2], v, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c & 1][3], dout, row0, N);
+        cp_async_commit();
+    };
+    fetch(0);
+    State<T, D> st;
+    const float* rec = prefix ? prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
+    st.seed(rec, rec + D * D, warp, lane);
+    st.template publish<LO>(sm.sop[0][0], sm.zs[0], warp, lane, sm.sop[0][BQ::PARTS - 1]);
+    GateRegs<C> gr;
+    if (warp == 0) {
+        load_gates<T, C>(gr, gate, nullptr, nullptr, first, N, lane);
+        scan_gates<C>(sm.gates[0], gr, end - first, lane);
+    }
+    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
+    const int i0 = rg * 16, col0 = cg * SH::NCOL;
+
+    // dgp of chunk c from the sums its warps left: a suffix sum over the chunk
+    auto finish = [&](int c) {
+        if (warp != SH::NW - 1) return;
+        constexpr int R = C / 32;
+        float x[R], run = 0.f;
+#pragma unroll
+        for (int e = R - 1; e >= 0; --e) {
+            const int i = lane * R + e;
+            float s = sm.row[c & 1][0][i];
+#pragma unroll
+            for (int r = 0; r < SH::RG; ++r)
+                if (r >= i / 16) s -= sm.cols[c & 1][r][i];
+            x[e] = s + run;
+            run = x[e];
+        }
+        float after = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_down_sync(0xffffffffu, after, o);
+            if (lane + o < 32) after += y;
+        }
+        after -= run;  // the lanes behind this one
+#pragma unroll
+        for (int e = 0; e < R; ++e) {
+            const int i = first + c * C + lane * R + e;
+            if (i < end) dgp[i] = x[e] + after;
+        }
+    };
+
+    for (int c = 0; c < nch; ++c) {
+        cp_async_wait<0>();
+        __syncthreads();
+        if (c + 1 < nch) {
+            fetch(c + 1);
+            if (warp == 0) load_gates<T, C>(gr, gate, nullptr, nullptr, first + (c + 1) * C, N, lane);
+        }
+        if (c > 0) finish(c - 1);
+        const T *qt = sm.tiles[c & 1][0], *kt = sm.tiles[c & 1][1], *vt = sm.tiles[c & 1][2], *gt = sm.tiles[c & 1][3];
+        const Gates<C>& gs = sm.gates[c & 1];
+        const int sb = BQ::COPIES == 2 ? (c & 1) : 0;
+        const T* sop = sm.sop[sb][0];
+        const float* zs = sm.zs[sb];
+        ChunkState<T, D>::write(states + (size_t)c * ChunkState<T, D>::BYTES, st, zs);
+
+        // dout S^T, and q . z
+        float acc[NT][4] = {}, oz[4] = {};
+#pragma unroll
+        for (int k0 = 0; k0 < D; k0 += 16) {
+            FragA<T> a;
+            load_a<LD>(a, gt, i0, k0, lane);
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                FragB<T> b[2];
+                load_bt<LD>(b, sop, col0 + 16 * n, k0, lane);
+                mma_step(acc[2 * n], a, b[0]);
+                mma_step(acc[2 * n + 1], a, b[1]);
+                if constexpr (LO) {
+                    load_bt<LD>(b, sm.sop[sb][1], col0 + 16 * n, k0, lane);
+                    mma_step(acc[2 * n], a, b[0]);
+                    mma_step(acc[2 * n + 1], a, b[1]);
+                }
+            }
+            if (normalize) {
+                FragB<T> b;
+                load_a<LD>(a, qt, i0, k0, lane);
+                phi_frag<PHI>(a);
+                load_column(b, zs, k0, lane);
+                mma_step(oz, a, b);
+            }
+        }
+        // q . (S dout), over this warp's columns, then over the column groups
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x, y;
+            const T* p = qt + (i0 + g) * LD + col0 + 8 * n + 2 * t;
+            load_pair(p, x, y);
+            s0 += phi_f<PHI>(x) * acc[n][0] + phi_f<PHI>(y) * acc[n][1];
+            load_pair(p + 8 * LD, x, y);
+            s1 += phi_f<PHI>(x) * acc[n][2] + phi_f<PHI>(y) * acc[n][3];
+        }
+        s0 = quad_sum(s0);
+        s1 = quad_sum(s1);
+        if constexpr (SH::CG > 1) {
+            if (t == 0) {
+                sm.part[cg][i0 + g] = s0;
+                sm.part[cg][i0 + g + 8] = s1;
+            }
+            __syncthreads();
+            s0 = s1 = 0.f;
+#pragma unroll
+            for (int x = 0; x < SH::CG; ++x) {
+                s0 += sm.part[x][i0 + g];
+                s1 += sm.part[x][i0 + g + 8];
+            }
+        }
+        const float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
+        const float hi0 = gs.hi[i0 + g], lo0 = gs.lo[i0 + g], hi1 = gs.hi[i0 + g + 8], lo1 = gs.lo[i0 + g + 8];
+        const float qz0 = f0 * quad_sum(t == 0 ? oz[0] + oz[1] : 0.f), qz1 = f1 * quad_sum(t == 0 ? oz[2] + oz[3] : 0.f);
+        s0 *= f0;
+        s1 *= f1;
+
+        // P = phi(q) phi(k)^T and dP = dout v^T of the keys up to this row group
+        float p[SH::RG][2][4], dp[SH::RG][2][4];
+        float den0 = 0.f, den1 = 0.f, num0 = 0.f, num1 = 0.f;
+#pragma unroll
+        for (int jt = 0; jt < SH::RG; ++jt) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[jt][n][e] = dp[jt][n][e] = 0.f;
+            if (jt > rg) continue;
+#pragma unroll
+            for (int k0 = 0; k0 < D; k0 += 16) {
+                FragA<T> a;
+                FragB<T> b[2];
+                load_a<LD>(a, qt, i0, k0, lane);
+                phi_frag<PHI>(a);
+                load_bt<LD>(b, kt, jt * 16, k0, lane);
+                phi_frag<PHI>(b[0]);
+                phi_frag<PHI>(b[1]);
+                mma_step(p[jt][0], a, b[0]);
+                mma_step(p[jt][1], a, b[1]);
+                load_a<LD>(a, gt, i0, k0, lane);
+                load_bt<LD>(b, vt, jt * 16, k0, lane);
+                mma_step(dp[jt][0], a, b[0]);
+                mma_step(dp[jt][1], a, b[1]);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int jl = n * 8 + 2 * t + e, j = jt * 16 + jl;
+                    const float w0 = jt < rg || jl <= g ? p[jt][n][e] * decay(gs, hi0, lo0, j) : 0.f;
+                    const float w1 = jt < rg || jl <= g + 8 ? p[jt][n][2 + e] * decay(gs, hi1, lo1, j) : 0.f;
+                    den0 += w0;
+                    den1 += w1;
+                    num0 += w0 * dp[jt][n][e];
+                    num1 += w1 * dp[jt][n][2 + e];
+                }
+        }
+        den0 = quad_sum(den0);
+        den1 = quad_sum(den1);
+        num0 = quad_sum(num0);
+        num1 = quad_sum(num1);
+        float up0 = 1.f, up1 = 1.f, de0 = 0.f, de1 = 0.f;
+        if (normalize) {
+            up0 = 1.f / (den0 + qz0);
+            up1 = 1.f / (den1 + qz1);
+            de0 = (num0 + s0) * up0;  // out . dout
+            de1 = (num1 + s1) * up1;
+        }
+        const int row = first + c * C + i0 + g;
+        if (cg == 0 && t == 0) {
+            // the row sum of W and the queries' part with earlier keys
+            sm.row[c & 1][0][i0 + g] = row < end ? up0 * ((num0 - de0 * den0) + (s0 - de0 * qz0)) : 0.f;
+            sm.row[c & 1][0][i0 + g + 8] = row + 8 < end ? up1 * ((num1 - de1 * den1) + (s1 - de1 * qz1)) : 0.f;
+            if (normalize) {
+                if (row < end) {
+                    up[toff + row] = up0;
+                    col[toff + row] = -de0;
+                }
+                if (row + 8 < end) {
+                    up[toff + row + 8] = up1;
+                    col[toff + row + 8] = -de1;
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float2 z = *reinterpret_cast<const float2*>(zs + col0 + 8 * n + 2 * t);
+            acc[n][0] = f0 * up0 * (acc[n][0] - de0 * z.x);
+            acc[n][1] = f0 * up0 * (acc[n][1] - de0 * z.y);
+            acc[n][2] = f1 * up1 * (acc[n][2] - de1 * z.x);
+            acc[n][3] = f1 * up1 * (acc[n][3] - de1 * z.y);
+        }
+        float rs0 = 0.f, rs1 = 0.f;  // row sums of ds, for the shift of phi(k)
+#pragma unroll
+        for (int jt = 0; jt < SH::RG; ++jt) {
+            if (jt > rg) continue;
+            float ds[2][4], cs[2][2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int jl = n * 8 + 2 * t + e, j = jt * 16 + jl;
+                    ds[n][e] = jt < rg || jl <= g ? up0 * (dp[jt][n][e] - de0) * decay(gs, hi0, lo0, j) : 0.f;
+                    ds[n][2 + e] = jt < rg || jl <= g + 8 ? up1 * (dp[jt][n][2 + e] - de1) * decay(gs, hi1, lo1, j) : 0.f;
+                    // rows past the last token hold no query
+                    cs[n][e] = (row < end ? p[jt][n][e] * ds[n][e] : 0.f) +
+                               (row + 8 < end ? p[jt][n][2 + e] * ds[n][2 + e] : 0.f);
+                }
+            if (cg == 0) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = cs[n][e];
+                        x += __shfl_xor_sync(0xffffffffu, x, 4);
+                        x += __shfl_xor_sync(0xffffffffu, x, 8);
+                        x += __shfl_xor_sync(0xffffffffu, x, 16);
+                        if (g == 0) sm.cols[c & 1][rg][jt * 16 + n * 8 + 2 * t + e] = x;
+                    }
+            }
+            rs0 += (ds[0][0] + ds[0][1]) + (ds[1][0] + ds[1][1]);
+            rs1 += (ds[0][2] + ds[0][3]) + (ds[1][2] + ds[1][3]);
+            FragA<T> a;
+            make_a(a, ds[0], ds[1]);  // bf16: rounded once, like every operand of the gradients' products
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                FragB<T> b[2];
+                load_b<LD>(b, kt, jt * 16, col0 + 16 * n, lane);
+                base_frag<PHI>(b[0]);
+                base_frag<PHI>(b[1]);
+                mma_step(acc[2 * n], a, b[0]);
+                mma_step(acc[2 * n + 1], a, b[1]);
+            }
+        }
+        rs0 = shifted<PHI> ? quad_sum(rs0) : 0.f;
+        rs1 = shifted<PHI> ? quad_sum(rs1) : 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x, y;
+            const T* qp = qt + (i0 + g) * LD + col0 + 8 * n + 2 * t;
+            T* o = dq + (size_t)row * D + col0 + 8 * n + 2 * t;
+            if (row < end) {
+                load_pair(qp, x, y);
+                store_pair(o, (acc[n][0] + rs0) * phi_grad(x, PHI), (acc[n][1] + rs0) * phi_grad(y, PHI));
+            }
+            if (row + 8 < end) {
+                load_pair(qp + 8 * LD, x, y);
+                store_pair(o + 8 * D, (acc[n][2] + rs1) * phi_grad(x, PHI), (acc[n][3] + rs1) * phi_grad(y, PHI));
+            }
+        }
+        if (c + 1 < nch) {
+            st.template update<PHI>(kt, vt, gs.to_end, nullptr, gs.all, warp, lane);
+            if (BQ::COPIES == 1) __syncthreads();  // every warp has read the operand
+            const int nb = BQ::COPIES == 2 ? ((c + 1) & 1) : 0;
+            st.template publish<LO>(sm.sop[nb][0], sm.zs[nb], warp, lane, sm.sop[nb][BQ::PARTS - 1]);
+            if (warp == 0) scan_gates<C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
+        }
+    }
+    __syncthreads();
+    finish(nch - 1);
+}
+
+template <typename T, int D, int PHI>
+__global__ void __launch_bounds__(Shape<T, D>::THREADS)
+gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
+                    const T* __restrict__ dout, const float* suffix, int N, int block_tokens, int nblk,
+                    const float* up, const float* col, const float* __restrict__ dgp,
+                    const uint8_t* __restrict__ chunk_state, T* __restrict__ dk, T* __restrict__ dv, T* __restrict__ dg) {
+    using SH = Shape<T, D>;
+    constexpr int C = SH::C, LD = SH::LD, NT = SH::NCOL / 8;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    auto& sm = *reinterpret_cast<BwdKvSmem<T, D>*>(smem_raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
+    const int blk = blockIdx.x, bh = blockIdx.y;
+    const int first = blk * block_tokens, end = min(N, first + block_tokens);
+    const int nch = (end - first + C - 1) / C;
+    const size_t off = (size_t)bh * N * D, toff = (size_t)bh * N;
+    q += off; k += off; v += off; dout += off; dk += off; dv += off;
+    gate += toff;
+    dgp += toff;
+    dg += toff;
+    if (up) up += toff;
+    if (col) col += toff;
+    const uint8_t* states = chunk_state + ((size_t)bh * ((N + C - 1) / C) + first / C) * ChunkState<T, D>::BYTES;
+    pdl_wait();
+
+    // step s of the sweep is chunk nch - 1 - s
+    auto fetch = [&](int s) {
+        const int row0 = first + (nch - 1 - s) * C;
+        load_tile<SH, T, D>(sm.tiles[s & 1][0], q, row0, N);
+        load_tile<SH, T, D>(sm.tiles[s & 1][1], k, row0, N);
+        load_tile<SH, T, D>(sm.tiles[s & 1][2], v, row0, N);
+        load_tile<SH, T, D>(sm.tiles[s & 1][3], dout, row0, N);
+        cp_async_commit();
+    };
+    fetch(0);
+    State<T, D> st;
+    const float* rec = suffix ? suffix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
+    st.seed(rec, rec + D * D, warp, lane);
+    st.publish(sm.sop[0][0], sm.zs[0], warp, lane);
+    GateRegs<C> gr;
+    auto scan = [&](int s) {
+        Gates<C>& gs = sm.gates[s & 1];
+        scan_gates<C>(gs, gr, end - first - (nch - 1 - s) * C, lane);
+#pragma unroll
+        for (int e = 0; e < C / 32; ++e) {
+            const int i = lane * (C / 32) + e;
+            gs.from_start[i] *= gs.up[i];
+        }
+    };
+    if (warp == 0) {
+        load_gates<T, C>(gr, gate, up, col, first + (nch - 1) * C, N, lane);
+        scan(0);
+    }
+    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
+    const int j0 = rg * 16, col0 = cg * SH::NCOL;
+
+    // dg of step s: what the first sweep left, the keys in front and the outside
+    auto finish = [&](int s) {
+        if (warp != SH::NW - 1) return;
+        constexpr int R = C / 32;
+        const int row0 = first + (nch - 1 - s) * C;
+        float outside = 0.f;
+#pragma unroll
+        for (int w = 0; w < SH::NW; ++w) outside += sm.dot[s & 1][w];
+        float x[R], own = 0.f;
+#pragma unroll
+        for (int e = 0; e < R; ++e) {
+            const int i = lane * R + e;
+            x[e] = own;  // the keys of this lane in front of i
+#pragma unroll
+            for (int y = 0; y < SH::CG; ++y) own += sm.row[s & 1][y][i];
+        }
+        float run = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += y;
+        }
+        run -= own;
+#pragma unroll
+        for (int e = 0; e < R; ++e) {
+            const int i = row0 + lane * R + e;
+            if (i >= end) continue;
+            // nothing passes a closed gate: its gradient is exactly 0
+            const bool closed = to_f32<T>(gate[i]) < -104.f;  // e^g is 0 in fp32
+            dg[i] = from_f32<T>(closed ? 0.f : dgp[i] + run + x[e] + outside);
+        }
+    };
+
+    for (int s = 0; s < nch; ++s) {
+        const int c = nch - 1 - s;
+        cp_async_wait<0>();
+        __syncthreads();
+        if (s + 1 < nch) {
+            fetch(s + 1);
+            if (warp == 0) load_gates<T, C>(gr, gate, up, col, first + (c - 1) * C, N, lane);
+        }
+        if (s > 0) finish(s - 1);
+        const T *qt = sm.tiles[s & 1][0], *kt = sm.tiles[s & 1][1], *vt = sm.tiles[s & 1][2], *gt = sm.tiles[s & 1][3];
+        const Gates<C>& gs = sm.gates[s & 1];
+        const int sb = SH::SB == 2 ? (s & 1) : 0;
+        const T* sop = sm.sop[sb][0];
+        const float* zs = sm.zs[sb];
+
+        float dot = gs.all * ChunkState<T, D>::product(states + (size_t)c * ChunkState<T, D>::BYTES, st, zs);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) sm.dot[s & 1][warp] = dot;
+
+        // keys with the queries behind the chunk: phi(k) G and v G^T + h
+        float av[NT][4] = {}, ak[NT][4] = {};
+#pragma unroll
+        for (int k0 = 0; k0 < D; k0 += 16) {
+            FragA<T> a;
+            FragB<T> b[2];
+            load_a<LD>(a, kt, j0, k0, lane);
+            phi_frag<PHI>(a);
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                load_b<LD>(b, sop, k0, col0 + 16 * n, lane);
+                mma_step(av[2 * n], a, b[0]);
+                mma_step(av[2 * n + 1], a, b[1]);
+            }
+            load_a<LD>(a, vt, j0, k0, lane);
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                load_bt<LD>(b, sop, col0 + 16 * n, k0, lane);
+                mma_step(ak[2 * n], a, b[0]);
+                mma_step(ak[2 * n + 1], a, b[1]);
+            }
+        }
+        const float e0 = gs.to_end[j0 + g], e1 = gs.to_end[j0 + g + 8];
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float2 h = *reinterpret_cast<const float2*>(zs + col0 + 8 * n + 2 * t);
+            av[n][0] *= e0; av[n][1] *= e0; av[n][2] *= e1; av[n][3] *= e1;
+            ak[n][0] = e0 * (ak[n][0] + h.x);
+            ak[n][1] = e0 * (ak[n][1] + h.y);
+            ak[n][2] = e1 * (ak[n][2] + h.x);
+            ak[n][3] = e1 * (ak[n][3] + h.y);
+            float x, y;
+            const T* p = kt + (j0 + g) * LD + col0 + 8 * n + 2 * t;
+            load_pair(p, x, y);
+            s0 += phi_f<PHI>(x) * ak[n][0] + phi_f<PHI>(y) * ak[n][1];
+            load_pair(p + 8 * LD, x, y);
+            s1 += phi_f<PHI>(x) * ak[n][2] + phi_f<PHI>(y) * ak[n][3];
+        }
+        s0 = quad_sum(s0);
+        s1 = quad_sum(s1);
+        if (t == 0) {
+            sm.row[s & 1][cg][j0 + g] = s0;
+            sm.row[s & 1][cg][j0 + g + 8] = s1;
+        }
+
+        const float hi0 = gs.hi[j0 + g], lo0 = gs.lo[j0 + g], hi1 = gs.hi[j0 + g + 8], lo1 = gs.lo[j0 + g + 8];
+        float rs0 = 0.f, rs1 = 0.f;  // row sums of the pairs' gradients, for the shift of phi(q)
+#pragma unroll
+        for (int it = 0; it < SH::RG; ++it) {
+            if (it < rg) continue;
+            float p[2][4] = {}, dp[2][4] = {};
+#pragma unroll
+            for (int k0 = 0; k0 < D; k0 += 16) {
+                FragA<T> a;
+                FragB<T> b[2];
+                load_a<LD>(a, kt, j0, k0, lane);
+                phi_frag<PHI>(a);
+                load_bt<LD>(b, qt, it * 16, k0, lane);
+                phi_frag<PHI>(b[0]);
+                phi_frag<PHI>(b[1]);
+                mma_step(p[0], a, b[0]);
+                mma_step(p[1], a, b[1]);
+                load_a<LD>(a, vt, j0, k0, lane);
+                load_bt<LD>(b, gt, it * 16, k0, lane);
+                mma_step(dp[0], a, b[0]);
+                mma_step(dp[1], a, b[1]);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int il = n * 8 + 2 * t + e, i = it * 16 + il;
+                    const float hi = gs.hi[i], lo = gs.lo[i], u = gs.up[i], cl = gs.col[i];
+                    const float w0 = it > rg || il >= g ? u * exp2_fast((hi - hi0) + (lo - lo0)) : 0.f;
+                    const float w1 = it > rg || il >= g + 8 ? u * exp2_fast((hi - hi1) + (lo - lo1)) : 0.f;
+                    p[n][e] *= w0;
+                    p[n][2 + e] *= w1;
+                    dp[n][e] = w0 * (dp[n][e] + cl);
+                    dp[n][2 + e] = w1 * (dp[n][2 + e] + cl);
+                }
+            rs0 += (dp[0][0] + dp[0][1]) + (dp[1][0] + dp[1][1]);
+            rs1 += (dp[0][2] + dp[0][3]) + (dp[1][2] + dp[1][3]);
+            FragA<T> ap, ad;  // bf16: rounded once
+            make_a(ap, p[0], p[1]);
+            make_a(ad, dp[0], dp[1]);
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                FragB<T> b[2];
+                load_b<LD>(b, gt, it * 16, col0 + 16 * n, lane);
+                mma_step(av[2 * n], ap, b[0]);
+                mma_step(av[2 * n + 1], ap, b[1]);
+                load_b<LD>(b, qt, it * 16, col0 + 16 * n, lane);
+                base_frag<PHI>(b[0]);
+                base_frag<PHI>(b[1]);
+                mma_step(ak[2 * n], ad, b[0]);
+                mma_step(ak[2 * n + 1], ad, b[1]);
+            }
+        }
+        const int row = first + c * C + j0 + g;
+        rs0 = shifted<PHI> ? quad_sum(rs0) : 0.f;
+        rs1 = shifted<PHI> ? quad_sum(rs1) : 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x, y;
+            const int cc = col0 + 8 * n + 2 * t;
+            const T* kp = kt + (j0 + g) * LD + cc;
+            if (row < end) {
+                load_pair(kp, x, y);
+                store_pair(dk + (size_t)row * D + cc, (ak[n][0] + rs0) * phi_grad(x, PHI), (ak[n][1] + rs0) * phi_grad(y, PHI));
+                store_pair(dv + (size_t)row * D + cc, av[n][0], av[n][1]);
+            }
+            if (row + 8 < end) {
+                load_pair(kp + 8 * LD, x, y);
+                store_pair(dk + (size_t)(row + 8) * D + cc, (ak[n][2] + rs1) * phi_grad(x, PHI), (ak[n][3] + rs1) * phi_grad(y, PHI));
+                store_pair(dv + (size_t)(row + 8) * D + cc, av[n][2], av[n][3]);
+            }
+        }
+        if (s + 1 < nch) {
+            st.template update<PHI>(qt, gt, gs.from_start, gs.col, gs.all, warp, lane);
+            if (SH::SB == 1) __syncthreads();  // every warp has read the operand
+            const int nb = SH::SB == 2 ? ((s + 1) & 1) : 0;
+            st.publish(sm.sop[nb][0], sm.zs[nb], warp, lane);
+            if (warp == 0) scan(s + 1);
+        }
+    }
+    __syncthreads();
+    finish(nch - 1);
+}
+
+template <typename T, int D, int PHI>
+cudaError_t launch_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
+                         const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+                         void* chunk_state, cudaStream_t st) {
+    constexpr size_t smem = sizeof(typename BwdQ<T, D, PHI>::Smem);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    const cudaError_t e = ensure_smem<gated_bwd_q_kernel<T, D, PHI>>(smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(gated_bwd_q_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
+                      smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+                      static_cast<const T*>(g), static_cast<const T*>(dout), prefix, p.N, block_tokens, nblk,
+                      p.normalize, static_cast<T*>(dq), up, col, dgp, static_cast<uint8_t*>(chunk_state));
+}
+
+template <typename T, int D, int PHI>
+cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
+                          const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
+                          const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
+    constexpr size_t smem = sizeof(BwdKvSmem<T, D>);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    const cudaError_t e = ensure_smem<gated_bwd_kv_kernel<T, D, PHI>>(smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(gated_bwd_kv_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
+                      smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+                      static_cast<const T*>(g), static_cast<const T*>(dout), suffix, p.N, block_tokens, nblk, up, col, dgp,
+                      static_cast<const uint8_t*>(chunk_state), static_cast<T*>(dk), static_cast<T*>(dv),
+                      static_cast<T*>(dg));
+}
+
+}  // namespace gated
+
+template <typename T>
+cudaError_t gated_bwd_q_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
+                          const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+                          void* chunk_state, cudaStream_t st) {
+    return gated::dispatch(p, [&](auto d, auto phi) {
+        return gated::launch_bwd_q<T, decltype(d)::value, decltype(phi)::value>(
+            p, q, k, v, g, dout, prefix, block_tokens, nblk, dq, up, col, dgp, chunk_state, st);
+    });
+}
+template <typename T>
+cudaError_t gated_bwd_kv_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
+                           const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
+                           const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
+    return gated::dispatch(p, [&](auto d, auto phi) {
+        return gated::launch_bwd_kv<T, decltype(d)::value, decltype(phi)::value>(
+            p, q, k, v, g, dout, suffix, block_tokens, nblk, up, col, dgp, chunk_state, dk, dv, dg, st);
+    });
+}
+
+}  // namespace la

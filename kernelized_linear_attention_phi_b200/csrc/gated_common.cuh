@@ -1,0 +1,268 @@
+// What the gated kernels share: tile shapes, the gates of a chunk as sums of
+// logarithms, tile loads, and the state's update.
+#pragma once
+
+#include "gated_mma.cuh"
+#include "internal.h"
+
+namespace la {
+namespace gated {
+
+// Tile shapes per element type and d. A chunk has C tokens; NW warps split
+// it into RG row groups of 16 tokens and CG column groups of NCOL channels.
+// The state S (d x d, fp32) lives in the warps' registers: SRT row tiles of
+// 16, each cut into SCG column groups of SN columns. SB: operand copies of S
+// in shared memory (one copy costs one more barrier per chunk).
+// fp32 rows are twice as long, so d >= 64 takes chunks of 32 tokens to keep
+// two stages of tiles within the shared memory of an SM.
+template <typename T, int D> struct Shape {
+    static constexpr bool F32 = sizeof(T) == 4;
+    static constexpr int C = F32 && D >= 64 ? 32 : 64;
+    static constexpr int NW = D == 128 ? 8 : 4;
+    static constexpr int SB = F32 && D == 128 ? 1 : 2;
+    static constexpr int THREADS = NW * 32;
+    static constexpr int LD = D + (F32 ? 8 : 8);
+    static constexpr int EPV = 16 / sizeof(T);
+    static constexpr int RG = C / 16, CG = NW / RG, NCOL = D / CG < 16 ? 16 : D / CG;
+    static constexpr int CGU = D / NCOL;  // column groups with work
+    static constexpr int SRT = D / 16 < NW ? D / 16 : NW;
+    static constexpr int SCG = (NW / SRT) < (D / 16) ? (NW / SRT) : (D / 16);
+    static constexpr int SN = D / SCG;
+    static constexpr int TILE = C * LD;  // elements of a [C x D] tile
+    static constexpr int SOP = D * LD;   // elements of the S operand
+    static_assert(RG * CG == NW && SRT * 16 == D, "tiles");
+};
+
+// The gates of one chunk, from b_i = log2 of the product of the chunk's gates
+// up to token i. b is formed in 64 bits and kept as hi + lo, so that
+// b_i - b_j keeps 2^-24 of its own size however far the chunk has decayed; a
+// closed gate (-inf) counts as 2^-14000, far below any product that fp32 can
+// hold, and drops out of every difference behind it exactly.
+template <int C> struct alignas(16) Gates {
+    float hi[C], lo[C];
+    float from_start[C];  // 2^b_i; 0 past the last token
+    float to_end[C];      // 2^(b_last - b_j); 0 past the last token
+    float up[C], col[C];  // gradients: 1 / den_i and -(out_i . dout_i); 0 past the last token
+    float all;            // 2^b_last
+};
+constexpr double kLog2e = 1.4426950408889634;
+constexpr double kClosed = -14000.0;
+
+// One lane's gates of a chunk, held from the load to the scan.
+template <int C> struct GateRegs { float g[C / 32], up[C / 32], col[C / 32]; };
+template <typename T, int C>
+__device__ __forceinline__ void load_gates(GateRegs<C>& r, const T* g, const float* up, const float* col, int row0, int N,
+                                           int lane) {
+#pragma unroll
+    for (int e = 0; e < C / 32; ++e) {
+        const int i = row0 + lane * (C / 32) + e;
+        const bool in = i < N;
+        r.g[e] = in ? to_f32<T>(g[i]) : 0.f;
+        r.up[e] = in ? (up ? up[i] : 1.f) : 0.f;
+        r.col[e] = in && col ? col[i] : 0.f;
+    }
+}
+// A whole warp. Returns the chunk's log2 sum (every lane).
+template <int C>
+__device__ __forceinline__ double scan_gates(Gates<C>& s, const GateRegs<C>& r, int valid, int lane) {
+    constexpr int R = C / 32;
+    double x[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const double l = (double)r.g[e] * kLog2e;
+        x[e] = l < kClosed ? kClosed : l;  // a NaN stays
+        if (e) x[e] += x[e - 1];
+    }
+    double run = x[R - 1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+    }
+    const double before = run - x[R - 1];
+    const double last = __shfl_sync(0xffffffffu, run, 31);
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const int i = lane * R + e;
+        const double b = before + x[e];
+        const float hi = (float)b;
+        const bool in = i < valid;
+        s.hi[i] = hi;
+        s.lo[i] = (float)(b - (double)hi);
+        s.from_start[i] = in ? exp2_fast((float)b) : 0.f;
+        s.to_end[i] = in ? exp2_fast((float)(last - b)) : 0.f;
+        s.up[i] = r.up[e];
+        s.col[i] = r.col[e];
+    }
+    if (lane == 0) s.all = exp2_fast((float)last);
+    return last;
+}
+
+// The decay from key j to query i of a chunk, 0 for j > i. The differences of
+// -inf sums cannot occur: closed gates are finite here.
+template <int C> __device__ __forceinline__ float decay(const Gates<C>& s, float hi_i, float lo_i, int j) {
+    return exp2_fast((hi_i - s.hi[j]) + (lo_i - s.lo[j]));
+}
+
+// Starts the copy of rows row0 .. row0 + C - 1 of a [N, D] matrix (zeros past N).
+template <typename SH, typename T, int D>
+__device__ __forceinline__ void load_tile(T* dst, const T* src, int row0, int N) {
+    constexpr int VPR = D / SH::EPV;
+#pragma unroll
+    for (int u = threadIdx.x; u < SH::C * VPR; u += SH::THREADS) {
+        const int row = u / VPR, col = (u % VPR) * SH::EPV;
+        const bool in = row0 + row < N;
+        cp_async16(dst + row * SH::LD + col, src + (size_t)(in ? row0 + row : 0) * D + col, in);
+    }
+}
+
+// The state in registers: this warp's row tile and columns of S, and z in the
+// lanes of column 0 (its bf16 remainder products in column 1) of one more
+// accumulator. Warps past SRT * SCG hold nothing.
+template <typename T, int D> struct State {
+    using SH = Shape<T, D>;
+    float S[SH::SN / 8][4];
+    float z[4];
+
+    __device__ __forceinline__ static int row(int warp) { return (warp % SH::SRT) * 16; }
+    __device__ __forceinline__ static int col(int warp) { return (warp / SH::SRT) * SH::SN; }
+    __device__ __forceinline__ static bool owns(int warp) { return warp < SH::SRT * SH::SCG; }
+
+    // from a record (S d*d, then z d at zrec), or zero
+    __device__ __forceinline__ void seed(const float* rec, const float* zrec, int warp, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < SH::SN / 8; ++n) {
+            float2 x = make_float2(0.f, 0.f), y = x;
+            if (rec && owns(warp)) {
+                const float* p = rec + (row(warp) + g) * D + col(warp) + 8 * n + 2 * t;
+                x = *reinterpret_cast<const float2*>(p);
+                y = *reinterpret_cast<const float2*>(p + 8 * D);
+            }
+            S[n][0] = x.x; S[n][1] = x.y; S[n][2] = y.x; S[n][3] = y.y;
+        }
+        const bool zt = rec && owns(warp) && t == 0;
+        z[0] = zt ? zrec[row(warp) + g] : 0.f;
+        z[2] = zt ? zrec[row(warp) + g + 8] : 0.f;
+        z[1] = z[3] = 0.f;
+    }
+    __device__ __forceinline__ void store(float* rec, float* zrec, int warp, int lane) const {
+        if (!owns(warp)) return;
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < SH::SN / 8; ++n) {
+            float* p = rec + (row(warp) + g) * D + col(warp) + 8 * n + 2 * t;
+            *reinterpret_cast<float2*>(p) = make_float2(S[n][0], S[n][1]);
+            *reinterpret_cast<float2*>(p + 8 * D) = make_float2(S[n][2], S[n][3]);
+        }
+        if (col(warp) == 0 && t == 0) {
+            zrec[row(warp) + g] = z[0] + z[1];
+            zrec[row(warp) + g + 8] = z[2] + z[3];
+        }
+    }
+    // the operand of the next chunk's products: S in the element type (bf16:
+    // rounded once, like every other operand of the output's products; the
+    // state itself stays fp32) and, where lo is given, what that rounding
+    // left; z in fp32
+    template <bool LO = false>
+    __device__ __forceinline__ void publish(T* sop, float* zs, int warp, int lane, T* lo = nullptr) const {
+        if (!owns(warp)) return;
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < SH::SN / 8; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = (row(warp) + g + 8 * h) * SH::LD + col(warp) + 8 * n + 2 * t;
+                const float x = S[n][2 * h], y = S[n][2 * h + 1];
+                if constexpr (SH::F32) {
+                    *reinterpret_cast<float2*>(sop + at) = make_float2(x, y);
+                } else {
+                    const uint32_t hi = pack_bf16(x, y);
+                    *reinterpret_cast<uint32_t*>(sop + at) = hi;
+                    if constexpr (LO)
+                        *reinterpret_cast<uint32_t*>(lo + at) = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+                }
+            }
+        if (col(warp) == 0 && t == 0) {
+            zs[row(warp) + g] = z[0] + z[1];
+            zs[row(warp) + g + 8] = z[2] + z[3];
+        }
+    }
+    // S = all S + sum_j w_j phi(x_j) (x) y_j,  z = all z + sum_j w_j phi(x_j) c_j
+    // with x, y [C x D] tiles and w, c (c null: ones) of the chunk. w phi(x)
+    // is formed in fp32 and multiplied as hi + lo operands, so a state of bf16
+    // rows errs by 2^-17 of its terms, not by bf16's 2^-8.
+    template <int PHI>
+    __device__ __forceinline__ void update(const T* x, const T* y, const float* w, const float* c, float all, int warp,
+                                           int lane) {
+        if (!owns(warp)) return;
+        const int t = lane & 3;
+        constexpr int K = SH::C / 16;
+        FragA<T> hi[K], lo[K];
+#pragma unroll
+        for (int kt = 0; kt < K; ++kt) {
+            const int k0 = kt * 16;
+            FragA<T> a;
+            float f[8];
+            load_at<SH::LD>(a, x, k0, row(warp), lane);
+            unpack(a, f);
+            const float2 w0 = *reinterpret_cast<const float2*>(w + k0 + 2 * t);
+            const float2 w1 = *reinterpret_cast<const float2*>(w + k0 + 8 + 2 * t);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                f[2 * r] = phi_f<PHI>(f[2 * r]) * w0.x;
+                f[2 * r + 1] = phi_f<PHI>(f[2 * r + 1]) * w0.y;
+                f[4 + 2 * r] = phi_f<PHI>(f[4 + 2 * r]) * w1.x;
+                f[5 + 2 * r] = phi_f<PHI>(f[5 + 2 * r]) * w1.y;
+            }
+            split_a(hi[kt], lo[kt], f);
+        }
+        // A chunk's sum is formed from zero and then added: the matrix
+        // instructions' additions do not round to nearest, which over a
+        // long row would pull every entry the same way.
+#pragma unroll
+        for (int n = 0; n < SH::SN / 16; ++n) {
+            float s[2][4] = {};
+#pragma unroll
+            for (int kt = 0; kt < K; ++kt) {
+                FragB<T> b[2];
+                load_b<SH::LD>(b, y, kt * 16, col(warp) + 16 * n, lane);
+                if constexpr (!SH::F32) {
+                    mma_step(s[0], lo[kt], b[0]);
+                    mma_step(s[1], lo[kt], b[1]);
+                }
+                mma_step(s[0], hi[kt], b[0]);
+                mma_step(s[1], hi[kt], b[1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                S[2 * n][e] = fmaf(S[2 * n][e], all, s[0][e]);
+                S[2 * n + 1][e] = fmaf(S[2 * n + 1][e], all, s[1][e]);
+            }
+        }
+        if (col(warp) == 0) {
+            float s[4] = {};
+#pragma unroll
+            for (int kt = 0; kt < K; ++kt) {
+                FragB<T> b;
+                if (c) {
+                    load_column(b, c, kt * 16, lane);
+                } else {
+                    const bool one = lane < 4;  // column 0 of ones
+                    if constexpr (SH::F32) {
+                        b.r[0] = b.r[1] = b.r[2] = b.r[3] = one ? 1.f : 0.f;
+                    } else {
+                        b.r[0] = b.r[1] = one ? 0x3f803f80u : 0u;
+                    }
+                }
+                if constexpr (!SH::F32) mma_step(s, lo[kt], b);
+                mma_step(s, hi[kt], b);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = fmaf(z[e], all, s[e]);
+        }
+    }
+};
+
+}  // namespace gated
+}  // namespace la

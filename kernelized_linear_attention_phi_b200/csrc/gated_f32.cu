@@ -1,0 +1,14 @@
+// Gated linear attention, forward, fp32 (gated_fwd.cuh).
+
+#include "gated_fwd.cuh"
+
+namespace la {
+
+template cudaError_t gated_sweep_t<float>(
+    const Problem&, const void*, const void*, const void*, const void*, const float*, const float*, const float*, int, int,
+    void*, float*, float*, cudaStream_t);
+template cudaError_t gated_states_t<float>(
+    const Problem&, bool, const void*, const void*, const void*, const float*, const float*, int, int, int, int, float*,
+    float*, cudaStream_t);
+
+}  // namespace la

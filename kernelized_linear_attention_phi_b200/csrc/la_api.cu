@@ -6,14 +6,17 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
 #include "common.cuh"
 #include "device.h"
+#include "gated.h"
 #include "internal.h"
 #include "launch_util.h"
 #include "plan.h"
+#include "qk_rope.h"
 #include "tc.h"
 #include "tc_common.cuh"
 
@@ -79,12 +82,16 @@ plan::SplitPlan kv_plan(const Problem& p) { return plan::kv_plan(p, device_sms()
 plan::BlockPlan block_plan(const Problem& p) { return plan::block_plan(p, device_sms()); }
 using plan::BlockPlan;
 using plan::SplitPlan;
+BlockPlan gated_plan(const Problem& p, bool backward) {
+    return plan::gated_plan(p, device_sms(), plan::gated_ctas_per_sm(p, backward));
+}
 
 int prefix_nbins(const Problem& p, int kchunk) { return p.N / kchunk + 1; }
 
 struct WsLayout {
     size_t part = 0, sz = 0, perm = 0, msort = 0, bins = 0, total = 0;
     size_t grec = 0, gtot = 0, gn = 0, gden = 0;  // gradients
+    size_t dec = 0, up = 0, col = 0, dgp = 0, chunks = 0;  // gated forms
 };
 
 WsLayout ws_layout(const Problem& p, int op) {
@@ -145,6 +152,28 @@ WsLayout ws_layout(const Problem& p, int op) {
         off = round_up(off + sizeof(float) * (size_t)p.bh() * p.N * p.d, kAlign);
         L.gden = off;
         off = round_up(off + sizeof(float) * (size_t)p.bh() * p.N, kAlign);
+    } else if (op == LA_OP_GATED_CAUSAL || op == LA_OP_GATED_CAUSAL_BWD) {
+        const bool bwd = op == LA_OP_GATED_CAUSAL_BWD;
+        const BlockPlan bp = gated_plan(p, bwd);
+        if (bp.nblk > 1) {  // block states and the products of the blocks' gates
+            L.part = off;
+            off = round_up(off + (size_t)p.bh() * bp.nblk * rec, kAlign);
+            L.dec = off;
+            off = round_up(off + (size_t)p.bh() * bp.nblk * sizeof(float), kAlign);
+        } else if (!bwd) {
+            return L;
+        }
+        if (bwd) {
+            const size_t tokens = (size_t)p.bh() * p.N * sizeof(float);
+            L.up = off;
+            off = round_up(off + tokens, kAlign);
+            L.col = off;
+            off = round_up(off + tokens, kAlign);
+            L.dgp = off;
+            off = round_up(off + tokens, kAlign);
+            L.chunks = off;
+            off = round_up(off + (size_t)p.bh() * cdiv(p.N, gated_chunk(p)) * gated_chunk_state_bytes(p), kAlign);
+        }
     } else {
         return L;
     }
@@ -174,6 +203,48 @@ la_status check_ws(const WsLayout& L, void* ws, size_t ws_bytes) {
         la_status s__ = (expr);           \
         if (s__ != LA_OK) return s__;     \
     } while (0)
+
+la_status check_rope(const la_rope_desc* d) {
+    if (d == nullptr) return LA_ERR_INVALID_ARG;
+    if (d->B <= 0 || d->N <= 0 || d->Hq <= 0 || d->Hk <= 0 || d->d <= 0) return LA_ERR_INVALID_ARG;
+    if (d->dtype != LA_F32 && d->dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (d->interleaved != 0 && d->interleaved != 1) return LA_ERR_INVALID_ARG;
+    if (d->rot < 0 || d->table_rows < 0 || !(d->eps >= 0.f) || !std::isfinite(d->eps)) return LA_ERR_INVALID_ARG;
+    if (d->d != 16 && d->d != 32 && d->d != 64 && d->d != 128) return LA_ERR_UNSUPPORTED;
+    if (d->rot > d->d || d->rot % 16 != 0) return LA_ERR_UNSUPPORTED;
+    if (d->rot > 0 && d->table_rows == 0) return LA_ERR_INVALID_ARG;
+    if (d->Hq > 32767 || d->Hk > 32767) return LA_ERR_UNSUPPORTED;  // grid.y limit
+    if ((long long)d->B * d->N >= (1LL << 31)) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+// A [B, N, H, d] view: strides in multiples of 16 bytes, not negative; rows of
+// an output must not fall on one another.
+la_status check_strides(const la_rope_desc& d, const la_strides& s, int H, bool output) {
+    const long long unit = d.dtype == LA_F32 ? 4 : 8;
+    const long long size[3] = {d.B, d.N, H}, stride[3] = {s.b, s.n, s.h};
+    for (int i = 0; i < 3; ++i) {
+        if (size[i] == 1) continue;
+        if (stride[i] < 0 || (output && stride[i] < d.d)) return LA_ERR_INVALID_ARG;
+        if (stride[i] % unit != 0) return LA_ERR_MISALIGNED;
+    }
+    return LA_OK;
+}
+
+la_status check_rope_inputs(const la_rope_desc& d, const void* q, const la_strides* qs, const void* k,
+                            const la_strides* ks, const float* wq, const float* wk, const float* cos, const float* sin,
+                            const int32_t* positions) {
+    if (!q || !k || !qs || !ks) return LA_ERR_INVALID_ARG;
+    if ((wq == nullptr) != (wk == nullptr)) return LA_ERR_INVALID_ARG;
+    if (d.rot > 0 && (!cos || !sin)) return LA_ERR_INVALID_ARG;
+    if (d.rot > 0 && !positions && d.table_rows < d.N) return LA_ERR_INVALID_ARG;
+    for (const void* ptr : {q, k, static_cast<const void*>(wq), static_cast<const void*>(wk),
+                            static_cast<const void*>(cos), static_cast<const void*>(sin),
+                            static_cast<const void*>(positions)})
+        if (!aligned16(ptr)) return LA_ERR_MISALIGNED;
+    LA_TRY(check_strides(d, *qs, d.Hq, false));
+    return check_strides(d, *ks, d.Hk, false);
+}
 
 la_status kv_summary_impl(const Problem& p, const void* k, const void* v, float* S, float* z,
                           void* ws, cudaStream_t st) {
@@ -235,7 +306,7 @@ const char* la_status_string(la_status s) {
 size_t la_workspace_size(const la_desc* desc, int32_t op, int32_t chunk) {
     if (check_desc(desc) != LA_OK) return 0;
     if ((op == LA_OP_CAUSAL || op == LA_OP_PREFIX) && check_chunk(chunk) != LA_OK) return 0;
-    if (op < LA_OP_KV_SUMMARY || op > LA_OP_CAUSAL_BWD) return 0;
+    if (op < LA_OP_KV_SUMMARY || op > LA_OP_GATED_CAUSAL_BWD) return 0;
     return ws_layout(to_problem(desc), op).total;
 }
 
@@ -495,6 +566,133 @@ la_status la_decode_step(const la_desc* desc, const void* q, const void* k, cons
     timing_begin(static_cast<cudaStream_t>(stream));
     return cuda_status(decode_step(to_problem(&d1), q, k, v, S, z, out,
                                    static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, const void* v, const void* g,
+                          const float* S_in, const float* z_in, void* out, float* S_out, float* z_out, void* ws,
+                          size_t ws_bytes, void* stream) {
+    LA_TRY(check_desc(desc));
+    if (!q || !k || !v || !g || !out) return LA_ERR_INVALID_ARG;
+    if ((S_in == nullptr) != (z_in == nullptr) || (S_out == nullptr) != (z_out == nullptr)) return LA_ERR_INVALID_ARG;
+    for (const void* ptr : {q, k, v, g, static_cast<const void*>(out), static_cast<const void*>(S_in),
+                            static_cast<const void*>(z_in), static_cast<const void*>(S_out),
+                            static_cast<const void*>(z_out)})
+        if (!aligned16(ptr)) return LA_ERR_MISALIGNED;
+    const Problem p = to_problem(desc);
+    const WsLayout L = ws_layout(p, LA_OP_GATED_CAUSAL);
+    if (L.total) LA_TRY(check_ws(L, ws, ws_bytes));
+    LA_TRY(check_device());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    timing_begin(st);
+    const BlockPlan bp = gated_plan(p, false);
+    if (bp.nblk == 1)
+        return cuda_status(gated_sweep(p, q, k, v, g, nullptr, S_in, z_in, bp.block_tokens, 1, out, S_out, z_out, st));
+    // own states of the blocks (the last block's only for the state after it),
+    // then the state in front of each, then the outputs
+    float* part = at<float>(ws, L.part);
+    float* dec = at<float>(ws, L.dec);
+    LA_TRY(cuda_status(gated_states(p, false, k, v, g, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
+                                    S_out ? bp.nblk : bp.nblk - 1, part, dec, st)));
+    LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));
+    return cuda_status(gated_sweep(p, q, k, v, g, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, nullptr, nullptr,
+                                   st));
+}
+
+la_status la_gated_causal_backward(const la_desc* desc, const void* q, const void* k, const void* v, const void* g,
+                                   const void* dout, void* dq, void* dk, void* dv, void* dg, void* ws, size_t ws_bytes,
+                                   void* stream) {
+    LA_TRY(check_desc(desc));
+    if (!q || !k || !v || !g || !dout || !dq || !dk || !dv || !dg) return LA_ERR_INVALID_ARG;
+    for (const void* ptr : {q, k, v, g, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                            static_cast<const void*>(dv), static_cast<const void*>(dg)})
+        if (!aligned16(ptr)) return LA_ERR_MISALIGNED;
+    const Problem p = to_problem(desc);
+    const WsLayout L = ws_layout(p, LA_OP_GATED_CAUSAL_BWD);
+    LA_TRY(check_ws(L, ws, ws_bytes));
+    LA_TRY(check_device());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    timing_begin(st);
+    const BlockPlan bp = gated_plan(p, true);
+    float* up = p.normalize ? at<float>(ws, L.up) : nullptr;
+    float* col = p.normalize ? at<float>(ws, L.col) : nullptr;
+    float* dgp = at<float>(ws, L.dgp);
+    void* chunks = at<char>(ws, L.chunks);
+    float *part = nullptr, *dec = nullptr;
+    if (bp.nblk > 1) {
+        part = at<float>(ws, L.part);
+        dec = at<float>(ws, L.dec);
+        LA_TRY(cuda_status(gated_states(p, false, k, v, g, nullptr, nullptr, bp.block_tokens, bp.nblk, 0, bp.nblk - 1,
+                                        part, dec, st)));
+        LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
+    }
+    LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, g, dout, part, bp.block_tokens, bp.nblk, dq, up, col, dgp, chunks, st)));
+    if (bp.nblk > 1) {  // the same records, from the other end
+        LA_TRY(cuda_status(gated_states(p, true, q, dout, g, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, part, dec,
+                                        st)));
+        LA_TRY(cuda_status(gated_scan(p, true, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
+    }
+    return cuda_status(gated_bwd_kv(p, q, k, v, g, dout, part, bp.block_tokens, bp.nblk, up, col, dgp, chunks, dk, dv, dg,
+                                    st));
+}
+
+la_status la_gated_decode_step(const la_desc* desc, const void* q, const void* k, const void* v, const void* g,
+                               const float* S, const float* z, float* S_out, float* z_out, void* out, void* stream) {
+    if (desc == nullptr) return LA_ERR_INVALID_ARG;
+    la_desc d1 = *desc;
+    d1.N = 1;  // N is not used by a step
+    LA_TRY(check_desc(&d1));
+    if (!q || !k || !v || !g || !S || !z || !S_out || !z_out || !out) return LA_ERR_INVALID_ARG;
+    for (const void* ptr : {q, k, v, g, static_cast<const void*>(S), static_cast<const void*>(z),
+                            static_cast<const void*>(S_out), static_cast<const void*>(z_out),
+                            static_cast<const void*>(out)})
+        if (!aligned16(ptr)) return LA_ERR_MISALIGNED;
+    LA_TRY(check_device());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    timing_begin(st);
+    return cuda_status(gated_decode(to_problem(&d1), q, k, v, g, S, z, S_out, z_out, out, st));
+}
+
+size_t la_qk_norm_rope_workspace_size(const la_rope_desc* desc) {
+    if (check_rope(desc) != LA_OK) return 0;
+    return WS_HEADER + round_up(qk_rope_partials(*desc, device_sms()) * desc->d * sizeof(float), kAlign);
+}
+
+la_status la_qk_norm_rope(const la_rope_desc* desc, const void* q, const la_strides* q_strides, const void* k,
+                          const la_strides* k_strides, const float* wq, const float* wk, const float* cos,
+                          const float* sin, const int32_t* positions, void* q_out, void* k_out, void* stream) {
+    LA_TRY(check_rope(desc));
+    LA_TRY(check_rope_inputs(*desc, q, q_strides, k, k_strides, wq, wk, cos, sin, positions));
+    if (!q_out || !k_out) return LA_ERR_INVALID_ARG;
+    if (!aligned16(q_out) || !aligned16(k_out)) return LA_ERR_MISALIGNED;
+    LA_TRY(check_device());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    timing_begin(st);
+    return cuda_status(qk_norm_rope(*desc, q, *q_strides, k, *k_strides, wq, wk, cos, sin, positions, q_out, k_out, st));
+}
+
+la_status la_qk_norm_rope_backward(const la_rope_desc* desc, const void* q, const la_strides* q_strides, const void* k,
+                                   const la_strides* k_strides, const float* wq, const float* wk, const float* cos,
+                                   const float* sin, const int32_t* positions, const void* dq_out, const void* dk_out,
+                                   void* dq, const la_strides* dq_strides, void* dk, const la_strides* dk_strides,
+                                   float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream) {
+    LA_TRY(check_rope(desc));
+    LA_TRY(check_rope_inputs(*desc, q, q_strides, k, k_strides, wq, wk, cos, sin, positions));
+    if (!dq_out || !dk_out || !dq || !dk || !dq_strides || !dk_strides) return LA_ERR_INVALID_ARG;
+    if ((dwq == nullptr) != (dwk == nullptr)) return LA_ERR_INVALID_ARG;
+    for (const void* ptr : {dq_out, dk_out, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                            static_cast<const void*>(dwq), static_cast<const void*>(dwk)})
+        if (!aligned16(ptr)) return LA_ERR_MISALIGNED;
+    LA_TRY(check_strides(*desc, *dq_strides, desc->Hq, true));
+    LA_TRY(check_strides(*desc, *dk_strides, desc->Hk, true));
+    WsLayout L;
+    L.total = la_qk_norm_rope_workspace_size(desc);
+    LA_TRY(check_ws(L, ws, ws_bytes));
+    LA_TRY(check_device());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    timing_begin(st);
+    return cuda_status(qk_norm_rope_backward(*desc, q, *q_strides, k, *k_strides, wq, wk, cos, sin, positions, dq_out,
+                                             dk_out, dq, *dq_strides, dk, *dk_strides, dwq, dwk,
+                                             at<float>(ws, WS_HEADER), st));
 }
 
 la_status la_last_error(void* ws, void* stream, uint32_t* flags_out) {

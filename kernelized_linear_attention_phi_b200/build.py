@@ -25,7 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["la_api.cu", "device.cu", "simt.cu", "bin.cu", "decode.cu", "tc_host.cu", "tc_kv.cu", "tc_sweep.cu", "tc_sweep_t.cu", "tc_f32.cu",
            "static_scratch.cu", "timing.cu", "bwd.cu", "tc_bwd.cu", "tc_bwd_causal.cu", "tc_bwd_causal_t.cu", "tc_fused.cu",
-           "gated.cu", "gated_bf16.cu", "gated_f32.cu", "gated_bwd_bf16.cu", "gated_bwd_f32.cu", "qk_rope.cu"]
+           "gated.cu", "gated_bf16.cu", "gated_f32.cu", "gated_bwd_bf16.cu", "gated_bwd_f32.cu", "tc_gated.cu", "qk_rope.cu"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

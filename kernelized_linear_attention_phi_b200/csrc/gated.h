@@ -31,6 +31,15 @@ cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const vo
 // is not read.
 cudaError_t gated_scan(const Problem& p, bool reverse, float* rec, const float* dec, int nblk, const float* S_in,
                        const float* z_in, float* S_out, float* z_out, cudaStream_t st);
+// The same on tcgen05 tensor cores (tc_gated.cu): bf16, d = 128, forward
+// states and outputs. An expired wait sets tc::FLAG_TIMEOUT in *err.
+bool tc_gated_supported(const Problem& p);
+cudaError_t tc_gated_states(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
+                            int count, float* part, float* dec, uint32_t* err, cudaStream_t st);
+cudaError_t tc_gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g,
+                           const float* prefix, const float* S_in, const float* z_in, int block_tokens, int nblk, void* out,
+                           uint32_t* err, cudaStream_t st);
+
 // One token: S_out = e^g S + phi(k) (x) v and so on, read out. S_out / z_out
 // may be S / z.
 cudaError_t gated_decode(const Problem& p, const void* q, const void* k, const void* v, const void* g, const float* S,

@@ -155,7 +155,8 @@ WsLayout ws_layout(const Problem& p, int op) {
     } else if (op == LA_OP_GATED_CAUSAL || op == LA_OP_GATED_CAUSAL_BWD) {
         const bool bwd = op == LA_OP_GATED_CAUSAL_BWD;
         const BlockPlan bp = gated_plan(p, bwd);
-        if (bp.nblk > 1) {  // block states and the products of the blocks' gates
+        const bool tcf = !bwd && tc_gated_supported(p);  // forms the last state from a record too
+        if (bp.nblk > 1 || tcf) {  // block states and the products of the blocks' gates
             L.part = off;
             off = round_up(off + (size_t)p.bh() * bp.nblk * rec, kAlign);
             L.dec = off;
@@ -585,12 +586,21 @@ la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, con
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     timing_begin(st);
     const BlockPlan bp = gated_plan(p, false);
-    if (bp.nblk == 1)
-        return cuda_status(gated_sweep(p, q, k, v, g, nullptr, S_in, z_in, bp.block_tokens, 1, out, S_out, z_out, st));
     // own states of the blocks (the last block's only for the state after it),
     // then the state in front of each, then the outputs
     float* part = at<float>(ws, L.part);
     float* dec = at<float>(ws, L.dec);
+    if (tc_gated_supported(p)) {
+        uint32_t* flags = at<uint32_t>(ws, 0);
+        const int count = S_out ? bp.nblk : bp.nblk - 1;
+        if (count == 0)
+            return cuda_status(tc_gated_sweep(p, q, k, v, g, nullptr, S_in, z_in, bp.block_tokens, 1, out, flags, st));
+        LA_TRY(cuda_status(tc_gated_states(p, k, v, g, bp.block_tokens, bp.nblk, count, part, dec, flags, st)));
+        LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));
+        return cuda_status(tc_gated_sweep(p, q, k, v, g, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, flags, st));
+    }
+    if (bp.nblk == 1)
+        return cuda_status(gated_sweep(p, q, k, v, g, nullptr, S_in, z_in, bp.block_tokens, 1, out, S_out, z_out, st));
     LA_TRY(cuda_status(gated_states(p, false, k, v, g, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
                                     S_out ? bp.nblk : bp.nblk - 1, part, dec, st)));
     LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));

@@ -1,0 +1,696 @@
+// Gated linear attention at d = 128 on tcgen05 tensor cores (bf16), forward.
+//
+// Block states (tc_gated_state_kernel): a block's own state is
+//   S = sum_j w_j phi(k_j) (x) v_j,  w_j = product of the block's gates behind j,
+// with the weights relative to the block's end: the chunks run from the last
+// to the first, so w is a running product and S is never rescaled. w phi(K) is
+// formed in fp32 and multiplied as two bf16 operands (error 2^-17 of a term).
+//
+// Sweep (tc_gated_sweep_kernel): the transposed layout of the ungated d = 128
+// sweep (tc_sweep_t.cu): S^T and O^T have d_v = 128 lanes. Per chunk, with
+// b_i = log2 of the product of the chunk's gates up to i:
+//   O^T  = S_prev^T phi(Q)^T                     query i unscaled
+//   O^T += V^T P~^T,  P~_ij = (phi(q_i).phi(k_j)) 2^(-b_j)   j <= i
+//   out_i = 2^(b_i) O_i / den_i,  den_i = 2^(b_i) (phi(q_i).z_prev + sum_j P~_ij)
+//   S^T  = 2^(b_last) S^T + V^T (w phi(K)),  w_j = 2^(b_last - b_j)
+// so that one accumulator takes both parts and the decay of a weight is one
+// factor per key (and of a normalized output none at all). 2^(-b_j) is bounded:
+// where b_i < -90 the scale 2^(b_i) becomes 2^(-90), P~_ij = P_ij 2^(b_i + 90 -
+// b_j), which leaves the state in front a weight of 2^(-90) next to the
+// query's own key instead of the smaller true one.
+
+#include "tc_gated.cuh"
+
+namespace la {
+namespace {
+
+using namespace tcg;
+
+// ---------------------------------------------------------------------------
+// Block states
+// ---------------------------------------------------------------------------
+struct GsCfg {
+    static constexpr int D = 128, C = 64, NB = 2, BOX = C * 128, TILE = NB * BOX;
+    static constexpr int STAGES = 4;
+    static constexpr int STAGE = 2 * TILE;          // K (becomes the high part), V
+    static constexpr int FLUSH = 8;                 // chunks per accumulation in TMEM
+    static constexpr int RED = 8 * D * 4;
+    static constexpr int NBAR = 3 * STAGES + 2;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 2 * TILE + RED + STAGES * C * 4 + 8 * NBAR + 16;
+    static constexpr int THREADS = 64 + 256;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// Warp 0: TMA and gates; warp 1: MMA; warps 2..9: w phi(K) in two parts, z, and
+// the accumulators' sums (each FLUSH chunks' products are added to fp32
+// registers, so long blocks do not depend on how the tensor core rounds its
+// additions).
+template <int PHI>
+__global__ void __launch_bounds__(GsCfg::THREADS, 1)
+tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                      const __nv_bfloat16* __restrict__ gate, int N, int block_tokens, int nblk, float* __restrict__ part,
+                      float* __restrict__ dec, uint32_t* __restrict__ err) {
+    using CF = GsCfg;
+    constexpr int D = CF::D, C = CF::C;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = align1024(smem_raw);
+    uint8_t* lo = stages + CF::STAGES * CF::STAGE;  // low parts of two chunks
+    float* red = reinterpret_cast<float*>(lo + 2 * CF::TILE);
+    float* wts = red + 8 * D;  // [stage][C]
+    uint64_t* full = reinterpret_cast<uint64_t*>(wts + CF::STAGES * C);
+    uint64_t* tdone = full + CF::STAGES;
+    uint64_t* empty = tdone + CF::STAGES;
+    uint64_t* acc = empty + CF::STAGES;  // [2] accumulator complete
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc + 2);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int blk = blockIdx.x, bh = blockIdx.y;
+    const int first = blk * block_tokens, end = min(N, first + block_tokens);
+    const int nci = (end - first + C - 1) / C;
+    if (threadIdx.x == 0) {
+        cta_abort_reset();
+        for (int s = 0; s < CF::STAGES; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(tdone + s, 256);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(acc, 1);
+        mbar_init(acc + 1, 1);
+        fence_mbar_init();
+        tma_prefetch_map(&mK);
+        tma_prefetch_map(&mV);
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 256);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    // step i is chunk nci - 1 - i
+    if (warp == 0) {
+        const __nv_bfloat16* g = gate + (size_t)bh * N;
+        double after = 0.0;  // log2 of the gates behind the chunk, within the block
+        float2 gr = load_gates(g, first + (nci - 1) * C, end, lane);
+        int issued = 0;
+        for (int i = 0; i < nci; ++i) {
+            const int s = i % CF::STAGES, u = i / CF::STAGES, row = first + (nci - 1 - i) * C;
+            if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(empty + s, (u - 1) & 1, err))) break;
+            double b0, b1;
+            const double last = scan_gates(gr, lane, b0, b1);
+            float* w = wts + s * C + 2 * lane;
+            w[0] = row + 2 * lane < end ? ex2((float)(after + (last - b0))) : 0.f;
+            w[1] = row + 2 * lane + 1 < end ? ex2((float)(after + (last - b1))) : 0.f;
+            after += last;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full + s, CF::STAGE);
+                uint8_t* st = stages + s * CF::STAGE;
+#pragma unroll
+                for (int bx = 0; bx < CF::NB; ++bx) {
+                    tma_load_3d(st + bx * CF::BOX, &mK, full + s, bx * 64, row, bh);
+                    tma_load_3d(st + CF::TILE + bx * CF::BOX, &mV, full + s, bx * 64, row, bh);
+                }
+            }
+            issued = i + 1;
+            if (i + 1 < nci) gr = load_gates(g, row - C, end, lane);
+        }
+        if (lane == 0) {
+            dec[(size_t)bh * nblk + blk] = ex2((float)after);
+            for (int i = max(0, issued - CF::STAGES); i < issued; ++i)
+                mbar_wait(full + i % CF::STAGES, (i / CF::STAGES) & 1, err, false);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_bf16(D, D, true, true);
+            bool ok = true;
+            for (int i = 0; i < nci && ok; ++i) {
+                const int s = i % CF::STAGES, f = i / CF::FLUSH;
+                if (!(ok = mbar_wait(tdone + s, (i / CF::STAGES) & 1, err))) break;
+                tc_fence_after();
+                const uint32_t kt = smem_u32(stages + s * CF::STAGE), vt = kt + CF::TILE;
+                const uint32_t lt = smem_u32(lo + (i & 1) * CF::TILE), d = tmem + (f & 1) * D;
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk) {
+                    const uint64_t b = sdesc(vt + kk * 2048, CF::BOX, 1024);
+                    mma_bf16(d, sdesc(lt + kk * 2048, CF::BOX, 1024), b, id, (i % CF::FLUSH > 0 || kk > 0) ? 1u : 0u);
+                    mma_bf16(d, sdesc(kt + kk * 2048, CF::BOX, 1024), b, id, 1u);
+                }
+                mma_commit(empty + s);
+                if (i + 1 == nci || (i + 1) % CF::FLUSH == 0) mma_commit(acc + (f & 1));
+            }
+        }
+    } else {
+        const int et = threadIdx.x - 64, wq = warp - 2, sp = warp & 3, half = wq / 4;
+        const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
+        const int g = (lane & 7) ^ ((et >> 3) & 7);  // column group (of 8) of this thread's 16-byte chunks
+        float S[64], zk[CF::NB][8];
+#pragma unroll
+        for (int e = 0; e < 64; ++e) S[e] = 0.f;
+#pragma unroll
+        for (int b = 0; b < CF::NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) zk[b][e] = 0.f;
+        // adds accumulator f; its next use starts two flushes later, behind
+        // the tdone arrivals of every thread here
+        auto take = [&](int f) {
+            mbar_wait(acc + (f & 1), (f >> 1) & 1, err);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[16];
+                tmem_ld16(tmem + lane_base + (f & 1) * D + half * 64 + 16 * c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) S[16 * c + e] += __uint_as_float(r[e]);
+            }
+            tc_fence_before();
+        };
+        for (int i = 0; i < nci; ++i) {
+            const int s = i % CF::STAGES, u = i / CF::STAGES;
+            // accumulator f is taken during the first chunk of flush f + 1
+            if (i > 0 && i % CF::FLUSH == 0) take(i / CF::FLUSH - 1);
+            mbar_wait(full + s, u & 1, err);
+            // the low part's buffer: chunk i - 2's products have read it
+            if (i >= 2) mbar_wait(empty + (i - 2) % CF::STAGES, ((i - 2) / CF::STAGES) & 1, err);
+            uint8_t* kt = stages + s * CF::STAGE;
+            uint8_t* lt = lo + (i & 1) * CF::TILE;
+            const float* w = wts + s * C;
+#pragma unroll
+            for (int bx = 0; bx < CF::NB; ++bx)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int p = et + 256 * j;
+                    uint4* kp = reinterpret_cast<uint4*>(kt + bx * CF::BOX + p * 16);
+                    float f[8];
+                    uint4 hi, rest;
+                    weighted8<PHI>(*kp, w[p >> 3], f, hi, rest);
+                    *kp = hi;
+                    *reinterpret_cast<uint4*>(lt + bx * CF::BOX + p * 16) = rest;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) zk[bx][e] += f[e];
+                }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(tdone + s);
+        }
+        take((nci - 1) / CF::FLUSH);
+        float* rec = part + ((size_t)bh * nblk + blk) * (size_t)(D * D + D);
+#pragma unroll
+        for (int bx = 0; bx < CF::NB; ++bx) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {  // lanes l, l^9, l^18, l^27 hold the same column group
+                zk[bx][e] += __shfl_xor_sync(0xffffffffu, zk[bx][e], 9);
+                zk[bx][e] += __shfl_xor_sync(0xffffffffu, zk[bx][e], 18);
+            }
+            if (lane < 8) {
+                float4* dst = reinterpret_cast<float4*>(red + wq * D + bx * 64 + g * 8);
+                dst[0] = make_float4(zk[bx][0], zk[bx][1], zk[bx][2], zk[bx][3]);
+                dst[1] = make_float4(zk[bx][4], zk[bx][5], zk[bx][6], zk[bx][7]);
+            }
+        }
+        named_bar(1, 256);
+        if (et < D) {
+            float z = 0.f;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) z += red[x * D + et];
+            rec[(size_t)D * D + et] = z;
+        }
+        float4* o = reinterpret_cast<float4*>(rec + (size_t)(sp * 32 + lane) * D + half * 64);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sweep
+// ---------------------------------------------------------------------------
+struct GtCfg {
+    static constexpr int D = 128, C = 64, NB = 2;
+    static constexpr int BOX = C * 128;            // one 64-row x 64-column box (8 KB)
+    static constexpr int KBOX = (C + 16) * 128;    // K box + 16 rows (z_hi, z_lo, zeros)
+    static constexpr int TILE = NB * BOX;
+    static constexpr int OFF_K = TILE, OFF_V = OFF_K + NB * KBOX, STAGE = OFF_V + TILE;
+    static constexpr uint32_t TX = 3 * TILE;
+    static constexpr int STAGES = 3;
+    static constexpr int PT = C * C * 2;           // P~ [query][key], K-major (x2)
+    static constexpr int STG = TILE;               // output staging tile
+    static constexpr int KW = 2 * TILE;            // w phi(K), high and low part
+    static constexpr int RED = 8 * D * 4;          // column-sum partials [warp][d_k]
+    static constexpr int INV = C * 4;              // output scale per query row
+    static constexpr int GATES = STAGES * 2 * C * 4;  // [stage][b | 2^-b]
+    static constexpr int NBAR = 2 * STAGES + 2 + 4 * 2;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 2 * PT + STG + KW + RED + INV + GATES + 8 * NBAR + 16;
+    // TMEM columns, as in tc_sweep_t.cu
+    static constexpr int COL_S = 0, COL_SB = 128, COL_P = 256, COL_O = 384;
+    static constexpr int PREP = 256, THREADS = 64 + PREP + 128;
+    static_assert(SMEM + 16 <= 227 * 1024, "shared memory (16 bytes static)");
+    static_assert(STAGE % 1024 == 0 && KBOX % 1024 == 0, "1024-byte aligned operand tiles");
+};
+
+template <int PHI>
+__global__ void __launch_bounds__(GtCfg::THREADS, 1)
+tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                      const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mOut,
+                      const __nv_bfloat16* __restrict__ gate, const float* __restrict__ prefix,
+                      const float* __restrict__ S_in, const float* __restrict__ z_in, int N, int block_tokens, int nblk,
+                      int normalize, uint32_t* __restrict__ err) {
+    using CF = GtCfg;
+    constexpr int D = CF::D, C = CF::C;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = align1024(smem_raw);
+    uint8_t* pt = stages + CF::STAGES * CF::STAGE;
+    uint8_t* stg = pt + 2 * CF::PT;
+    uint8_t* kw = stg + CF::STG;
+    float* red = reinterpret_cast<float*>(kw + CF::KW);
+    float* inv = red + 8 * D;
+    float* gates = inv + C;
+    uint64_t* full = reinterpret_cast<uint64_t*>(gates + CF::STAGES * 2 * C);
+    uint64_t* empty = full + CF::STAGES;
+    uint64_t* bprep = empty + CF::STAGES;  // K', Q, w phi(K) and S_prev^T ready
+    uint64_t* bsdone = bprep + 1;          // S^T update of the chunk done
+    uint64_t* bpfull = bsdone + 1;         // per slot (chunk % 2): P ready, P~ written, O^T ready, O^T read
+    uint64_t* bptready = bpfull + 2;
+    uint64_t* bofull = bptready + 2;
+    uint64_t* bofree = bofull + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bofree + 2);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int blk = blockIdx.x, bh = blockIdx.y;
+    const int first = blk * block_tokens, end = min(N, first + block_tokens);
+    const int nci = (end - first + C - 1) / C;
+    constexpr bool mapped = PHI != PHI_IDENTITY;
+
+    if (threadIdx.x == 0) {
+        cta_abort_reset();
+        for (int s = 0; s < CF::STAGES; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(bprep, CF::PREP);
+        mbar_init(bsdone, 1);
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(bpfull + j, 1);
+            mbar_init(bptready + j, 128);
+            mbar_init(bofull + j, 1);
+            mbar_init(bofree + j, 128);
+        }
+        fence_mbar_init();
+        tma_prefetch_map(&mQ);
+        tma_prefetch_map(&mK);
+        tma_prefetch_map(&mV);
+        tma_prefetch_map(&mOut);
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    if (warp == 0) {
+        // ---------------- TMA producer and gates (whole warp) ----------------
+        const __nv_bfloat16* g = gate + (size_t)bh * N;
+        float2 gr = load_gates(g, first, end, lane);
+        int nld = 0;
+        for (int ci = 0; ci < nci; ++ci) {
+            const int s = ci % CF::STAGES, u = ci / CF::STAGES, row = first + ci * C;
+            if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(empty + s, (u - 1) & 1, err))) break;
+            double b0, b1;
+            scan_gates(gr, lane, b0, b1);
+            float* gs = gates + s * 2 * C + 2 * lane;
+            const float f0 = (float)b0, f1 = (float)b1;
+            float low = fminf(f0, f1);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+            gs[0] = f0;
+            gs[1] = f1;
+            // 2^-b, or in its first place infinity: some query lies below kDeep
+            gs[C] = lane == 0 && low < kDeep ? INFINITY : ex2(-f0);
+            gs[C + 1] = ex2(-f1);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full + s, CF::TX);
+                uint8_t* st = stages + s * CF::STAGE;
+#pragma unroll
+                for (int bx = 0; bx < CF::NB; ++bx) {
+                    tma_load_3d(st + bx * CF::BOX, &mQ, full + s, bx * 64, row, bh);
+                    tma_load_3d(st + CF::OFF_K + bx * CF::KBOX, &mK, full + s, bx * 64, row, bh);
+                    tma_load_3d(st + CF::OFF_V + bx * CF::BOX, &mV, full + s, bx * 64, row, bh);
+                }
+            }
+            nld = ci + 1;
+            if (ci + 1 < nci) gr = load_gates(g, row + C, end, lane);
+        }
+        // drain: the loads still in flight land before the CTA exits
+        if (lane == 0)
+            for (int c2 = max(0, nld - CF::STAGES); c2 < nld; ++c2)
+                mbar_wait(full + c2 % CF::STAGES, (c2 / CF::STAGES) & 1, err, false);
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            const uint32_t idP = idesc_bf16(C, normalize ? C + 16 : C, false, false);  // P = Q [K; z]^T
+            constexpr uint32_t idS = idesc_bf16(D, D, true, true);    // S^T += V^T (w K)
+            constexpr uint32_t idO = idesc_bf16(D, C, false, false);  // O^T = S_prev^T Q^T
+            constexpr uint32_t idV = idesc_bf16(D, C, true, false);   // O^T += V^T P~^T
+            const uint32_t pta = smem_u32(pt), kwa = smem_u32(kw);
+            bool ok = true;
+            // O^T += V^T P~^T of chunk `ci`, issued after the next chunk's P and O^T
+            auto flush = [&](int ci) {
+                const int j = ci & 1;
+                ok = ok && mbar_wait(bptready + j, (ci >> 1) & 1, err);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t vt = smem_u32(stages + (ci % CF::STAGES) * CF::STAGE) + CF::OFF_V;
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    mma_bf16(tmem + CF::COL_O + j * C, sdesc(vt + kk * 2048, CF::BOX, 1024),
+                             sdesc(pta + j * CF::PT + kk * 32, 16, 1024), idV, 1u);
+                mma_commit(bofull + j);
+                mma_commit(empty + ci % CF::STAGES);
+            };
+            for (int ci = 0; ci < nci && ok; ++ci) {
+                const int s = ci % CF::STAGES, j = ci & 1, k = ci >> 1;
+                const uint32_t qt = smem_u32(stages + s * CF::STAGE);
+                const uint32_t kt = qt + CF::OFF_K, vt = qt + CF::OFF_V;
+                ok = mbar_wait(bprep, ci & 1, err);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk) {
+                    const uint64_t a = sdesc(vt + kk * 2048, CF::BOX, 1024);
+                    mma_bf16(tmem + CF::COL_S, a, sdesc(kwa + CF::TILE + kk * 2048, CF::BOX, 1024), idS, 1u);
+                    mma_bf16(tmem + CF::COL_S, a, sdesc(kwa + kk * 2048, CF::BOX, 1024), idS, 1u);
+                }
+                mma_commit(bsdone);
+                // P[j] was read two chunks ago (that chunk's P~ was waited for in its flush)
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_bf16(tmem + CF::COL_P + j * (16u << 16), sdesc(qt + (kk / 4) * CF::BOX + (kk % 4) * 32, 16, 1024),
+                             sdesc(kt + (kk / 4) * CF::KBOX + (kk % 4) * 32, 16, 1024), idP, kk > 0);
+                mma_commit(bpfull + j);
+                if (k > 0) ok = mbar_wait(bofree + j, (k - 1) & 1, err);  // O^T[j] read two chunks ago
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sb = tmem + CF::COL_SB + j * 64;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_bf16_ts(tmem + CF::COL_O + j * C, sb + kk * 8,
+                                sdesc(qt + (kk / 4) * CF::BOX + (kk % 4) * 32, 16, 1024), idO, kk > 0);
+                if (ci > 0) flush(ci - 1);
+            }
+            if (ok) flush(nci - 1);
+        }
+    } else if (warp < 10) {
+        // ---------------- prep warps ----------------
+        const int et = threadIdx.x - 64, wq = warp - 2, sp = warp & 3, half = wq / 4;
+        const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
+        const int a = sp * 32 + lane;  // the S^T row (d_v) of this thread; its columns: half
+        const float *pS = nullptr, *pz = nullptr;
+        if (prefix) {
+            pS = prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D);
+            pz = pS + D * D;
+        } else if (S_in) {
+            pS = S_in + (size_t)bh * D * D;
+            pz = z_in + (size_t)bh * D;
+        }
+        // rows 66..79 of every extended K box stay zero (TMA writes rows 0..63)
+        for (int x = et; x < CF::STAGES * CF::NB * 14 * 8; x += CF::PREP) {
+            const int s = x / (CF::NB * 112), bx = (x / 112) % CF::NB, r = 66 + (x % 112) / 8, q16 = x % 8;
+            *reinterpret_cast<uint4*>(stages + s * CF::STAGE + CF::OFF_K + bx * CF::KBOX + r * 128 + q16 * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll 1
+        for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 16) {
+            uint32_t r[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = pS ? __float_as_uint(pS[(size_t)(c0 + e) * D + a]) : 0u;
+            tmem_st16(tmem + CF::COL_S + lane_base + c0, r);
+        }
+        tmem_st_wait();
+        float zp = pz && et < D ? pz[et] : 0.f;  // z_prev[d_k = et]
+        const int g = (lane & 7) ^ ((et >> 3) & 7);  // column group (of 8) of this thread's 16-byte chunks
+        for (int ci = 0; ci < nci; ++ci) {
+            const int s = ci % CF::STAGES, u = ci / CF::STAGES;
+            const int kvalid = min(C, end - first - ci * C);
+            uint8_t* st = stages + s * CF::STAGE;
+            uint8_t* kt = st + CF::OFF_K;
+            mbar_wait(full + s, u & 1, err);
+            const float* gs = gates + s * 2 * C;
+            const float blast = gs[C - 1], all = ex2(blast);
+            if (normalize && et < D) {
+                const __nv_bfloat16 hi = __float2bfloat16_rn(zp);
+                const __nv_bfloat16 lo = __float2bfloat16_rn(zp - __bfloat162float(hi));
+                uint8_t* kb = kt + (et / 64) * CF::KBOX;
+                *reinterpret_cast<__nv_bfloat16*>(kb + sw128_off(C, et % 64)) = hi;
+                *reinterpret_cast<__nv_bfloat16*>(kb + sw128_off(C + 1, et % 64)) = lo;
+            }
+            if (mapped) {
+#pragma unroll
+                for (int bx = 0; bx < CF::NB; ++bx)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint4* qp = reinterpret_cast<uint4*>(st + bx * CF::BOX + (et + 256 * i) * 16);
+                        *qp = phi8<PHI>(*qp);
+                    }
+            }
+            // the previous chunk's S^T update has read w phi(K) and left S^T
+            if (ci > 0) {
+                mbar_wait(bsdone, (ci - 1) & 1, err);
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int bx = 0; bx < CF::NB; ++bx) {
+                float cs[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) cs[e] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int p = et + 256 * i, r = p >> 3;  // 16-byte chunk within the box, its token
+                    uint4* kp = reinterpret_cast<uint4*>(kt + bx * CF::KBOX + p * 16);
+                    const uint4 x = *kp;
+                    const float w = r < kvalid ? ex2(blast - gs[r]) : 0.f;
+                    float f[8];
+                    uint4 hi, lo;
+                    weighted8<PHI>(x, w, f, hi, lo);
+                    *reinterpret_cast<uint4*>(kw + bx * CF::BOX + p * 16) = hi;
+                    *reinterpret_cast<uint4*>(kw + CF::TILE + bx * CF::BOX + p * 16) = lo;
+                    if (mapped) *kp = phi8<PHI>(x);  // rows past the end are masked in P~
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) cs[e] += f[e];
+                }
+                if (normalize) {
+                    // lanes l, l^9, l^18, l^27 hold the same column group g
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        cs[e] += __shfl_xor_sync(0xffffffffu, cs[e], 9);
+                        cs[e] += __shfl_xor_sync(0xffffffffu, cs[e], 18);
+                    }
+                    if (lane < 8) {
+                        float4* dst = reinterpret_cast<float4*>(red + wq * D + bx * 64 + g * 8);
+                        dst[0] = make_float4(cs[0], cs[1], cs[2], cs[3]);
+                        dst[1] = make_float4(cs[4], cs[5], cs[6], cs[7]);
+                    }
+                }
+            }
+            // S_prev^T -> bf16 pairs, and scaled in place for this chunk's update
+            const uint32_t sb = tmem + CF::COL_SB + (ci & 1) * 64 + lane_base + half * 32;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t col = tmem + CF::COL_S + lane_base + half * 64 + 32 * h;
+                uint32_t r[32];
+                tmem_ld16(col, *reinterpret_cast<uint32_t(*)[16]>(r));
+                tmem_ld16(col + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+                tmem_ld_wait();
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                tmem_st16(sb + 16 * h, w);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * all);
+                tmem_st16(col, *reinterpret_cast<uint32_t(*)[16]>(r));
+                tmem_st16(col + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+            }
+            tmem_st_wait();
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(bprep);
+            if (normalize) {
+                named_bar(2, CF::PREP);
+                if (et < D) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) sum += red[x * D + et];
+                    zp = fmaf(zp, all, sum);
+                }
+                named_bar(2, CF::PREP);  // red is written again for the next chunk
+            }
+        }
+    } else {
+        // ---------------- mask + epilogue warps ----------------
+        const int sp = warp & 3;
+        const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
+        const int i = sp * 16 + (lane & 15);  // P row (query) of this thread: M = 64 layout
+        const int half = lane >= 16 ? 1 : 0;  // the two warp halves take the two column halves
+        const int et2 = threadIdx.x - 64 - CF::PREP;
+        bool ok = true;  // no early exit (named barrier 3); a failed wait only suppresses the stores
+        for (int ci = 0; ci < nci; ++ci) {
+            const int slot = ci & 1, use = ci >> 1;
+            const uint32_t lane_s = lane_base + static_cast<uint32_t>(slot) * (16u << 16);
+            uint8_t* pts = pt + slot * CF::PT;
+            ok = mbar_wait(bpfull + slot, use & 1, err) && ok;
+            // the gates came with the chunk's tiles, which P has waited for
+            mbar_wait(full + ci % CF::STAGES, (ci / CF::STAGES) & 1, err);
+            tc_fence_after();
+            const float* gs = gates + (ci % CF::STAGES) * 2 * C;
+            const float bi = gs[i];
+            const bool deep = isinf(gs[C]);  // some query of the chunk lies below kDeep
+            const float own = bi - fmaxf(bi, kDeep);
+            uint32_t r[32];
+            tmem_ld16x2<32>(tmem + CF::COL_P + lane_s, *reinterpret_cast<uint32_t(*)[16]>(r));
+            tmem_ld16x2<32>(tmem + CF::COL_P + lane_s + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+            uint32_t zq = 0;
+            if (normalize) tmem_ld1x2<1>(tmem + CF::COL_P + lane_s + C, zq);
+            tmem_ld_wait();
+            float rs = 0.f;
+#pragma unroll
+            for (int gq = 0; gq < 4; ++gq) {
+                float f[8];
+                const int j0 = 32 * half + 8 * gq;
+                if (!deep) {
+                    const float4 x = *reinterpret_cast<const float4*>(gs + C + j0);
+                    const float4 y = *reinterpret_cast<const float4*>(gs + C + j0 + 4);
+                    const float e8[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = j0 + e <= i ? __uint_as_float(r[8 * gq + e]) * e8[e] : 0.f;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        f[e] = j0 + e <= i ? __uint_as_float(r[8 * gq + e]) * ex2(own - gs[j0 + e]) : 0.f;
+                }
+                const uint4 w = pack8(f);
+                *reinterpret_cast<uint4*>(pts + sw128_off(i, j0)) = w;
+                // the denominator sums the rounded weights: the output is a mean with these very weights
+                unpack8(w, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) rs += f[e];
+            }
+            if (normalize) {
+                rs += __shfl_xor_sync(0xffffffffu, rs, 16);
+                float qz = __uint_as_float(zq);  // phi(Q_i).z_hi (lanes < 16), .z_lo (lanes >= 16)
+                qz += __shfl_xor_sync(0xffffffffu, qz, 16);
+                if (lane < 16) inv[i] = __frcp_rn(rs + qz);
+            } else if (lane < 16) {
+                inv[i] = ex2(fmaxf(bi, kDeep));
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(bptready + slot);
+            // epilogue: this thread's d_v column of the chunk's output rows
+            ok = ok && mbar_wait(bofull + slot, use & 1, err);
+            tc_fence_after();
+            if (et2 == 0) bulk_wait_read0();  // the previous chunk's store has read stg
+            named_bar(3, 128);                // also: inv[] is written
+            const int mi = lane >> 3, mj = lane & 7;
+            const int q2 = 2 * (lane & 3);
+            const uint32_t stg_u = smem_u32(stg);
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl) {
+                const int a0 = sp * 32 + 16 * hl;
+                uint32_t o[32];
+                tmem_ld16x256_x8(tmem + CF::COL_O + slot * C + (static_cast<uint32_t>(a0) << 16), o);
+                tmem_ld_wait();
+                if (hl == 1) {
+                    tc_fence_before();
+                    mbar_arrive(bofree + slot);  // O^T[slot] read
+                }
+                const uint32_t box = stg_u + (a0 / 64) * CF::BOX;
+                const int ch = (a0 % 64) / 8 + (mi & 1);
+#pragma unroll
+                for (int cb = 0; cb < C; cb += 16) {
+                    const float2 i0 = *reinterpret_cast<const float2*>(inv + cb + q2);
+                    const float2 i1 = *reinterpret_cast<const float2*>(inv + cb + 8 + q2);
+                    const uint32_t* x = o + (cb / 8) * 4;
+                    const uint32_t p0 = pack_bf16(__uint_as_float(x[0]) * i0.x, __uint_as_float(x[1]) * i0.y);
+                    const uint32_t p1 = pack_bf16(__uint_as_float(x[2]) * i0.x, __uint_as_float(x[3]) * i0.y);
+                    const uint32_t p2 = pack_bf16(__uint_as_float(x[4]) * i1.x, __uint_as_float(x[5]) * i1.y);
+                    const uint32_t p3 = pack_bf16(__uint_as_float(x[6]) * i1.x, __uint_as_float(x[7]) * i1.y);
+                    const uint32_t row = cb + 8 * (mi >> 1) + mj;
+                    stmatrix_x4_trans(box + row * 128u + ((static_cast<uint32_t>(ch) ^ (row & 7u)) << 4), p0, p1, p2, p3);
+                }
+            }
+            fence_async_smem();
+            named_bar(3, 128);
+            if (et2 == 0 && ok) {
+#pragma unroll
+                for (int bx = 0; bx < CF::NB; ++bx) tma_store_3d(&mOut, stg + bx * CF::BOX, bx * 64, first + ci * C, bh);
+                bulk_commit();
+            }
+        }
+        if (et2 == 0) bulk_wait0();  // the output stores have landed
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int PHI>
+cudaError_t launch_state(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
+                         int count, float* part, float* dec, uint32_t* err, cudaStream_t st) {
+    using CF = GsCfg;
+    CUtensorMap mk, mv;
+    cudaError_t e = make_map(&mk, k, CF::D, p.N, p.bh(), CF::C);
+    if (e == cudaSuccess) e = make_map(&mv, v, CF::D, p.N, p.bh(), CF::C);
+    if (e == cudaSuccess) e = ensure_smem<tc_gated_state_kernel<PHI>>(CF::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(tc_gated_state_kernel<PHI>, dim3((unsigned)count, (unsigned)p.bh()), dim3(CF::THREADS), CF::SMEM, st,
+                      mk, mv, static_cast<const __nv_bfloat16*>(g), p.N, block_tokens, nblk, part, dec, err);
+}
+
+template <int PHI>
+cudaError_t launch_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g, const float* prefix,
+                         const float* S_in, const float* z_in, int block_tokens, int nblk, void* out, uint32_t* err,
+                         cudaStream_t st) {
+    using CF = GtCfg;
+    CUtensorMap mq, mk, mv, mo;
+    cudaError_t e = make_map(&mq, q, CF::D, p.N, p.bh(), CF::C);
+    if (e == cudaSuccess) e = make_map(&mk, k, CF::D, p.N, p.bh(), CF::C);
+    if (e == cudaSuccess) e = make_map(&mv, v, CF::D, p.N, p.bh(), CF::C);
+    if (e == cudaSuccess) e = make_map(&mo, out, CF::D, p.N, p.bh(), CF::C);
+    if (e == cudaSuccess) e = ensure_smem<tc_gated_sweep_kernel<PHI>>(CF::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(tc_gated_sweep_kernel<PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(CF::THREADS), CF::SMEM, st,
+                      mq, mk, mv, mo, static_cast<const __nv_bfloat16*>(g), prefix, S_in, z_in, p.N, block_tokens, nblk,
+                      p.normalize, err);
+}
+
+}  // namespace
+
+bool tc_gated_supported(const Problem& p) { return p.dtype == DT_BF16 && p.d == 128; }
+
+cudaError_t tc_gated_states(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
+                            int count, float* part, float* dec, uint32_t* err, cudaStream_t st) {
+    auto* f = p.phi == PHI_RELU1  ? launch_state<PHI_RELU1>
+              : p.phi == PHI_ELU1 ? launch_state<PHI_ELU1>
+                                  : launch_state<PHI_IDENTITY>;
+    return f(p, k, v, g, block_tokens, nblk, count, part, dec, err, st);
+}
+
+cudaError_t tc_gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g,
+                           const float* prefix, const float* S_in, const float* z_in, int block_tokens, int nblk, void* out,
+                           uint32_t* err, cudaStream_t st) {
+    auto* f = p.phi == PHI_RELU1  ? launch_sweep<PHI_RELU1>
+              : p.phi == PHI_ELU1 ? launch_sweep<PHI_ELU1>
+                                  : launch_sweep<PHI_IDENTITY>;
+    return f(p, q, k, v, g, prefix, S_in, z_in, block_tokens, nblk, out, err, st);
+}
+
+}  // namespace la

@@ -156,10 +156,10 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     const float* rec = prefix ? prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
     st.seed(rec, rec + D * D, warp, lane);
     st.template publish<LO>(sm.sop[0][0], sm.zs[0], warp, lane, sm.sop[0][BQ::PARTS - 1]);
-    GateRegs<C> gr;
+    GateRegs<T, C> gr;
     if (warp == 0) {
         load_gates<T, C>(gr, gate, nullptr, nullptr, first, N, lane);
-        scan_gates<C>(sm.gates[0], gr, end - first, lane);
+        scan_gates<T, C>(sm.gates[0], gr, end - first, lane);
     }
     const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
     const int i0 = rg * 16, col0 = cg * SH::NCOL;
@@ -403,7 +403,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             if (BQ::COPIES == 1) __syncthreads();  // every warp has read the operand
             const int nb = BQ::COPIES == 2 ? ((c + 1) & 1) : 0;
             st.template publish<LO>(sm.sop[nb][0], sm.zs[nb], warp, lane, sm.sop[nb][BQ::PARTS - 1]);
-            if (warp == 0) scan_gates<C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
+            if (warp == 0) scan_gates<T, C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
         }
     }
     __syncthreads();
@@ -448,10 +448,10 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     const float* rec = suffix ? suffix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
     st.seed(rec, rec + D * D, warp, lane);
     st.publish(sm.sop[0][0], sm.zs[0], warp, lane);
-    GateRegs<C> gr;
+    GateRegs<T, C> gr;
     auto scan = [&](int s) {
         Gates<C>& gs = sm.gates[s & 1];
-        scan_gates<C>(gs, gr, end - first - (nch - 1 - s) * C, lane);
+        scan_gates<T, C>(gs, gr, end - first - (nch - 1 - s) * C, lane);
 #pragma unroll
         for (int e = 0; e < C / 32; ++e) {
             const int i = lane * (C / 32) + e;

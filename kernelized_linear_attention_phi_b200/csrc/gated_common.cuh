@@ -48,28 +48,48 @@ template <int C> struct alignas(16) Gates {
 constexpr double kLog2e = 1.4426950408889634;
 constexpr double kClosed = -14000.0;
 
-// One lane's gates of a chunk, held from the load to the scan.
-template <int C> struct GateRegs { float g[C / 32], up[C / 32], col[C / 32]; };
+// One lane's gates of a chunk, held from the load to the scan as they were
+// loaded (converting them at once would wait for the load).
+__device__ __forceinline__ uint32_t load_raw(const float* p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint16_t load_raw(const __nv_bfloat16* p) {
+    uint16_t r;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ float raw_f32(uint32_t r) { return __uint_as_float(r); }
+__device__ __forceinline__ float raw_f32(uint16_t r) { return __uint_as_float((uint32_t)r << 16); }
+template <typename T, int C> struct GateRegs {
+    decltype(load_raw(static_cast<const T*>(nullptr))) g[C / 32];
+    float up[C / 32], col[C / 32];
+};
 template <typename T, int C>
-__device__ __forceinline__ void load_gates(GateRegs<C>& r, const T* g, const float* up, const float* col, int row0, int N,
+__device__ __forceinline__ void load_gates(GateRegs<T, C>& r, const T* g, const float* up, const float* col, int row0, int N,
                                            int lane) {
 #pragma unroll
     for (int e = 0; e < C / 32; ++e) {
         const int i = row0 + lane * (C / 32) + e;
-        const bool in = i < N;
-        r.g[e] = in ? to_f32<T>(g[i]) : 0.f;
-        r.up[e] = in ? (up ? up[i] : 1.f) : 0.f;
-        r.col[e] = in && col ? col[i] : 0.f;
+        r.g[e] = 0;
+        r.up[e] = r.col[e] = 0.f;
+        if (i < N) {
+            r.g[e] = load_raw(g + i);
+            r.up[e] = 1.f;
+            if (up) r.up[e] = up[i];
+            if (col) r.col[e] = col[i];
+        }
     }
 }
 // A whole warp. Returns the chunk's log2 sum (every lane).
-template <int C>
-__device__ __forceinline__ double scan_gates(Gates<C>& s, const GateRegs<C>& r, int valid, int lane) {
+template <typename T, int C>
+__device__ __forceinline__ double scan_gates(Gates<C>& s, const GateRegs<T, C>& r, int valid, int lane) {
     constexpr int R = C / 32;
     double x[R];
 #pragma unroll
     for (int e = 0; e < R; ++e) {
-        const double l = (double)r.g[e] * kLog2e;
+        const double l = (double)raw_f32(r.g[e]) * kLog2e;
         x[e] = l < kClosed ? kClosed : l;  // a NaN stays
         if (e) x[e] += x[e - 1];
     }

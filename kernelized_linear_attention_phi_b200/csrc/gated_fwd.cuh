@@ -65,10 +65,10 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         st.seed(S_in ? S_in + (size_t)bh * D * D : nullptr, z_in ? z_in + (size_t)bh * D : nullptr, warp, lane);
     }
     st.publish(sm.sop[0], sm.zs[0], warp, lane);
-    GateRegs<C> gr;
+    GateRegs<T, C> gr;
     if (warp == 0) {
         load_gates<T, C>(gr, gate, nullptr, nullptr, first, N, lane);
-        scan_gates<C>(sm.gates[0], gr, end - first, lane);
+        scan_gates<T, C>(sm.gates[0], gr, end - first, lane);
     }
     // the warps' row groups differ in work (a group sees the keys before it):
     // CTAs of an SM start them at different warps
@@ -180,7 +180,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             if (c + 1 < nch) {
                 const int nb = SH::SB == 2 ? ((c + 1) & 1) : 0;
                 st.publish(sm.sop[nb], sm.zs[nb], warp, lane);
-                if (warp == 0) scan_gates<C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
+                if (warp == 0) scan_gates<T, C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
             }
         }
     }
@@ -222,11 +222,11 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __
     st.seed(nullptr, nullptr, warp, lane);
     // the gates: one warp (the last, which has the least to do when S has fewer row tiles than warps)
     constexpr int GW = SH::NW - 1;
-    GateRegs<C> gr;
+    GateRegs<T, C> gr;
     double total = 0.0;
     auto scan = [&](int c) {
         Gates<C>& s = sm.gates[c & 1];
-        total += scan_gates<C>(s, gr, end - first - chunk(c) * C, lane);
+        total += scan_gates<T, C>(s, gr, end - first - chunk(c) * C, lane);
         if (REVERSE) {
 #pragma unroll
             for (int e = 0; e < C / 32; ++e) {

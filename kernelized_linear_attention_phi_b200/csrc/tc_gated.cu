@@ -70,7 +70,7 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
         cta_abort_reset();
         for (int s = 0; s < CF::STAGES; ++s) {
             mbar_init(full + s, 1);
-            mbar_init(tdone + s, 256);
+            mbar_init(tdone + s, 8);
             mbar_init(empty + s, 1);
         }
         mbar_init(acc, 1);
@@ -90,19 +90,21 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     if (warp == 0) {
         const __nv_bfloat16* g = gate + (size_t)bh * N;
         double after = 0.0;  // log2 of the gates behind the chunk, within the block
-        float2 gr = load_gates(g, first + (nci - 1) * C, end, lane);
+        Gates2 gr = load_gates(g, first + (nci - 1) * C, end, lane);
         int issued = 0;
+#pragma unroll 1
         for (int i = 0; i < nci; ++i) {
             const int s = i % CF::STAGES, u = i / CF::STAGES, row = first + (nci - 1 - i) * C;
-            if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(empty + s, (u - 1) & 1, err))) break;
             double b0, b1;
             const double last = scan_gates(gr, lane, b0, b1);
+            if (i + 1 < nci) gr = load_gates(g, row - C, end, lane);
+            if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(empty + s, (u - 1) & 1, err))) break;
             float* w = wts + s * C + 2 * lane;
             w[0] = row + 2 * lane < end ? ex2((float)(after + (last - b0))) : 0.f;
             w[1] = row + 2 * lane + 1 < end ? ex2((float)(after + (last - b1))) : 0.f;
             after += last;
             __syncwarp();
-            if (lane == 0) {
+            if (elect_one()) {
                 mbar_arrive_expect_tx(full + s, CF::STAGE);
                 uint8_t* st = stages + s * CF::STAGE;
 #pragma unroll
@@ -111,8 +113,8 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                     tma_load_3d(st + CF::TILE + bx * CF::BOX, &mV, full + s, bx * 64, row, bh);
                 }
             }
+            __syncwarp();
             issued = i + 1;
-            if (i + 1 < nci) gr = load_gates(g, row - C, end, lane);
         }
         if (lane == 0) {
             dec[(size_t)bh * nblk + blk] = ex2((float)after);
@@ -120,24 +122,27 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                 mbar_wait(full + i % CF::STAGES, (i / CF::STAGES) & 1, err, false);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t id = idesc_bf16(D, D, true, true);
-            bool ok = true;
-            for (int i = 0; i < nci && ok; ++i) {
-                const int s = i % CF::STAGES, f = i / CF::FLUSH;
-                if (!(ok = mbar_wait(tdone + s, (i / CF::STAGES) & 1, err))) break;
-                tc_fence_after();
-                const uint32_t kt = smem_u32(stages + s * CF::STAGE), vt = kt + CF::TILE;
-                const uint32_t lt = smem_u32(lo + (i & 1) * CF::TILE), d = tmem + (f & 1) * D;
+        constexpr uint32_t id = idesc_bf16(D, D, true, true);
+        const uint64_t kd = sdesc(smem_u32(stages), CF::BOX, 1024), ld = sdesc(smem_u32(lo), CF::BOX, 1024);
+#pragma unroll 1
+        for (int i = 0; i < nci; ++i) {
+            const int s = i % CF::STAGES, f = i / CF::FLUSH;
+            if (!__all_sync(0xffffffffu, mbar_wait(tdone + s, (i / CF::STAGES) & 1, err))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t k0 = kd + s * (CF::STAGE >> 4), v0 = k0 + (CF::TILE >> 4), l0 = ld + (i & 1) * (CF::TILE >> 4);
+                const uint32_t d = tmem + (f & 1) * D;
+                uint32_t add = i % CF::FLUSH > 0 ? 1u : 0u;
 #pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk) {
-                    const uint64_t b = sdesc(vt + kk * 2048, CF::BOX, 1024);
-                    mma_bf16(d, sdesc(lt + kk * 2048, CF::BOX, 1024), b, id, (i % CF::FLUSH > 0 || kk > 0) ? 1u : 0u);
-                    mma_bf16(d, sdesc(kt + kk * 2048, CF::BOX, 1024), b, id, 1u);
+                for (int kk = 0; kk < C / 16; ++kk) {  // 16 tokens: 16 rows of 128 bytes
+                    mma_bf16(d, l0 + kk * 128, v0 + kk * 128, id, add);
+                    add = 1u;
+                    mma_bf16(d, k0 + kk * 128, v0 + kk * 128, id, 1u);
                 }
                 mma_commit(empty + s);
                 if (i + 1 == nci || (i + 1) % CF::FLUSH == 0) mma_commit(acc + (f & 1));
             }
+            __syncwarp();
         }
     } else {
         const int et = threadIdx.x - 64, wq = warp - 2, sp = warp & 3, half = wq / 4;
@@ -165,10 +170,12 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
             }
             tc_fence_before();
         };
-        for (int i = 0; i < nci; ++i) {
+#pragma unroll 1
+        for (int i = 0;; ++i) {
             const int s = i % CF::STAGES, u = i / CF::STAGES;
-            // accumulator f is taken during the first chunk of flush f + 1
-            if (i > 0 && i % CF::FLUSH == 0) take(i / CF::FLUSH - 1);
+            // accumulator f is taken during the first chunk of flush f + 1, or at the end
+            if (i > 0 && (i == nci || i % CF::FLUSH == 0)) take((i - 1) / CF::FLUSH);
+            if (i == nci) break;
             mbar_wait(full + s, u & 1, err);
             // the low part's buffer: chunk i - 2's products have read it
             if (i >= 2) mbar_wait(empty + (i - 2) % CF::STAGES, ((i - 2) / CF::STAGES) & 1, err);
@@ -182,8 +189,8 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                     const int p = et + 256 * j;
                     uint4* kp = reinterpret_cast<uint4*>(kt + bx * CF::BOX + p * 16);
                     float f[8];
-                    uint4 hi, rest;
-                    weighted8<PHI>(*kp, w[p >> 3], f, hi, rest);
+                    uint4 phi, hi, rest;
+                    weighted8<PHI>(*kp, w[p >> 3], f, phi, hi, rest);
                     *kp = hi;
                     *reinterpret_cast<uint4*>(lt + bx * CF::BOX + p * 16) = rest;
 #pragma unroll
@@ -191,9 +198,8 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                 }
             fence_async_smem();
             tc_fence_before();
-            mbar_arrive(tdone + s);
+            warp_arrive(tdone + s, lane);
         }
-        take((nci - 1) / CF::FLUSH);
         float* rec = part + ((size_t)bh * nblk + blk) * (size_t)(D * D + D);
 #pragma unroll
         for (int bx = 0; bx < CF::NB; ++bx) {
@@ -230,27 +236,34 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
 // ---------------------------------------------------------------------------
 // Sweep
 // ---------------------------------------------------------------------------
+// Warp roles (576 threads): warp 0 TMA and gates, warp 1 MMA and TMEM, warps
+// 2..9 "transform" (phi on Q and K, w phi(K) in two parts, z), warps 10..13
+// "state" (S^T: the bf16 operand, and its decay in place), warps 14..17 "mask"
+// (P~, denominators, epilogue). The transforms run a chunk ahead: the loop
+// from one S^T update to the next holds only the state warps' pass over S^T
+// and that update's products.
 struct GtCfg {
     static constexpr int D = 128, C = 64, NB = 2;
     static constexpr int BOX = C * 128;            // one 64-row x 64-column box (8 KB)
     static constexpr int KBOX = (C + 16) * 128;    // K box + 16 rows (z_hi, z_lo, zeros)
     static constexpr int TILE = NB * BOX;
-    static constexpr int OFF_K = TILE, OFF_V = OFF_K + NB * KBOX, STAGE = OFF_V + TILE;
-    static constexpr uint32_t TX = 3 * TILE;
-    static constexpr int STAGES = 3;
+    static constexpr int QK = TILE + NB * KBOX;    // Q, K' of a chunk: two slots, free after its P and O^T
+    static constexpr int VS = 3;                   // V slots: free after its O^T += V^T P~^T, a chunk later
+    static constexpr int GS = 4;                   // gate slots [b | 2^-b]
     static constexpr int PT = C * C * 2;           // P~ [query][key], K-major (x2)
     static constexpr int STG = TILE;               // output staging tile
-    static constexpr int KW = 2 * TILE;            // w phi(K), high and low part
+    static constexpr int KW = 2 * TILE;            // w phi(K), high and low part (x2)
     static constexpr int RED = 8 * D * 4;          // column-sum partials [warp][d_k]
     static constexpr int INV = C * 4;              // output scale per query row
-    static constexpr int GATES = STAGES * 2 * C * 4;  // [stage][b | 2^-b]
-    static constexpr int NBAR = 2 * STAGES + 2 + 4 * 2;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 2 * PT + STG + KW + RED + INV + GATES + 8 * NBAR + 16;
+    static constexpr int GATES = GS * 2 * C * 4;
+    static constexpr int NBAR = 2 + 2 + 2 * VS + GS + 2 + 2 + 2 + 4 * 2;
+    static constexpr size_t SMEM = 1024 + 2 * (size_t)QK + VS * TILE + 2 * PT + STG + 2 * KW + RED + INV + GATES +
+                                   8 * NBAR + 16;
     // TMEM columns, as in tc_sweep_t.cu
     static constexpr int COL_S = 0, COL_SB = 128, COL_P = 256, COL_O = 384;
-    static constexpr int PREP = 256, THREADS = 64 + PREP + 128;
+    static constexpr int TRANSFORM = 256, STATE = 128, MASK = 128, THREADS = 64 + TRANSFORM + STATE + MASK;
     static_assert(SMEM + 16 <= 227 * 1024, "shared memory (16 bytes static)");
-    static_assert(STAGE % 1024 == 0 && KBOX % 1024 == 0, "1024-byte aligned operand tiles");
+    static_assert(QK % 1024 == 0 && KBOX % 1024 == 0, "1024-byte aligned operand tiles");
 };
 
 template <int PHI>
@@ -263,18 +276,24 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     using CF = GtCfg;
     constexpr int D = CF::D, C = CF::C;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* stages = align1024(smem_raw);
-    uint8_t* pt = stages + CF::STAGES * CF::STAGE;
+    uint8_t* qks = align1024(smem_raw);
+    uint8_t* vs = qks + 2 * CF::QK;
+    uint8_t* pt = vs + CF::VS * CF::TILE;
     uint8_t* stg = pt + 2 * CF::PT;
-    uint8_t* kw = stg + CF::STG;
-    float* red = reinterpret_cast<float*>(kw + CF::KW);
+    uint8_t* kws = stg + CF::STG;
+    float* red = reinterpret_cast<float*>(kws + 2 * CF::KW);
     float* inv = red + 8 * D;
     float* gates = inv + C;
-    uint64_t* full = reinterpret_cast<uint64_t*>(gates + CF::STAGES * 2 * C);
-    uint64_t* empty = full + CF::STAGES;
-    uint64_t* bprep = empty + CF::STAGES;  // K', Q, w phi(K) and S_prev^T ready
-    uint64_t* bsdone = bprep + 1;          // S^T update of the chunk done
-    uint64_t* bpfull = bsdone + 1;         // per slot (chunk % 2): P ready, P~ written, O^T ready, O^T read
+    uint64_t* fullqk = reinterpret_cast<uint64_t*>(gates + CF::GS * 2 * C);
+    uint64_t* emptyqk = fullqk + 2;
+    uint64_t* fullv = emptyqk + 2;
+    uint64_t* emptyv = fullv + CF::VS;
+    uint64_t* gfull = emptyv + CF::VS;     // gates of a chunk written
+    uint64_t* bstate = gfull + CF::GS;     // S_prev^T operand written, S^T scaled
+    uint64_t* bsdone = bstate + 1;         // S^T update of the chunk done
+    uint64_t* btrans = bsdone + 1;         // per slot (chunk % 2): K', Q and w phi(K) written
+    uint64_t* kwfree = btrans + 2;         // w phi(K) read
+    uint64_t* bpfull = kwfree + 2;         // P ready, P~ written, O^T ready, O^T read
     uint64_t* bptready = bpfull + 2;
     uint64_t* bofull = bptready + 2;
     uint64_t* bofree = bofull + 2;
@@ -284,21 +303,25 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     const int blk = blockIdx.x, bh = blockIdx.y;
     const int first = blk * block_tokens, end = min(N, first + block_tokens);
     const int nci = (end - first + C - 1) / C;
-    constexpr bool mapped = PHI != PHI_IDENTITY;
 
     if (threadIdx.x == 0) {
         cta_abort_reset();
-        for (int s = 0; s < CF::STAGES; ++s) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, 1);
+        for (int j = 0; j < CF::VS; ++j) {
+            mbar_init(fullv + j, 1);
+            mbar_init(emptyv + j, 1);
         }
-        mbar_init(bprep, CF::PREP);
+        for (int j = 0; j < CF::GS; ++j) mbar_init(gfull + j, 1);
+        mbar_init(bstate, CF::STATE / 32);
         mbar_init(bsdone, 1);
         for (int j = 0; j < 2; ++j) {
+            mbar_init(fullqk + j, 1);
+            mbar_init(emptyqk + j, 1);
+            mbar_init(btrans + j, CF::TRANSFORM / 32);
+            mbar_init(kwfree + j, 1);
             mbar_init(bpfull + j, 1);
-            mbar_init(bptready + j, 128);
+            mbar_init(bptready + j, CF::MASK / 32);
             mbar_init(bofull + j, 1);
-            mbar_init(bofree + j, 128);
+            mbar_init(bofree + j, CF::MASK / 32);
         }
         fence_mbar_init();
         tma_prefetch_map(&mQ);
@@ -316,133 +339,151 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     if (warp == 0) {
         // ---------------- TMA producer and gates (whole warp) ----------------
         const __nv_bfloat16* g = gate + (size_t)bh * N;
-        float2 gr = load_gates(g, first, end, lane);
-        int nld = 0;
+        Gates2 gr = load_gates(g, first, end, lane);
+        int nqk = 0, nv = 0;
+#pragma unroll 1
         for (int ci = 0; ci < nci; ++ci) {
-            const int s = ci % CF::STAGES, u = ci / CF::STAGES, row = first + ci * C;
-            if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(empty + s, (u - 1) & 1, err))) break;
+            const int j = ci & 1, s = ci % CF::VS, row = first + ci * C;
             double b0, b1;
             scan_gates(gr, lane, b0, b1);
-            float* gs = gates + s * 2 * C + 2 * lane;
+            if (ci + 1 < nci) gr = load_gates(g, row + C, end, lane);
             const float f0 = (float)b0, f1 = (float)b1;
-            float low = fminf(f0, f1);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+            const bool low = __any_sync(0xffffffffu, fminf(f0, f1) < kDeep);
+            // chunk ci - 2's P and O^T are done, and with them (in order) all
+            // that chunk ci - 4 needed its gates for
+            if (ci >= 2 && !__all_sync(0xffffffffu, mbar_wait(emptyqk + j, ((ci >> 1) - 1) & 1, err))) break;
+            float* gs = gates + (ci % CF::GS) * 2 * C + 2 * lane;
             gs[0] = f0;
             gs[1] = f1;
             // 2^-b, or in its first place infinity: some query lies below kDeep
-            gs[C] = lane == 0 && low < kDeep ? INFINITY : ex2(-f0);
+            gs[C] = lane == 0 && low ? INFINITY : ex2(-f0);
             gs[C + 1] = ex2(-f1);
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive_expect_tx(full + s, CF::TX);
-                uint8_t* st = stages + s * CF::STAGE;
+            if (elect_one()) {
+                mbar_arrive(gfull + ci % CF::GS);
+                mbar_arrive_expect_tx(fullqk + j, 2 * CF::TILE);
+                uint8_t* st = qks + j * CF::QK;
 #pragma unroll
                 for (int bx = 0; bx < CF::NB; ++bx) {
-                    tma_load_3d(st + bx * CF::BOX, &mQ, full + s, bx * 64, row, bh);
-                    tma_load_3d(st + CF::OFF_K + bx * CF::KBOX, &mK, full + s, bx * 64, row, bh);
-                    tma_load_3d(st + CF::OFF_V + bx * CF::BOX, &mV, full + s, bx * 64, row, bh);
+                    tma_load_3d(st + CF::TILE + bx * CF::KBOX, &mK, fullqk + j, bx * 64, row, bh);
+                    tma_load_3d(st + bx * CF::BOX, &mQ, fullqk + j, bx * 64, row, bh);
                 }
             }
-            nld = ci + 1;
-            if (ci + 1 < nci) gr = load_gates(g, row + C, end, lane);
+            __syncwarp();
+            nqk = ci + 1;
+            if (ci >= CF::VS && !__all_sync(0xffffffffu, mbar_wait(emptyv + s, (ci / CF::VS - 1) & 1, err))) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(fullv + s, CF::TILE);
+#pragma unroll
+                for (int bx = 0; bx < CF::NB; ++bx)
+                    tma_load_3d(vs + s * CF::TILE + bx * CF::BOX, &mV, fullv + s, bx * 64, row, bh);
+            }
+            __syncwarp();
+            nv = ci + 1;
         }
         // drain: the loads still in flight land before the CTA exits
-        if (lane == 0)
-            for (int c2 = max(0, nld - CF::STAGES); c2 < nld; ++c2)
-                mbar_wait(full + c2 % CF::STAGES, (c2 / CF::STAGES) & 1, err, false);
-    } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
         if (lane == 0) {
-            const uint32_t idP = idesc_bf16(C, normalize ? C + 16 : C, false, false);  // P = Q [K; z]^T
-            constexpr uint32_t idS = idesc_bf16(D, D, true, true);    // S^T += V^T (w K)
-            constexpr uint32_t idO = idesc_bf16(D, C, false, false);  // O^T = S_prev^T Q^T
-            constexpr uint32_t idV = idesc_bf16(D, C, true, false);   // O^T += V^T P~^T
-            const uint32_t pta = smem_u32(pt), kwa = smem_u32(kw);
-            bool ok = true;
-            // O^T += V^T P~^T of chunk `ci`, issued after the next chunk's P and O^T
-            auto flush = [&](int ci) {
-                const int j = ci & 1;
-                ok = ok && mbar_wait(bptready + j, (ci >> 1) & 1, err);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t vt = smem_u32(stages + (ci % CF::STAGES) * CF::STAGE) + CF::OFF_V;
+            for (int c = max(0, nqk - 2); c < nqk; ++c) mbar_wait(fullqk + (c & 1), (c >> 1) & 1, err, false);
+            for (int c = max(0, nv - CF::VS); c < nv; ++c)
+                mbar_wait(fullv + c % CF::VS, (c / CF::VS) & 1, err, false);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (whole warp; one lane issues) ----------------
+        const uint32_t idP = idesc_bf16(C, normalize ? C + 16 : C, false, false);  // P = Q [K; z]^T
+        constexpr uint32_t idS = idesc_bf16(D, D, true, true);    // S^T += V^T (w K)
+        constexpr uint32_t idO = idesc_bf16(D, C, false, false);  // O^T = S_prev^T Q^T
+        constexpr uint32_t idV = idesc_bf16(D, C, true, false);   // O^T += V^T P~^T
+        const uint64_t dq0 = sdesc(smem_u32(qks), 16, 1024), dk0 = dq0 + (CF::TILE >> 4);
+        const uint64_t dv0 = sdesc(smem_u32(vs), CF::BOX, 1024), dw0 = sdesc(smem_u32(kws), CF::BOX, 1024);
+        const uint64_t dp0 = sdesc(smem_u32(pt), 16, 1024);
+        bool ok = true;
+        // O^T += V^T P~^T of chunk `ci`, issued after the next chunk's P and O^T
+        auto flush = [&](int ci) {
+            const int j = ci & 1;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bptready + j, (ci >> 1) & 1, err));
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t v = dv0 + (ci % CF::VS) * (CF::TILE >> 4), pp = dp0 + j * (CF::PT >> 4);
 #pragma unroll
                 for (int kk = 0; kk < C / 16; ++kk)
-                    mma_bf16(tmem + CF::COL_O + j * C, sdesc(vt + kk * 2048, CF::BOX, 1024),
-                             sdesc(pta + j * CF::PT + kk * 32, 16, 1024), idV, 1u);
+                    mma_bf16(tmem + CF::COL_O + j * C, v + kk * 128, pp + kk * 2, idV, 1u);
                 mma_commit(bofull + j);
-                mma_commit(empty + ci % CF::STAGES);
-            };
-            for (int ci = 0; ci < nci && ok; ++ci) {
-                const int s = ci % CF::STAGES, j = ci & 1, k = ci >> 1;
-                const uint32_t qt = smem_u32(stages + s * CF::STAGE);
-                const uint32_t kt = qt + CF::OFF_K, vt = qt + CF::OFF_V;
-                ok = mbar_wait(bprep, ci & 1, err);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk) {
-                    const uint64_t a = sdesc(vt + kk * 2048, CF::BOX, 1024);
-                    mma_bf16(tmem + CF::COL_S, a, sdesc(kwa + CF::TILE + kk * 2048, CF::BOX, 1024), idS, 1u);
-                    mma_bf16(tmem + CF::COL_S, a, sdesc(kwa + kk * 2048, CF::BOX, 1024), idS, 1u);
-                }
-                mma_commit(bsdone);
-                // P[j] was read two chunks ago (that chunk's P~ was waited for in its flush)
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16(tmem + CF::COL_P + j * (16u << 16), sdesc(qt + (kk / 4) * CF::BOX + (kk % 4) * 32, 16, 1024),
-                             sdesc(kt + (kk / 4) * CF::KBOX + (kk % 4) * 32, 16, 1024), idP, kk > 0);
-                mma_commit(bpfull + j);
-                if (k > 0) ok = mbar_wait(bofree + j, (k - 1) & 1, err);  // O^T[j] read two chunks ago
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sb = tmem + CF::COL_SB + j * 64;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_bf16_ts(tmem + CF::COL_O + j * C, sb + kk * 8,
-                                sdesc(qt + (kk / 4) * CF::BOX + (kk % 4) * 32, 16, 1024), idO, kk > 0);
-                if (ci > 0) flush(ci - 1);
+                mma_commit(emptyv + ci % CF::VS);
             }
-            if (ok) flush(nci - 1);
+            __syncwarp();
+        };
+#pragma unroll 1
+        for (int ci = 0; ci <= nci; ++ci) {
+            const int j = ci & 1, k = ci >> 1;
+            if (ci < nci) {
+                const uint64_t q = dq0 + j * (CF::QK >> 4), kd = dk0 + j * (CF::QK >> 4);
+                ok = mbar_wait(fullv + ci % CF::VS, (ci / CF::VS) & 1, err) && mbar_wait(btrans + j, k & 1, err) &&
+                     mbar_wait(bstate, ci & 1, err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t v = dv0 + (ci % CF::VS) * (CF::TILE >> 4), w = dw0 + j * (CF::KW >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < C / 16; ++kk) {
+                        mma_bf16(tmem + CF::COL_S, v + kk * 128, w + (CF::TILE >> 4) + kk * 128, idS, 1u);
+                        mma_bf16(tmem + CF::COL_S, v + kk * 128, w + kk * 128, idS, 1u);
+                    }
+                    mma_commit(bsdone);
+                    mma_commit(kwfree + j);
+                    // P[j] was read two chunks ago (that chunk's P~ was waited for in its flush)
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_bf16(tmem + CF::COL_P + j * (16u << 16), q + (kk / 4) * (CF::BOX >> 4) + (kk % 4) * 2,
+                                 kd + (kk / 4) * (CF::KBOX >> 4) + (kk % 4) * 2, idP, kk > 0);
+                    mma_commit(bpfull + j);
+                }
+                __syncwarp();
+                if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(bofree + j, (k - 1) & 1, err));  // O^T[j] read two chunks ago
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t sb = tmem + CF::COL_SB + j * 64;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_bf16_ts(tmem + CF::COL_O + j * C, sb + kk * 8, q + (kk / 4) * (CF::BOX >> 4) + (kk % 4) * 2, idO,
+                                    kk > 0);
+                    mma_commit(emptyqk + j);
+                }
+                __syncwarp();
+            }
+            if (ci > 0) flush(ci - 1);
         }
     } else if (warp < 10) {
-        // ---------------- prep warps ----------------
-        const int et = threadIdx.x - 64, wq = warp - 2, sp = warp & 3, half = wq / 4;
-        const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
-        const int a = sp * 32 + lane;  // the S^T row (d_v) of this thread; its columns: half
-        const float *pS = nullptr, *pz = nullptr;
-        if (prefix) {
-            pS = prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D);
-            pz = pS + D * D;
-        } else if (S_in) {
-            pS = S_in + (size_t)bh * D * D;
-            pz = z_in + (size_t)bh * D;
-        }
-        // rows 66..79 of every extended K box stay zero (TMA writes rows 0..63)
-        for (int x = et; x < CF::STAGES * CF::NB * 14 * 8; x += CF::PREP) {
+        // ---------------- transform warps ----------------
+        const int et = threadIdx.x - 64, wq = warp - 2;
+        const float* pz = prefix ? prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) + D * D
+                          : z_in ? z_in + (size_t)bh * D
+                                 : nullptr;
+        // rows 66..79 of both extended K boxes stay zero (TMA writes rows 0..63)
+        for (int x = et; x < 2 * CF::NB * 14 * 8; x += CF::TRANSFORM) {
             const int s = x / (CF::NB * 112), bx = (x / 112) % CF::NB, r = 66 + (x % 112) / 8, q16 = x % 8;
-            *reinterpret_cast<uint4*>(stages + s * CF::STAGE + CF::OFF_K + bx * CF::KBOX + r * 128 + q16 * 16) =
+            *reinterpret_cast<uint4*>(qks + s * CF::QK + CF::TILE + bx * CF::KBOX + r * 128 + q16 * 16) =
                 make_uint4(0, 0, 0, 0);
         }
-#pragma unroll 1
-        for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 16) {
-            uint32_t r[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = pS ? __float_as_uint(pS[(size_t)(c0 + e) * D + a]) : 0u;
-            tmem_st16(tmem + CF::COL_S + lane_base + c0, r);
-        }
-        tmem_st_wait();
         float zp = pz && et < D ? pz[et] : 0.f;  // z_prev[d_k = et]
         const int g = (lane & 7) ^ ((et >> 3) & 7);  // column group (of 8) of this thread's 16-byte chunks
         for (int ci = 0; ci < nci; ++ci) {
-            const int s = ci % CF::STAGES, u = ci / CF::STAGES;
+            const int j = ci & 1, k = ci >> 1;
             const int kvalid = min(C, end - first - ci * C);
-            uint8_t* st = stages + s * CF::STAGE;
-            uint8_t* kt = st + CF::OFF_K;
-            mbar_wait(full + s, u & 1, err);
-            const float* gs = gates + s * 2 * C;
-            const float blast = gs[C - 1], all = ex2(blast);
+            uint8_t* qt = qks + j * CF::QK;
+            uint8_t* kt = qt + CF::TILE;
+            uint8_t* kw = kws + j * CF::KW;
+            mbar_wait(fullqk + j, k & 1, err);
+            const float* gs = gates + (ci % CF::GS) * 2 * C;
+            const float blast = gs[C - 1];
+            float w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = (et >> 3) + 32 * i;
+                w[i] = r < kvalid ? ex2(blast - gs[r]) : 0.f;
+            }
             if (normalize && et < D) {
                 const __nv_bfloat16 hi = __float2bfloat16_rn(zp);
                 const __nv_bfloat16 lo = __float2bfloat16_rn(zp - __bfloat162float(hi));
@@ -450,37 +491,26 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                 *reinterpret_cast<__nv_bfloat16*>(kb + sw128_off(C, et % 64)) = hi;
                 *reinterpret_cast<__nv_bfloat16*>(kb + sw128_off(C + 1, et % 64)) = lo;
             }
-            if (mapped) {
-#pragma unroll
-                for (int bx = 0; bx < CF::NB; ++bx)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint4* qp = reinterpret_cast<uint4*>(st + bx * CF::BOX + (et + 256 * i) * 16);
-                        *qp = phi8<PHI>(*qp);
-                    }
-            }
-            // the previous chunk's S^T update has read w phi(K) and left S^T
-            if (ci > 0) {
-                mbar_wait(bsdone, (ci - 1) & 1, err);
-                tc_fence_after();
-            }
-#pragma unroll
+            if (k > 0) mbar_wait(kwfree + j, (k - 1) & 1, err);  // chunk ci - 2's update has read kw
+#pragma unroll 1
             for (int bx = 0; bx < CF::NB; ++bx) {
                 float cs[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) cs[e] = 0.f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int p = et + 256 * i, r = p >> 3;  // 16-byte chunk within the box, its token
+                    const int p = et + 256 * i;  // 16-byte chunk within the box (token (et >> 3) + 32 i)
                     uint4* kp = reinterpret_cast<uint4*>(kt + bx * CF::KBOX + p * 16);
-                    const uint4 x = *kp;
-                    const float w = r < kvalid ? ex2(blast - gs[r]) : 0.f;
                     float f[8];
-                    uint4 hi, lo;
-                    weighted8<PHI>(x, w, f, hi, lo);
+                    uint4 phi, hi, lo;
+                    weighted8<PHI>(*kp, w[i], f, phi, hi, lo);
                     *reinterpret_cast<uint4*>(kw + bx * CF::BOX + p * 16) = hi;
                     *reinterpret_cast<uint4*>(kw + CF::TILE + bx * CF::BOX + p * 16) = lo;
-                    if (mapped) *kp = phi8<PHI>(x);  // rows past the end are masked in P~
+                    if (PHI != PHI_IDENTITY) {  // rows past the end are masked in P~
+                        *kp = phi;
+                        uint4* qp = reinterpret_cast<uint4*>(qt + bx * CF::BOX + p * 16);
+                        *qp = phi_round8<PHI>(*qp);
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) cs[e] += f[e];
                 }
@@ -498,11 +528,48 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                     }
                 }
             }
-            // S_prev^T -> bf16 pairs, and scaled in place for this chunk's update
-            const uint32_t sb = tmem + CF::COL_SB + (ci & 1) * 64 + lane_base + half * 32;
+            fence_async_smem();
+            warp_arrive(btrans + j, lane);
+            if (normalize) {
+                const float all = ex2(blast);
+                named_bar(2, CF::TRANSFORM);
+                if (et < D) {
+                    float sum = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t col = tmem + CF::COL_S + lane_base + half * 64 + 32 * h;
+                    for (int x = 0; x < 8; ++x) sum += red[x * D + et];
+                    zp = fmaf(zp, all, sum);
+                }
+                named_bar(2, CF::TRANSFORM);  // red is written again for the next chunk
+            }
+        }
+    } else if (warp < 14) {
+        // ---------------- state warps ----------------
+        const int sp = warp & 3;
+        const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
+        const int a = sp * 32 + lane;  // the S^T row (d_v) of this thread
+        const float* pS = prefix ? prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D)
+                          : S_in ? S_in + (size_t)bh * D * D
+                                 : nullptr;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t r[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = pS ? __float_as_uint(pS[(size_t)(c0 + e) * D + a]) : 0u;
+            tmem_st16(tmem + CF::COL_S + lane_base + c0, r);
+        }
+        tmem_st_wait();
+        for (int ci = 0; ci < nci; ++ci) {
+            mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
+            const float all = ex2(gates[(ci % CF::GS) * 2 * C + C - 1]);
+            if (ci > 0) {
+                mbar_wait(bsdone, (ci - 1) & 1, err);
+                tc_fence_after();
+            }
+            // S_prev^T -> bf16 pairs, and scaled in place for this chunk's update
+            const uint32_t sb = tmem + CF::COL_SB + (ci & 1) * 64 + lane_base;
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t col = tmem + CF::COL_S + lane_base + 32 * h;
                 uint32_t r[32];
                 tmem_ld16(col, *reinterpret_cast<uint32_t(*)[16]>(r));
                 tmem_ld16(col + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
@@ -517,19 +584,8 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                 tmem_st16(col + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
             }
             tmem_st_wait();
-            fence_async_smem();
             tc_fence_before();
-            mbar_arrive(bprep);
-            if (normalize) {
-                named_bar(2, CF::PREP);
-                if (et < D) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) sum += red[x * D + et];
-                    zp = fmaf(zp, all, sum);
-                }
-                named_bar(2, CF::PREP);  // red is written again for the next chunk
-            }
+            warp_arrive(bstate, lane);
         }
     } else {
         // ---------------- mask + epilogue warps ----------------
@@ -537,17 +593,17 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
         const int i = sp * 16 + (lane & 15);  // P row (query) of this thread: M = 64 layout
         const int half = lane >= 16 ? 1 : 0;  // the two warp halves take the two column halves
-        const int et2 = threadIdx.x - 64 - CF::PREP;
+        const int et2 = threadIdx.x - 64 - CF::TRANSFORM - CF::STATE;
         bool ok = true;  // no early exit (named barrier 3); a failed wait only suppresses the stores
+#pragma unroll 1
         for (int ci = 0; ci < nci; ++ci) {
             const int slot = ci & 1, use = ci >> 1;
             const uint32_t lane_s = lane_base + static_cast<uint32_t>(slot) * (16u << 16);
             uint8_t* pts = pt + slot * CF::PT;
             ok = mbar_wait(bpfull + slot, use & 1, err) && ok;
-            // the gates came with the chunk's tiles, which P has waited for
-            mbar_wait(full + ci % CF::STAGES, (ci / CF::STAGES) & 1, err);
+            mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
             tc_fence_after();
-            const float* gs = gates + (ci % CF::STAGES) * 2 * C;
+            const float* gs = gates + (ci % CF::GS) * 2 * C;
             const float bi = gs[i];
             const bool deep = isinf(gs[C]);  // some query of the chunk lies below kDeep
             const float own = bi - fmaxf(bi, kDeep);
@@ -557,22 +613,22 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             uint32_t zq = 0;
             if (normalize) tmem_ld1x2<1>(tmem + CF::COL_P + lane_s + C, zq);
             tmem_ld_wait();
+            if (deep) {  // the factors per pair; below, the table's are 1 then
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    r[e] = __float_as_uint(__uint_as_float(r[e]) * ex2(own - gs[32 * half + e]));
+            }
             float rs = 0.f;
 #pragma unroll
             for (int gq = 0; gq < 4; ++gq) {
                 float f[8];
                 const int j0 = 32 * half + 8 * gq;
-                if (!deep) {
-                    const float4 x = *reinterpret_cast<const float4*>(gs + C + j0);
-                    const float4 y = *reinterpret_cast<const float4*>(gs + C + j0 + 4);
-                    const float e8[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                const float4 x = *reinterpret_cast<const float4*>(gs + C + j0);
+                const float4 y = *reinterpret_cast<const float4*>(gs + C + j0 + 4);
+                const float e8[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = j0 + e <= i ? __uint_as_float(r[8 * gq + e]) * e8[e] : 0.f;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f[e] = j0 + e <= i ? __uint_as_float(r[8 * gq + e]) * ex2(own - gs[j0 + e]) : 0.f;
-                }
+                for (int e = 0; e < 8; ++e)
+                    f[e] = j0 + e <= i ? __uint_as_float(r[8 * gq + e]) * (deep ? 1.f : e8[e]) : 0.f;
                 const uint4 w = pack8(f);
                 *reinterpret_cast<uint4*>(pts + sw128_off(i, j0)) = w;
                 // the denominator sums the rounded weights: the output is a mean with these very weights
@@ -584,13 +640,13 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                 rs += __shfl_xor_sync(0xffffffffu, rs, 16);
                 float qz = __uint_as_float(zq);  // phi(Q_i).z_hi (lanes < 16), .z_lo (lanes >= 16)
                 qz += __shfl_xor_sync(0xffffffffu, qz, 16);
-                if (lane < 16) inv[i] = __frcp_rn(rs + qz);
+                if (lane < 16) inv[i] = __fdividef(1.f, rs + qz);
             } else if (lane < 16) {
                 inv[i] = ex2(fmaxf(bi, kDeep));
             }
             fence_async_smem();
             tc_fence_before();
-            mbar_arrive(bptready + slot);
+            warp_arrive(bptready + slot, lane);
             // epilogue: this thread's d_v column of the chunk's output rows
             ok = ok && mbar_wait(bofull + slot, use & 1, err);
             tc_fence_after();
@@ -599,7 +655,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             const int mi = lane >> 3, mj = lane & 7;
             const int q2 = 2 * (lane & 3);
             const uint32_t stg_u = smem_u32(stg);
-#pragma unroll
+#pragma unroll 1
             for (int hl = 0; hl < 2; ++hl) {
                 const int a0 = sp * 32 + 16 * hl;
                 uint32_t o[32];
@@ -607,7 +663,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                 tmem_ld_wait();
                 if (hl == 1) {
                     tc_fence_before();
-                    mbar_arrive(bofree + slot);  // O^T[slot] read
+                    warp_arrive(bofree + slot, lane);  // O^T[slot] read
                 }
                 const uint32_t box = stg_u + (a0 / 64) * CF::BOX;
                 const int ch = (a0 % 64) / 8 + (mi & 1);

@@ -19,22 +19,48 @@ constexpr float kClosedLog2 = -160.f;
 // Queries whose products reach below 2^-90 are scaled by 2^90 (tc_gated.cu).
 constexpr float kDeep = -90.f;
 
+// One arrival for the whole warp, behind all its lanes' accesses (each lane has
+// fenced what needs a fence): barriers count warps, since an arrival per thread
+// costs the shared-memory pipe a turn per thread.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// One lane of a converged warp. The warp runs its loops and waits as a whole and
+// only the issue is this lane's, which lets the compiler keep descriptors and
+// loop counters in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// The two gates of this lane (tokens row0 + 2 lane, + 1), 0 past the row's end.
-__device__ __forceinline__ float2 load_gates(const __nv_bfloat16* g, int row0, int end, int lane) {
+// The two gates of this lane (tokens row0 + 2 lane, + 1; 0 past the row's end),
+// as loaded: converting them here would wait for the load.
+struct Gates2 {
+    uint16_t a, b;
+};
+__device__ __forceinline__ Gates2 load_gates(const __nv_bfloat16* g, int row0, int end, int lane) {
     const int i = row0 + 2 * lane;
-    return make_float2(i < end ? __bfloat162float(g[i]) : 0.f, i + 1 < end ? __bfloat162float(g[i + 1]) : 0.f);
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(g) + i;
+    Gates2 r{0, 0};
+    if (i < end) asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r.a) : "l"(p));
+    if (i + 1 < end) asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r.b) : "l"(p + 1));
+    return r;
 }
 // A whole warp: inclusive sums (log2) of this lane's two tokens over the chunk.
 // Returns the chunk's sum.
-__device__ __forceinline__ double scan_gates(float2 g, int lane, double& b0, double& b1) {
+__device__ __forceinline__ double scan_gates(const Gates2& g, int lane, double& b0, double& b1) {
     constexpr double kLog2e = 1.4426950408889634;
-    double x = (double)g.x * kLog2e, y = (double)g.y * kLog2e;
+    double x = (double)__uint_as_float((uint32_t)g.a << 16) * kLog2e;
+    double y = (double)__uint_as_float((uint32_t)g.b << 16) * kLog2e;
     x = x < kClosedLog2 ? kClosedLog2 : x;  // a NaN stays
     y = y < kClosedLog2 ? kClosedLog2 : y;
     double run = x + y;
@@ -53,18 +79,33 @@ template <int PHI> __device__ __forceinline__ float phi_f32(float x) {
     if constexpr (PHI == PHI_ELU1) return x > 0.f ? x + 1.f : ex2(x * 1.4426950408889634f);
     return x;
 }
-// w phi(x) of eight bf16 values in fp32 (f), as a bf16 part and the bf16 of what it leaves.
+// phi(x) of eight bf16 values (rounded to bf16), and w phi(x) in fp32 (f), as a
+// bf16 part and the bf16 of what it leaves.
 template <int PHI>
-__device__ __forceinline__ void weighted8(const uint4& x, float w, float (&f)[8], uint4& hi, uint4& lo) {
+__device__ __forceinline__ void weighted8(const uint4& x, float w, float (&f)[8], uint4& phi, uint4& hi, uint4& lo) {
     unpack8(x, f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = phi_f32<PHI>(f[e]) * w;
+    for (int e = 0; e < 8; ++e) f[e] = phi_f32<PHI>(f[e]);
+    phi = PHI == PHI_IDENTITY ? x : pack8(f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= w;
     hi = pack8(f);
     float h[8];
     unpack8(hi, h);
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = f[e] - h[e];
     lo = pack8(h);
+}
+// phi(x) of eight bf16 values, rounded to bf16.
+template <int PHI> __device__ __forceinline__ uint4 phi_round8(const uint4& x) {
+    if constexpr (PHI == PHI_ELU1) {
+        float f[8];
+        unpack8(x, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = phi_f32<PHI>(f[e]);
+        return pack8(f);
+    }
+    return phi8<PHI>(x);
 }
 
 }  // namespace tcg

@@ -34,14 +34,14 @@ struct GsCfg {
     static constexpr int STAGES = 4;
     static constexpr int STAGE = 2 * TILE;          // K (becomes the high part), V
     static constexpr int FLUSH = 8;                 // chunks per accumulation in TMEM
-    static constexpr int RED = 8 * D * 4;
+    static constexpr int PREP = 512, RED = PREP / 32 * D * 4;
     static constexpr int NBAR = 3 * STAGES + 2;
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 2 * TILE + RED + STAGES * C * 4 + 8 * NBAR + 16;
-    static constexpr int THREADS = 64 + 256;
+    static constexpr int THREADS = 64 + PREP;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-// Warp 0: TMA and gates; warp 1: MMA; warps 2..9: w phi(K) in two parts, z, and
+// Warp 0: TMA and gates; warp 1: MMA; warps 2..17: w phi(K) in two parts, z, and
 // the accumulators' sums (each FLUSH chunks' products are added to fp32
 // registers, so long blocks do not depend on how the tensor core rounds its
 // additions).
@@ -56,13 +56,13 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     uint8_t* stages = align1024(smem_raw);
     uint8_t* lo = stages + CF::STAGES * CF::STAGE;  // low parts of two chunks
     float* red = reinterpret_cast<float*>(lo + 2 * CF::TILE);
-    float* wts = red + 8 * D;  // [stage][C]
+    float* wts = red + CF::RED / 4;  // [stage][C]
     uint64_t* full = reinterpret_cast<uint64_t*>(wts + CF::STAGES * C);
     uint64_t* tdone = full + CF::STAGES;
     uint64_t* empty = tdone + CF::STAGES;
     uint64_t* acc = empty + CF::STAGES;  // [2] accumulator complete
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc + 2);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = warp_index(), lane = threadIdx.x % 32;
     const int blk = blockIdx.x, bh = blockIdx.y;
     const int first = blk * block_tokens, end = min(N, first + block_tokens);
     const int nci = (end - first + C - 1) / C;
@@ -70,7 +70,7 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
         cta_abort_reset();
         for (int s = 0; s < CF::STAGES; ++s) {
             mbar_init(full + s, 1);
-            mbar_init(tdone + s, 8);
+            mbar_init(tdone + s, CF::PREP / 32);
             mbar_init(empty + s, 1);
         }
         mbar_init(acc, 1);
@@ -145,12 +145,12 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
             __syncwarp();
         }
     } else {
-        const int et = threadIdx.x - 64, wq = warp - 2, sp = warp & 3, half = wq / 4;
+        const int et = threadIdx.x - 64, wq = warp - 2, sp = warp & 3, quarter = wq / 4;
         const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
         const int g = (lane & 7) ^ ((et >> 3) & 7);  // column group (of 8) of this thread's 16-byte chunks
-        float S[64], zk[CF::NB][8];
+        float S[32], zk[CF::NB][8];
 #pragma unroll
-        for (int e = 0; e < 64; ++e) S[e] = 0.f;
+        for (int e = 0; e < 32; ++e) S[e] = 0.f;
 #pragma unroll
         for (int b = 0; b < CF::NB; ++b)
 #pragma unroll
@@ -161,9 +161,9 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
             mbar_wait(acc + (f & 1), (f >> 1) & 1, err);
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 uint32_t r[16];
-                tmem_ld16(tmem + lane_base + (f & 1) * D + half * 64 + 16 * c, r);
+                tmem_ld16(tmem + lane_base + (f & 1) * D + quarter * 32 + 16 * c, r);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) S[16 * c + e] += __uint_as_float(r[e]);
@@ -183,19 +183,16 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
             uint8_t* lt = lo + (i & 1) * CF::TILE;
             const float* w = wts + s * C;
 #pragma unroll
-            for (int bx = 0; bx < CF::NB; ++bx)
+            for (int bx = 0; bx < CF::NB; ++bx) {  // each thread one 16-byte chunk per box: token et >> 3
+                uint4* kp = reinterpret_cast<uint4*>(kt + bx * CF::BOX + et * 16);
+                float f[8];
+                uint4 phi, hi, rest;
+                weighted8<PHI>(*kp, w[et >> 3], f, phi, hi, rest);
+                *kp = hi;
+                *reinterpret_cast<uint4*>(lt + bx * CF::BOX + et * 16) = rest;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int p = et + 256 * j;
-                    uint4* kp = reinterpret_cast<uint4*>(kt + bx * CF::BOX + p * 16);
-                    float f[8];
-                    uint4 phi, hi, rest;
-                    weighted8<PHI>(*kp, w[p >> 3], f, phi, hi, rest);
-                    *kp = hi;
-                    *reinterpret_cast<uint4*>(lt + bx * CF::BOX + p * 16) = rest;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) zk[bx][e] += f[e];
-                }
+                for (int e = 0; e < 8; ++e) zk[bx][e] += f[e];
+            }
             fence_async_smem();
             tc_fence_before();
             warp_arrive(tdone + s, lane);
@@ -214,16 +211,16 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                 dst[1] = make_float4(zk[bx][4], zk[bx][5], zk[bx][6], zk[bx][7]);
             }
         }
-        named_bar(1, 256);
+        named_bar(1, CF::PREP);
         if (et < D) {
             float z = 0.f;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) z += red[x * D + et];
+            for (int x = 0; x < CF::PREP / 32; ++x) z += red[x * D + et];
             rec[(size_t)D * D + et] = z;
         }
-        float4* o = reinterpret_cast<float4*>(rec + (size_t)(sp * 32 + lane) * D + half * 64);
+        float4* o = reinterpret_cast<float4*>(rec + (size_t)(sp * 32 + lane) * D + quarter * 32);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+        for (int e = 0; e < 8; ++e) o[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
     }
     tc_fence_before();
     __syncthreads();
@@ -236,16 +233,16 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
 // ---------------------------------------------------------------------------
 // Sweep
 // ---------------------------------------------------------------------------
-// Warp roles (576 threads): warp 0 TMA and gates, warp 1 MMA and TMEM, warps
+// Warp roles (704 threads): warp 0 TMA and gates, warp 1 MMA and TMEM, warps
 // 2..9 "transform" (phi on Q and K, w phi(K) in two parts, z), warps 10..13
 // "state" (S^T: the bf16 operand, and its decay in place), warps 14..17 "mask"
-// (P~, denominators, epilogue). The transforms run a chunk ahead: the loop
+// (P~, denominators), warps 18..21 "out" (O^T to the outputs). The transforms run a chunk ahead: the loop
 // from one S^T update to the next holds only the state warps' pass over S^T
 // and that update's products.
 struct GtCfg {
     static constexpr int D = 128, C = 64, NB = 2;
     static constexpr int BOX = C * 128;            // one 64-row x 64-column box (8 KB)
-    static constexpr int KBOX = (C + 16) * 128;    // K box + 16 rows (z_hi, z_lo, zeros)
+    static constexpr int KBOX = (C + 16) * 128;    // K box + 16 rows: z_prev in 8 parts, high and low
     static constexpr int TILE = NB * BOX;
     static constexpr int QK = TILE + NB * KBOX;    // Q, K' of a chunk: two slots, free after its P and O^T
     static constexpr int VS = 3;                   // V slots: free after its O^T += V^T P~^T, a chunk later
@@ -253,15 +250,16 @@ struct GtCfg {
     static constexpr int PT = C * C * 2;           // P~ [query][key], K-major (x2)
     static constexpr int STG = TILE;               // output staging tile
     static constexpr int KW = 2 * TILE;            // w phi(K), high and low part (x2)
-    static constexpr int RED = 8 * D * 4;          // column-sum partials [warp][d_k]
-    static constexpr int INV = C * 4;              // output scale per query row
+    static constexpr int INV = 2 * C * 4;          // output scale per query row (x2)
     static constexpr int GATES = GS * 2 * C * 4;
-    static constexpr int NBAR = 2 + 2 + 2 * VS + GS + 2 + 2 + 2 + 4 * 2;
-    static constexpr size_t SMEM = 1024 + 2 * (size_t)QK + VS * TILE + 2 * PT + STG + 2 * KW + RED + INV + GATES +
+    static constexpr int NBAR = 2 + 2 + 2 * VS + GS + 2 + 2 + 2 + 5 * 2;
+    static constexpr size_t SMEM = 1024 + 2 * (size_t)QK + VS * TILE + 2 * PT + STG + 2 * KW + INV + GATES +
                                    8 * NBAR + 16;
     // TMEM columns, as in tc_sweep_t.cu
     static constexpr int COL_S = 0, COL_SB = 128, COL_P = 256, COL_O = 384;
-    static constexpr int TRANSFORM = 256, STATE = 128, MASK = 128, THREADS = 64 + TRANSFORM + STATE + MASK;
+    static constexpr int TRANSFORM = 256, STATE = 128, MASK = 128, OUT = 128;
+    static constexpr int THREADS = 64 + TRANSFORM + STATE + MASK + OUT;
+    static constexpr int AHEAD = 4;                // chunks between a prefetch into L2 and the load
     static_assert(SMEM + 16 <= 227 * 1024, "shared memory (16 bytes static)");
     static_assert(QK % 1024 == 0 && KBOX % 1024 == 0, "1024-byte aligned operand tiles");
 };
@@ -281,9 +279,8 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     uint8_t* pt = vs + CF::VS * CF::TILE;
     uint8_t* stg = pt + 2 * CF::PT;
     uint8_t* kws = stg + CF::STG;
-    float* red = reinterpret_cast<float*>(kws + 2 * CF::KW);
-    float* inv = red + 8 * D;
-    float* gates = inv + C;
+    float* inv = reinterpret_cast<float*>(kws + 2 * CF::KW);
+    float* gates = inv + 2 * C;
     uint64_t* fullqk = reinterpret_cast<uint64_t*>(gates + CF::GS * 2 * C);
     uint64_t* emptyqk = fullqk + 2;
     uint64_t* fullv = emptyqk + 2;
@@ -297,9 +294,10 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     uint64_t* bptready = bpfull + 2;
     uint64_t* bofull = bptready + 2;
     uint64_t* bofree = bofull + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bofree + 2);
+    uint64_t* binv = bofree + 2;           // output scales written
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(binv + 2);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = warp_index(), lane = threadIdx.x % 32;
     const int blk = blockIdx.x, bh = blockIdx.y;
     const int first = blk * block_tokens, end = min(N, first + block_tokens);
     const int nci = (end - first + C - 1) / C;
@@ -321,7 +319,8 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             mbar_init(bpfull + j, 1);
             mbar_init(bptready + j, CF::MASK / 32);
             mbar_init(bofull + j, 1);
-            mbar_init(bofree + j, CF::MASK / 32);
+            mbar_init(bofree + j, CF::OUT / 32);
+            mbar_init(binv + j, CF::MASK / 32);
         }
         fence_mbar_init();
         tma_prefetch_map(&mQ);
@@ -377,6 +376,14 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 #pragma unroll
                 for (int bx = 0; bx < CF::NB; ++bx)
                     tma_load_3d(vs + s * CF::TILE + bx * CF::BOX, &mV, fullv + s, bx * 64, row, bh);
+                if (ci + CF::AHEAD < nci) {
+#pragma unroll
+                    for (int bx = 0; bx < CF::NB; ++bx) {
+                        tma_prefetch_3d(&mK, bx * 64, row + CF::AHEAD * C, bh);
+                        tma_prefetch_3d(&mQ, bx * 64, row + CF::AHEAD * C, bh);
+                        tma_prefetch_3d(&mV, bx * 64, row + CF::AHEAD * C, bh);
+                    }
+                }
             }
             __syncwarp();
             nv = ci + 1;
@@ -461,14 +468,18 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         const float* pz = prefix ? prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) + D * D
                           : z_in ? z_in + (size_t)bh * D
                                  : nullptr;
-        // rows 66..79 of both extended K boxes stay zero (TMA writes rows 0..63)
-        for (int x = et; x < 2 * CF::NB * 14 * 8; x += CF::TRANSFORM) {
-            const int s = x / (CF::NB * 112), bx = (x / 112) % CF::NB, r = 66 + (x % 112) / 8, q16 = x % 8;
-            *reinterpret_cast<uint4*>(qks + s * CF::QK + CF::TILE + bx * CF::KBOX + r * 128 + q16 * 16) =
-                make_uint4(0, 0, 0, 0);
-        }
-        float zp = pz && et < D ? pz[et] : 0.f;  // z_prev[d_k = et]
         const int g = (lane & 7) ^ ((et >> 3) & 7);  // column group (of 8) of this thread's 16-byte chunks
+        // z_prev stands in 8 parts, one per warp (the tokens that warp transforms
+        // in every chunk): row 64 + wq of the K boxes is the part's bf16 value,
+        // row 72 + wq the rounding remainder, and P's columns 64..79 add up to
+        // phi(Q).z_prev. The lanes l, l^9, l^18, l^27 hold the same column group
+        // g of both boxes; each keeps two of its columns, from column zc on.
+        const int zc = 8 * g + 4 * ((lane >> 3) & 1) + 2 * (lane >> 4);
+        float2 zp[CF::NB];
+#pragma unroll
+        for (int bx = 0; bx < CF::NB; ++bx)
+            zp[bx] = pz && wq == 0 ? make_float2(pz[bx * 64 + zc], pz[bx * 64 + zc + 1]) : make_float2(0.f, 0.f);
+#pragma unroll 1
         for (int ci = 0; ci < nci; ++ci) {
             const int j = ci & 1, k = ci >> 1;
             const int kvalid = min(C, end - first - ci * C);
@@ -484,15 +495,9 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                 const int r = (et >> 3) + 32 * i;
                 w[i] = r < kvalid ? ex2(blast - gs[r]) : 0.f;
             }
-            if (normalize && et < D) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(zp);
-                const __nv_bfloat16 lo = __float2bfloat16_rn(zp - __bfloat162float(hi));
-                uint8_t* kb = kt + (et / 64) * CF::KBOX;
-                *reinterpret_cast<__nv_bfloat16*>(kb + sw128_off(C, et % 64)) = hi;
-                *reinterpret_cast<__nv_bfloat16*>(kb + sw128_off(C + 1, et % 64)) = lo;
-            }
+            const float all = ex2(blast);
             if (k > 0) mbar_wait(kwfree + j, (k - 1) & 1, err);  // chunk ci - 2's update has read kw
-#pragma unroll 1
+#pragma unroll
             for (int bx = 0; bx < CF::NB; ++bx) {
                 float cs[8];
 #pragma unroll
@@ -515,32 +520,32 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                     for (int e = 0; e < 8; ++e) cs[e] += f[e];
                 }
                 if (normalize) {
-                    // lanes l, l^9, l^18, l^27 hold the same column group g
+                    const uint32_t hi = pack_bf16(zp[bx].x, zp[bx].y);
+                    const float2 rest = make_float2(zp[bx].x - __uint_as_float(hi << 16),
+                                                    zp[bx].y - __uint_as_float(hi & 0xffff0000u));
+                    uint8_t* kb = kt + bx * CF::KBOX;
+                    *reinterpret_cast<uint32_t*>(kb + sw128_off(C + wq, zc)) = hi;
+                    *reinterpret_cast<uint32_t*>(kb + sw128_off(C + 8 + wq, zc)) = pack_bf16(rest.x, rest.y);
+                    // the warp's column sums: lanes with bit 3 set keep columns
+                    // 4..7 of the group, then lanes with bit 4 set the upper two
+                    float s4[4], s2[2];
+                    const bool b3 = lane & 8, b4 = lane & 16;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        cs[e] += __shfl_xor_sync(0xffffffffu, cs[e], 9);
-                        cs[e] += __shfl_xor_sync(0xffffffffu, cs[e], 18);
+                    for (int e = 0; e < 4; ++e) {
+                        const float give = b3 ? cs[e] : cs[4 + e], keep = b3 ? cs[4 + e] : cs[e];
+                        s4[e] = keep + __shfl_xor_sync(0xffffffffu, give, 9);
                     }
-                    if (lane < 8) {
-                        float4* dst = reinterpret_cast<float4*>(red + wq * D + bx * 64 + g * 8);
-                        dst[0] = make_float4(cs[0], cs[1], cs[2], cs[3]);
-                        dst[1] = make_float4(cs[4], cs[5], cs[6], cs[7]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float give = b4 ? s4[e] : s4[2 + e], keep = b4 ? s4[2 + e] : s4[e];
+                        s2[e] = keep + __shfl_xor_sync(0xffffffffu, give, 18);
                     }
+                    zp[bx].x = fmaf(zp[bx].x, all, s2[0]);
+                    zp[bx].y = fmaf(zp[bx].y, all, s2[1]);
                 }
             }
             fence_async_smem();
             warp_arrive(btrans + j, lane);
-            if (normalize) {
-                const float all = ex2(blast);
-                named_bar(2, CF::TRANSFORM);
-                if (et < D) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) sum += red[x * D + et];
-                    zp = fmaf(zp, all, sum);
-                }
-                named_bar(2, CF::TRANSFORM);  // red is written again for the next chunk
-            }
         }
     } else if (warp < 14) {
         // ---------------- state warps ----------------
@@ -587,33 +592,30 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             tc_fence_before();
             warp_arrive(bstate, lane);
         }
-    } else {
-        // ---------------- mask + epilogue warps ----------------
+    } else if (warp < 18) {
+        // ---------------- mask warps ----------------
         const int sp = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
         const int i = sp * 16 + (lane & 15);  // P row (query) of this thread: M = 64 layout
         const int half = lane >= 16 ? 1 : 0;  // the two warp halves take the two column halves
-        const int et2 = threadIdx.x - 64 - CF::TRANSFORM - CF::STATE;
-        bool ok = true;  // no early exit (named barrier 3); a failed wait only suppresses the stores
 #pragma unroll 1
         for (int ci = 0; ci < nci; ++ci) {
             const int slot = ci & 1, use = ci >> 1;
             const uint32_t lane_s = lane_base + static_cast<uint32_t>(slot) * (16u << 16);
             uint8_t* pts = pt + slot * CF::PT;
-            ok = mbar_wait(bpfull + slot, use & 1, err) && ok;
             mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
-            tc_fence_after();
             const float* gs = gates + (ci % CF::GS) * 2 * C;
             const float bi = gs[i];
             const bool deep = isinf(gs[C]);  // some query of the chunk lies below kDeep
             const float own = bi - fmaxf(bi, kDeep);
-            uint32_t r[32];
+            mbar_wait(bpfull + slot, use & 1, err);
+            tc_fence_after();
+            uint32_t r[32], zq[8];
             tmem_ld16x2<32>(tmem + CF::COL_P + lane_s, *reinterpret_cast<uint32_t(*)[16]>(r));
             tmem_ld16x2<32>(tmem + CF::COL_P + lane_s + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
-            uint32_t zq = 0;
-            if (normalize) tmem_ld1x2<1>(tmem + CF::COL_P + lane_s + C, zq);
+            if (normalize) tmem_ld8x2<8>(tmem + CF::COL_P + lane_s + C, zq);
             tmem_ld_wait();
-            if (deep) {  // the factors per pair; below, the table's are 1 then
+            if (deep) {  // the factors per pair; the table's are not used then
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                     r[e] = __float_as_uint(__uint_as_float(r[e]) * ex2(own - gs[32 * half + e]));
@@ -636,41 +638,49 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 #pragma unroll
                 for (int e = 0; e < 8; ++e) rs += f[e];
             }
-            if (normalize) {
-                rs += __shfl_xor_sync(0xffffffffu, rs, 16);
-                float qz = __uint_as_float(zq);  // phi(Q_i).z_hi (lanes < 16), .z_lo (lanes >= 16)
-                qz += __shfl_xor_sync(0xffffffffu, qz, 16);
-                if (lane < 16) inv[i] = __fdividef(1.f, rs + qz);
-            } else if (lane < 16) {
-                inv[i] = ex2(fmaxf(bi, kDeep));
-            }
             fence_async_smem();
             tc_fence_before();
             warp_arrive(bptready + slot, lane);
-            // epilogue: this thread's d_v column of the chunk's output rows
-            ok = ok && mbar_wait(bofull + slot, use & 1, err);
+            if (normalize) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) rs += __uint_as_float(zq[e]);  // phi(Q_i).z_prev, half of its parts
+                rs += __shfl_xor_sync(0xffffffffu, rs, 16);
+            }
+            // the scales of chunk ci - 2 have been read
+            if (use > 0) mbar_wait(bofree + slot, (use - 1) & 1, err);
+            if (lane < 16) inv[slot * C + i] = normalize ? __fdividef(1.f, rs) : ex2(fmaxf(bi, kDeep));
+            warp_arrive(binv + slot, lane);
+        }
+    } else {
+        // ---------------- out warps ----------------
+        const int sp = warp & 3, et = threadIdx.x - (CF::THREADS - CF::OUT);
+        const int mi = lane >> 3, mj = lane & 7, q2 = 2 * (lane & 3);
+        const uint32_t stg_u = smem_u32(stg);
+        bool ok = true;  // no early exit (named barrier 3); a failed wait only suppresses the stores
+#pragma unroll 1
+        for (int ci = 0; ci < nci; ++ci) {
+            const int slot = ci & 1, use = ci >> 1;
+            const float* scale = inv + slot * C;
+            ok = mbar_wait(binv + slot, use & 1, err) && ok;
+            ok = mbar_wait(bofull + slot, use & 1, err) && ok;
             tc_fence_after();
-            if (et2 == 0) bulk_wait_read0();  // the previous chunk's store has read stg
-            named_bar(3, 128);                // also: inv[] is written
-            const int mi = lane >> 3, mj = lane & 7;
-            const int q2 = 2 * (lane & 3);
-            const uint32_t stg_u = smem_u32(stg);
+            if (et == 0) bulk_wait_read0();  // the previous chunk's store has read stg
+            named_bar(3, CF::OUT);
+            // O^T rows (d_v) a0 .. a0 + 15, 16 columns (queries) at a time: the
+            // 16x256b TMEM shape hands each lane the fragment that stmatrix .trans
+            // stores with the queries as rows
 #pragma unroll 1
             for (int hl = 0; hl < 2; ++hl) {
                 const int a0 = sp * 32 + 16 * hl;
                 uint32_t o[32];
                 tmem_ld16x256_x8(tmem + CF::COL_O + slot * C + (static_cast<uint32_t>(a0) << 16), o);
                 tmem_ld_wait();
-                if (hl == 1) {
-                    tc_fence_before();
-                    warp_arrive(bofree + slot, lane);  // O^T[slot] read
-                }
                 const uint32_t box = stg_u + (a0 / 64) * CF::BOX;
                 const int ch = (a0 % 64) / 8 + (mi & 1);
 #pragma unroll
                 for (int cb = 0; cb < C; cb += 16) {
-                    const float2 i0 = *reinterpret_cast<const float2*>(inv + cb + q2);
-                    const float2 i1 = *reinterpret_cast<const float2*>(inv + cb + 8 + q2);
+                    const float2 i0 = *reinterpret_cast<const float2*>(scale + cb + q2);
+                    const float2 i1 = *reinterpret_cast<const float2*>(scale + cb + 8 + q2);
                     const uint32_t* x = o + (cb / 8) * 4;
                     const uint32_t p0 = pack_bf16(__uint_as_float(x[0]) * i0.x, __uint_as_float(x[1]) * i0.y);
                     const uint32_t p1 = pack_bf16(__uint_as_float(x[2]) * i0.x, __uint_as_float(x[3]) * i0.y);
@@ -680,15 +690,17 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                     stmatrix_x4_trans(box + row * 128u + ((static_cast<uint32_t>(ch) ^ (row & 7u)) << 4), p0, p1, p2, p3);
                 }
             }
+            tc_fence_before();
+            warp_arrive(bofree + slot, lane);  // O^T[slot] and its scales read
             fence_async_smem();
-            named_bar(3, 128);
-            if (et2 == 0 && ok) {
+            named_bar(3, CF::OUT);
+            if (et == 0 && ok) {
 #pragma unroll
                 for (int bx = 0; bx < CF::NB; ++bx) tma_store_3d(&mOut, stg + bx * CF::BOX, bx * 64, first + ci * C, bh);
                 bulk_commit();
             }
         }
-        if (et2 == 0) bulk_wait0();  // the output stores have landed
+        if (et == 0) bulk_wait0();  // the output stores have landed
     }
     tc_fence_before();
     __syncthreads();

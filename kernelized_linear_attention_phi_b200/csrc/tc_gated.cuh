@@ -19,6 +19,21 @@ constexpr float kClosedLog2 = -160.f;
 // Queries whose products reach below 2^-90 are scaled by 2^90 (tc_gated.cu).
 constexpr float kDeep = -90.f;
 
+// Brings a box of a tensor map towards L2, ahead of its load.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+// Warp-wide, M = 64 accumulators: lanes 0..15 receive TMEM lane (base + i),
+// columns [col, col + 8), lanes 16..31 TMEM lane (base + i - 16), columns
+// [col + SPLIT, col + SPLIT + 8).
+template <int SPLIT> __device__ __forceinline__ void tmem_ld8x2(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr), "n"(SPLIT));
+}
+
 // One arrival for the whole warp, behind all its lanes' accesses (each lane has
 // fenced what needs a fence): barriers count warps, since an arrival per thread
 // costs the shared-memory pipe a turn per thread.
@@ -26,6 +41,10 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
 }
+
+// The warp's index, through a shuffle: the compiler then knows that it is the
+// same in all lanes and that branches on it do not split the warp.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0); }
 
 // One lane of a converged warp. The warp runs its loops and waits as a whole and
 // only the issue is this lane's, which lets the compiler keep descriptors and

@@ -234,8 +234,8 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
 // Sweep
 // ---------------------------------------------------------------------------
 // Warp roles (704 threads): warp 0 TMA and gates, warp 1 MMA and TMEM, warps
-// 2..9 "transform" (phi on Q and K, w phi(K) in two parts, z), warps 10..13
-// "state" (S^T: the bf16 operand, and its decay in place), warps 14..17 "mask"
+// 2..9 "transform" (phi on K, w phi(K) in two parts, z), warps 10..13
+// "state" (phi on Q; S^T: the bf16 operand, and its decay in place), warps 14..17 "mask"
 // (P~, denominators), warps 18..21 "out" (O^T to the outputs). The transforms run a chunk ahead: the loop
 // from one S^T update to the next holds only the state warps' pass over S^T
 // and that update's products.
@@ -286,9 +286,9 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     uint64_t* fullv = emptyqk + 2;
     uint64_t* emptyv = fullv + CF::VS;
     uint64_t* gfull = emptyv + CF::VS;     // gates of a chunk written
-    uint64_t* bstate = gfull + CF::GS;     // S_prev^T operand written, S^T scaled
+    uint64_t* bstate = gfull + CF::GS;     // Q and the S_prev^T operand written, S^T scaled
     uint64_t* bsdone = bstate + 1;         // S^T update of the chunk done
-    uint64_t* btrans = bsdone + 1;         // per slot (chunk % 2): K', Q and w phi(K) written
+    uint64_t* btrans = bsdone + 1;         // per slot (chunk % 2): K' and w phi(K) written
     uint64_t* kwfree = btrans + 2;         // w phi(K) read
     uint64_t* bpfull = kwfree + 2;         // P ready, P~ written, O^T ready, O^T read
     uint64_t* bptready = bpfull + 2;
@@ -483,8 +483,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
         for (int ci = 0; ci < nci; ++ci) {
             const int j = ci & 1, k = ci >> 1;
             const int kvalid = min(C, end - first - ci * C);
-            uint8_t* qt = qks + j * CF::QK;
-            uint8_t* kt = qt + CF::TILE;
+            uint8_t* kt = qks + j * CF::QK + CF::TILE;
             uint8_t* kw = kws + j * CF::KW;
             mbar_wait(fullqk + j, k & 1, err);
             const float* gs = gates + (ci % CF::GS) * 2 * C;
@@ -511,11 +510,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
                     weighted8<PHI>(*kp, w[i], f, phi, hi, lo);
                     *reinterpret_cast<uint4*>(kw + bx * CF::BOX + p * 16) = hi;
                     *reinterpret_cast<uint4*>(kw + CF::TILE + bx * CF::BOX + p * 16) = lo;
-                    if (PHI != PHI_IDENTITY) {  // rows past the end are masked in P~
-                        *kp = phi;
-                        uint4* qp = reinterpret_cast<uint4*>(qt + bx * CF::BOX + p * 16);
-                        *qp = phi_round8<PHI>(*qp);
-                    }
+                    if (PHI != PHI_IDENTITY) *kp = phi;  // rows past the end are masked in P~
 #pragma unroll
                     for (int e = 0; e < 8; ++e) cs[e] += f[e];
                 }
@@ -563,7 +558,16 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             tmem_st16(tmem + CF::COL_S + lane_base + c0, r);
         }
         tmem_st_wait();
+#pragma unroll 1
         for (int ci = 0; ci < nci; ++ci) {
+            const int et = threadIdx.x - (64 + CF::TRANSFORM);
+            if (PHI != PHI_IDENTITY) {  // phi on the chunk's queries, while the last update runs
+                mbar_wait(fullqk + (ci & 1), (ci >> 1) & 1, err);
+                uint4* q = reinterpret_cast<uint4*>(qks + (ci & 1) * CF::QK);
+#pragma unroll 2
+                for (int x = et; x < CF::TILE / 16; x += CF::STATE) q[x] = phi_round8<PHI>(q[x]);
+                fence_async_smem();
+            }
             mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
             const float all = ex2(gates[(ci % CF::GS) * 2 * C + C - 1]);
             if (ci > 0) {

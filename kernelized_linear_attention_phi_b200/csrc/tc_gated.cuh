@@ -102,12 +102,23 @@ template <int PHI> __device__ __forceinline__ float phi_f32(float x) {
 // bf16 part and the bf16 of what it leaves.
 template <int PHI>
 __device__ __forceinline__ void weighted8(const uint4& x, float w, float (&f)[8], uint4& phi, uint4& hi, uint4& lo) {
-    unpack8(x, f);
+    if constexpr (PHI == PHI_RELU1) {  // w (relu(x) + 1) = w relu(x) + w; relu(x) is exact in bf16
+        phi = phi8<PHI>(x);
+        unpack8(relu_x8(x), f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = phi_f32<PHI>(f[e]);
-    phi = PHI == PHI_IDENTITY ? x : pack8(f);
+        for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], w, w);
+    } else {
+        unpack8(x, f);
+        if constexpr (PHI == PHI_ELU1) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= w;
+            for (int e = 0; e < 8; ++e) f[e] = phi_f32<PHI>(f[e]);
+            phi = pack8(f);
+        } else {
+            phi = x;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= w;
+    }
     hi = pack8(f);
     float h[8];
     unpack8(hi, h);

@@ -14,6 +14,7 @@ S [B, H, d, d] and z [B, H, d] float32, m [B, N] int32. ``phi`` is "relu1"
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -353,38 +354,69 @@ def la_causal_backward(q, k, v, dout, dq=None, dk=None, dv=None, phi="relu1", no
     return _backward("la_causal_backward", "causal_bwd", q, k, v, dout, dq, dk, dv, phi, normalize, ws, stream)
 
 
+# The entry points below take the caller's tensors as they are and check each
+# once; shapes, types and devices are compared as plain tuples and numbers,
+# since at one token the call is host time.
+
+
+# the handle of torch's current stream, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _on:
-    """The device of ``ref`` and ``stream`` (torch's current one there when
-    None) made current: what a call allocates and clears is then ordered with
-    its kernels, whatever device and stream the caller was on."""
+    """The device of a call's tensors and its stream (torch's current one there
+    when None) made current: what the call allocates and clears is then ordered
+    with its kernels, whatever device and stream the caller was on. Entering
+    gives the stream's handle."""
+
+    __slots__ = ("index", "guards", "stream")
 
     def __init__(self, ref, stream):
-        if not ref.is_cuda:
+        self.index = ref.get_device()
+        if self.index < 0:
             raise ValueError("tensors must be on a CUDA device")
-        self.device = torch.cuda.device(ref.device) if ref.device.index != torch.cuda.current_device() else None
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=ref.device)
-        self.stream = torch.cuda.stream(stream) if stream is not None else None
-        self.ref = ref
+        self.guards = None
+        self.stream = stream
 
     def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream(self.ref.device).cuda_stream)
+        if self.stream is None and self.index == torch.cuda.current_device():
+            return _raw_stream(self.index)
+        stream = self.stream
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.index)
+        self.guards = [torch.cuda.device(self.index)]
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+        for g in self.guards:
+            g.__enter__()
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+        for g in reversed(self.guards or ()):
+            g.__exit__(*exc)
 
 
-def _gates(g, ref):
-    B, H, N, _ = ref.shape
-    if g.dtype != ref.dtype or tuple(g.shape) != (B, H, N) or g.device != ref.device:
-        raise ValueError(f"g must be {ref.dtype} [{B}, {H}, {N}] on {ref.device}")
+def _arg(name, t, dtype, shape, index):
+    """The address of a contiguous tensor of the given type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _gated_desc(shape, dtype, phi, normalize):
+    if len(shape) != 4:
+        raise ValueError(f"expected a [B, H, N, d] tensor, got shape {tuple(shape)}")
+    if dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return make_desc(*shape, dtype, phi, normalize)
+
+
+def _pair(what, a, b):
+    if (a is None) != (b is None):
+        raise ValueError(f"give both S and z of {what}, or neither")
 
 
 def la_gated_causal(q, k, v, g, S_in=None, z_in=None, out=None, S_out=None, z_out=None, phi="relu1", normalize=True,
@@ -393,24 +425,26 @@ def la_gated_causal(q, k, v, g, S_in=None, z_in=None, out=None, S_out=None, z_ou
     log-gates, -inf starts anew). S_in, z_in: the state in front of the first
     token; S_out, z_out (may be the same) receive the one after the last.
     Returns out."""
-    desc = _desc_of(q, phi, normalize)
-    _gates(g, q)
-    for a, b in ((S_in, z_in), (S_out, z_out)):
-        if (a is None) != (b is None):
-            raise ValueError("give both S and z of a state, or neither")
-        if a is not None:
-            _state(a, b, q)
+    shape, dt = q.shape, q.dtype
+    desc = _gated_desc(shape, dt, phi, bool(normalize))
+    _pair("the state in front", S_in, z_in)
+    _pair("the state behind", S_out, z_out)
     with _on(q, stream) as st:
-        if out is None:
-            out = torch.empty_like(q)
-        _same(q, k, v, out)
-        if ws is None:
-            ws = workspace(desc, "gated_causal", device=q.device) if la_workspace_size(desc, "gated_causal") else None
-        else:
-            _ws(ws, q)
-        _check("la_gated_causal", lib().la_gated_causal(
-            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S_in), _ptr(z_in), _ptr(out), _ptr(S_out),
-            _ptr(z_out), _ptr(ws), 0 if ws is None else ws.numel(), st))
+        i = q.get_device()
+        B, H, N, d = shape
+        args = [_arg("q", q, dt, shape, i), _arg("k", k, dt, shape, i), _arg("v", v, dt, shape, i),
+                _arg("g", g, dt, (B, H, N), i)]
+        for S, z in ((S_in, z_in), (S_out, z_out)):
+            if S is None:
+                args += (None, None)
+            else:
+                args += (_arg("S", S, torch.float32, (B, H, d, d), i), _arg("z", z, torch.float32, (B, H, d), i))
+        out = torch.empty_like(q) if out is None else out
+        args.insert(6, _arg("out", out, dt, shape, i))
+        if ws is None and la_workspace_size(desc, "gated_causal"):
+            ws = workspace(desc, "gated_causal", device=q.device)
+        args += (None, 0) if ws is None else (_ws(ws, q).data_ptr(), ws.numel())
+        _check("la_gated_causal", lib().la_gated_causal(ctypes.byref(desc), *args, st))
     return out
 
 
@@ -418,80 +452,87 @@ def la_gated_causal_backward(q, k, v, g, dout, dq=None, dk=None, dv=None, dg=Non
                              stream=None):
     """Gradients (dq, dk, dv, dg) of la_gated_causal, from an empty state, for
     upstream dout."""
-    desc = _desc_of(q, phi, normalize)
-    _gates(g, q)
+    shape, dt = q.shape, q.dtype
+    desc = _gated_desc(shape, dt, phi, bool(normalize))
     with _on(q, stream) as st:
+        i, dev = q.get_device(), q.device
+        gates = tuple(shape[:3])
+        args = [_arg("q", q, dt, shape, i), _arg("k", k, dt, shape, i), _arg("v", v, dt, shape, i),
+                _arg("g", g, dt, gates, i), _arg("dout", dout, dt, shape, i)]
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
         dg = torch.empty_like(g) if dg is None else dg
-        _same(q, k, v, dout, dq, dk, dv)
-        _gates(dg, q)
-        ws = workspace(desc, "gated_causal_bwd", device=q.device) if ws is None else _ws(ws, q)
+        args += (_arg("dq", dq, dt, shape, i), _arg("dk", dk, dt, shape, i), _arg("dv", dv, dt, shape, i),
+                 _arg("dg", dg, dt, gates, i))
+        ws = workspace(desc, "gated_causal_bwd", device=dev) if ws is None else _ws(ws, q)
         _check("la_gated_causal_backward", lib().la_gated_causal_backward(
-            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
-            _ptr(ws), ws.numel(), st))
+            ctypes.byref(desc), *args, ws.data_ptr(), ws.numel(), st))
     return dq, dk, dv, dg
 
 
 def la_gated_decode_step(q, k, v, g, S, z, S_out=None, z_out=None, out=None, phi="relu1", normalize=True, stream=None):
     """One token on the state (S, z): q, k, v [B, H, 1, d], g [B, H, 1]. The new
     state goes to S_out, z_out, or in place when they are not given. Returns out."""
-    desc = _desc_of(q, phi, normalize)
-    if q.shape[2] != 1:
+    shape, dt = q.shape, q.dtype
+    desc = _gated_desc(shape, dt, phi, bool(normalize))
+    B, H, N, d = shape
+    if N != 1:
         raise ValueError("a step takes one token: [B, H, 1, d]")
-    _gates(g, q)
-    if (S_out is None) != (z_out is None):
-        raise ValueError("give both S and z of a state, or neither")
-    _state(S, z, q)
-    if S_out is None:
-        S_out, z_out = S, z
-    else:
-        _state(S_out, z_out, q)
+    _pair("the new state", S_out, z_out)
     with _on(q, stream) as st:
-        if out is None:
-            out = torch.empty_like(q)
-        _same(q, k, v, out)
+        i = q.get_device()
+        s = _arg("S", S, torch.float32, (B, H, d, d), i), _arg("z", z, torch.float32, (B, H, d), i)
+        new = s
+        if S_out is not None:
+            new = _arg("S_out", S_out, torch.float32, (B, H, d, d), i), _arg("z_out", z_out, torch.float32, (B, H, d), i)
+        out = torch.empty_like(q) if out is None else out
         _check("la_gated_decode_step", lib().la_gated_decode_step(
-            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(z), _ptr(S_out), _ptr(z_out), _ptr(out),
-            st))
+            ctypes.byref(desc), _arg("q", q, dt, shape, i), _arg("k", k, dt, shape, i), _arg("v", v, dt, shape, i),
+            _arg("g", g, dt, (B, H, 1), i), *s, *new, _arg("out", out, dt, shape, i), st))
     return out
 
 
-def _rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
-    """The descriptor and the pointers of the inputs both directions share."""
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
-        raise ValueError(f"expected q [B, N, Hq, d] and k [B, N, Hk, d], got {tuple(q.shape)} and {tuple(k.shape)}")
-    if q.dtype not in DTYPES or k.dtype != q.dtype or k.device != q.device:
-        raise ValueError("q and k must share a device and a dtype (float32 or bfloat16)")
-    B, N, Hq, d = q.shape
+@functools.lru_cache(maxsize=256)
+def _rope_desc(q_shape, k_shape, dtype, table, interleaved, eps):
+    if len(q_shape) != 4 or len(k_shape) != 4 or q_shape[:2] != k_shape[:2] or q_shape[3] != k_shape[3]:
+        raise ValueError(f"expected q [B, N, Hq, d] and k [B, N, Hk, d], got {tuple(q_shape)} and {tuple(k_shape)}")
+    if dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    B, N, Hq, d = q_shape
+    if len(table) != 2:
+        raise ValueError("cos and sin must be [rows, rot / 2] tables")
+    rows, rot = table[0], 2 * table[1]
+    if rows >= 1 << 31 or rot > d:
+        raise ValueError(f"the tables turn {rot} of {d} channels and have {rows} rows")
+    return la_rope_desc(B, N, Hq, k_shape[2], d, rot, DTYPES[dtype], int(interleaved), rows, eps)
+
+
+def _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    """The descriptor and the arguments that both directions share."""
     if (cos is None) != (sin is None) or (q_weight is None) != (k_weight is None):
         raise ValueError("give both cos and sin, and both weights, or neither")
-    rot = rows = 0
-    if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape:
-            raise ValueError("cos and sin must be [rows, rot / 2] tables")
-        rows, rot = cos.shape[0], 2 * cos.shape[1]
-        if rows >= 1 << 31 or rot > d:
-            raise ValueError(f"the tables turn {rot} of {d} channels and have {rows} rows")
-    for t in (q_weight, k_weight):
-        if t is not None and tuple(t.shape) != (d,):
-            raise ValueError(f"weights must be [{d}]")
-    for t in (q_weight, k_weight, cos, sin):
-        if t is not None and (t.dtype != torch.float32 or t.device != q.device):
-            raise ValueError(f"weights and tables must be float32 on {q.device}")
-    if positions is not None and (positions.dtype != torch.int32 or tuple(positions.shape) != (B, N) or
-                                  positions.device != q.device):
-        raise ValueError(f"positions must be int32 [{B}, {N}] on {q.device}")
-    desc = la_rope_desc(B, N, Hq, k.shape[2], d, rot, DTYPES[q.dtype], int(bool(interleaved)), rows, float(eps))
-    return desc, [_ptr(t) for t in (q_weight, k_weight, cos, sin, positions)]
+    table = (0, 0) if cos is None else cos.shape
+    desc = _rope_desc(q.shape, k.shape, q.dtype, table, bool(interleaved), float(eps))
+    i = q.get_device()
+    if k.dtype is not q.dtype or k.get_device() != i:
+        raise ValueError("q and k must share a device and a dtype (float32 or bfloat16)")
+    B, N, _, d = q.shape
+    f32 = torch.float32
+    small = []
+    for name, t, shape in (("q_weight", q_weight, (d,)), ("k_weight", k_weight, (d,)), ("cos", cos, table),
+                           ("sin", sin, table)):
+        small.append(None if t is None else _arg(name, t, f32, shape, i))
+    small.append(None if positions is None else _arg("positions", positions, torch.int32, (B, N), i))
+    return desc, [q.data_ptr(), _strides("q", q), k.data_ptr(), _strides("k", k), *small]
 
 
-def _rows(t):
-    """Pointer and strides of a [B, N, H, d] view with contiguous rows."""
-    if t.stride(3) != 1:
-        raise ValueError("the rows of q and k must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), ctypes.byref(la_strides(*t.stride()[:3]))
+def _strides(name, t):
+    """The strides of a [B, N, H, d] view with contiguous rows."""
+    b, n, h, one = t.stride()
+    if one != 1 and t.shape[3] != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return ctypes.byref(la_strides(b, n, h))
 
 
 def la_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, interleaved=False, q_out=None,
@@ -502,22 +543,16 @@ def la_qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6
     k [B, N, Hk, d] may be views into one projection; positions int32 [B, N],
     or None for 0 .. N - 1. Returns contiguous (q_out [B, Hq, N, d], k_out
     [B, Hk, N, d])."""
-    desc, small = _rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    B, N, Hq, d = q.shape
     with _on(q, stream) as st:
-        q_out = torch.empty(B, Hq, N, d, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        k_out = torch.empty(B, desc.Hk, N, d, dtype=q.dtype, device=q.device) if k_out is None else k_out
-        _outputs(q, (q_out, Hq), (k_out, desc.Hk))
+        desc, args = _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+        i, dt = q.get_device(), q.dtype
+        B, N, Hq, d = q.shape
+        qs, ks = (B, Hq, N, d), (B, desc.Hk, N, d)
+        q_out = q.new_empty(qs) if q_out is None else q_out
+        k_out = q.new_empty(ks) if k_out is None else k_out
         _check("la_qk_norm_rope", lib().la_qk_norm_rope(
-            ctypes.byref(desc), *_rows(q), *_rows(k), *small, _ptr(q_out), _ptr(k_out), st))
+            ctypes.byref(desc), *args, _arg("q_out", q_out, dt, qs, i), _arg("k_out", k_out, dt, ks, i), st))
     return q_out, k_out
-
-
-def _outputs(q, *pairs):
-    B, N, _, d = q.shape
-    for t, H in pairs:
-        if t.dtype != q.dtype or tuple(t.shape) != (B, H, N, d) or t.device != q.device:
-            raise ValueError(f"expected {q.dtype} [{B}, {H}, {N}, {d}] on {q.device}, got {t.dtype} {tuple(t.shape)}")
 
 
 def la_qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, dq_out, dk_out, positions=None, eps=1e-6,
@@ -526,30 +561,31 @@ def la_qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, dq_out, dk_out,
     dq_out [B, Hq, N, d], dk_out [B, Hk, N, d]. dq, dk may be given as views
     like q, k (of one packed gradient, say). Without weights the last two are
     None."""
-    desc, small = _rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    d = q.shape[3]
-    _outputs(q, (dq_out, desc.Hq), (dk_out, desc.Hk))
     with _on(q, stream) as st:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-        for t, like in ((dq, q), (dk, k)):
-            if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
+        desc, args = _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+        i, dt, dev = q.get_device(), q.dtype, q.device
+        B, N, Hq, d = q.shape
+        args += (_arg("dq_out", dq_out, dt, (B, Hq, N, d), i), _arg("dk_out", dk_out, dt, (B, desc.Hk, N, d), i))
+        dq = q.new_empty(q.shape) if dq is None else dq
+        dk = k.new_empty(k.shape) if dk is None else dk
+        for name, t, like in (("dq", dq, q), ("dk", dk, k)):
+            if t.dtype is not dt or t.shape != like.shape or t.get_device() != i:
                 raise ValueError("dq and dk must have the shape, dtype and device of q and k")
+            args += (t.data_ptr(), _strides(name, t))
         if q_weight is None:
             if dq_weight is not None or dk_weight is not None:
                 raise ValueError("there are no weights to differentiate")
+            args += (None, None)
         else:
-            dq_weight = torch.empty_like(q_weight) if dq_weight is None else dq_weight
-            dk_weight = torch.empty_like(k_weight) if dk_weight is None else dk_weight
-            for t in (dq_weight, dk_weight):
-                if t.dtype != torch.float32 or tuple(t.shape) != (d,) or t.device != q.device:
-                    raise ValueError(f"weight gradients must be float32 [{d}] on {q.device}")
-        n = int(lib().la_qk_norm_rope_workspace_size(ctypes.byref(desc)))
+            dq_weight = q_weight.new_empty((d,)) if dq_weight is None else dq_weight
+            dk_weight = k_weight.new_empty((d,)) if dk_weight is None else dk_weight
+            args += (_arg("dq_weight", dq_weight, torch.float32, (d,), i),
+                     _arg("dk_weight", dk_weight, torch.float32, (d,), i))
         if ws is None:
-            ws = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+            n = int(lib().la_qk_norm_rope_workspace_size(ctypes.byref(desc)))
+            ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
         else:
             _ws(ws, q)
         _check("la_qk_norm_rope_backward", lib().la_qk_norm_rope_backward(
-            ctypes.byref(desc), *_rows(q), *_rows(k), *small, _ptr(dq_out), _ptr(dk_out), *_rows(dq), *_rows(dk),
-            _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), ws.numel(), st))
+            ctypes.byref(desc), *args, ws.data_ptr(), ws.numel(), st))
     return dq, dk, dq_weight, dk_weight

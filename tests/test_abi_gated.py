@@ -134,29 +134,23 @@ def test_valid_requests_reach_the_device_check(lib):
     assert rope(lib, rope_desc(B=1, Hk=1), ks=(-3, 64, 1)) == CUDA
 
 
-def test_the_binding_checks_shapes():
+def test_the_binding_checks_devices_and_shapes():
     q = torch.zeros(1, 2, 8, 64)
     g = torch.zeros(1, 2, 8)
-    with pytest.raises(ValueError, match="g must be"):
-        B.la_gated_causal(q, q, q, g[:, :, :5])
-    with pytest.raises(ValueError, match="g must be"):
-        B.la_gated_causal(q, q, q, g.double())
+    S, z = torch.zeros(1, 2, 64, 64), torch.zeros(1, 2, 64)
+    for call in (lambda: B.la_gated_causal(q, q, q, g), lambda: B.la_gated_causal_backward(q, q, q, g, q),
+                 lambda: B.la_gated_decode_step(q[:, :, :1], q[:, :, :1], q[:, :, :1], g[:, :, :1], S, z),
+                 lambda: B.la_qk_norm_rope(q, q, None, None, None, None),
+                 lambda: B.la_qk_norm_rope_backward(q, q, None, None, None, None, q, q)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
     with pytest.raises(ValueError, match="both S and z"):
-        B.la_gated_causal(q, q, q, g, S_out=torch.zeros(1, 2, 64, 64))
+        B.la_gated_causal(q, q, q, g, S_out=S)
+    with pytest.raises(ValueError, match="both S and z"):
+        B.la_gated_decode_step(q[:, :, :1], q, q, g, S, z, z_out=z)
     with pytest.raises(ValueError, match="one token"):
-        B.la_gated_decode_step(q, q, q, g, torch.zeros(1, 2, 64, 64), torch.zeros(1, 2, 64))
-    with pytest.raises(ValueError, match="CUDA device"):
-        B.la_gated_causal(q, q, q, g)
-    with pytest.raises(ValueError, match="CUDA device"):
-        B.la_gated_causal_backward(q, q, q, g, q)
-    k = torch.zeros(1, 2, 1, 64)
-    t = torch.zeros(16, 32)
-    for a in (dict(q=q, k=torch.zeros(1, 3, 1, 64)), dict(q=q.half(), k=k.half()), dict(q=q, k=k.bfloat16()),
-              dict(q=q, k=k, cos=t), dict(q=q, k=k, cos=t, sin=torch.zeros(16, 16)),
-              dict(q=q, k=k, cos=torch.zeros(16, 40), sin=torch.zeros(16, 40)),
-              dict(q=q, k=k, cos=t.double(), sin=t.double()), dict(q=q, k=k, q_weight=torch.ones(64)),
-              dict(q=q, k=k, cos=t, sin=t, positions=torch.zeros(1, 2))):
-        full = dict(q_weight=None, k_weight=None, cos=None, sin=None)
-        full.update(a)
-        with pytest.raises(ValueError):
-            B.la_qk_norm_rope(**full)
+        B.la_gated_decode_step(q, q, q, g, S, z)
+    with pytest.raises(ValueError, match="B, H, N, d"):
+        B.la_gated_causal(q[0], q, q, g)
+    with pytest.raises(ValueError, match="dtype"):
+        B.la_gated_causal(q.half(), q, q, g)

@@ -266,3 +266,24 @@ def test_capture_replay_and_other_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(res, grads))
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    q, k, v, g = inputs(1, 2, 8, 64, "bf16", "relu1", seed=30)
+    S, z = some_state(1, 2, 64, "relu1", 1)
+    good = dict(q=q, k=k, v=v, g=g)
+    for bad in (dict(k=k.float()), dict(v=v[:, :, :4].contiguous()), dict(g=g.float()), dict(g=g[:, :, :4].contiguous()),
+                dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)), dict(g=g.cpu()), dict(S_in=S, z_in=z.double()),
+                dict(S_out=S[:, :, :, :32], z_out=z), dict(out=torch.empty_like(q).float()),
+                dict(ws=torch.zeros(512, device="cuda"))):
+        with pytest.raises((ValueError, la.LaError)):
+            la.la_gated_causal(**{**good, **bad})
+    with pytest.raises(ValueError):
+        la.la_gated_causal_backward(q, k, v, g, upstream(q, 1).float())
+    with pytest.raises(la.LaError, match="UNSUPPORTED"):
+        la.la_gated_causal(q, k, v, g, phi="identity", normalize=True)
+    with pytest.raises(la.LaError, match="WORKSPACE"):
+        la.la_gated_causal_backward(q, k, v, g, q, ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(la.LaError, match="MISALIGNED"):
+        flat = torch.zeros(q.numel() + 8, device="cuda", dtype=q.dtype)
+        la.la_gated_causal(flat[1:1 + q.numel()].view(q.shape), k, v, g)

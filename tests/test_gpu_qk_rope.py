@@ -137,3 +137,27 @@ def test_capture_and_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((*got, *got_grads), (*want, *grads)))
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    q, k = packed(2, 9, 4, 2, 64, "bf16", 16)
+    t, w = torch.zeros(16, 32, device="cuda"), torch.ones(64, device="cuda")
+    good = dict(q=q, k=k, q_weight=w, k_weight=w, cos=t, sin=t)
+    la.la_qk_norm_rope(**good)
+    for bad in (dict(k=k[:, :5]), dict(k=k.float()), dict(q=q[0]), dict(sin=None), dict(sin=t[:, :16]), dict(cos=t.double()),
+                dict(q_weight=None), dict(q_weight=w[:32]), dict(k_weight=w.bfloat16()),
+                dict(cos=torch.zeros(16, 40, device="cuda"), sin=torch.zeros(16, 40, device="cuda")),
+                dict(positions=torch.zeros(2, 9, device="cuda")), dict(positions=torch.zeros(9, dtype=torch.int32, device="cuda")),
+                dict(q=q.transpose(2, 3)), dict(q_out=torch.empty(2, 9, 4, 64, device="cuda", dtype=q.dtype))):
+        with pytest.raises(ValueError):
+            la.la_qk_norm_rope(**{**good, **bad})
+    with pytest.raises(la.LaError, match="INVALID_ARG"):  # nine tokens, eight rows, no positions
+        la.la_qk_norm_rope(q, k, None, None, t[:8], t[:8])
+    with pytest.raises(la.LaError, match="UNSUPPORTED"):  # 24 channels turned
+        la.la_qk_norm_rope(q, k, None, None, t[:, :12].contiguous(), t[:, :12].contiguous())
+    with pytest.raises(ValueError, match="no weights"):
+        la.la_qk_norm_rope_backward(q, k, None, None, t, t, torch.empty(2, 4, 9, 64, device="cuda", dtype=q.dtype),
+                                    torch.empty(2, 2, 9, 64, device="cuda", dtype=q.dtype), dq_weight=w, dk_weight=w)
+    with pytest.raises(la.LaError, match="INVALID_ARG"):  # gradient rows on one another
+        dy = torch.zeros(2, 4, 9, 64, device="cuda", dtype=q.dtype)
+        la.la_qk_norm_rope_backward(q, q, w, w, t, t, dy, dy, dq=torch.zeros(2, 9, 1, 64, device="cuda", dtype=q.dtype).expand(2, 9, 4, 64))

@@ -15,8 +15,12 @@
 // W is formed in fp32 from unrounded products.
 //
 // Two sweeps: chunks in order for dq (S in registers; the state in front of
-// each chunk is written out for the last term), then chunks in reverse for
-// dk, dv, dg (G in registers).
+// each chunk is written out for the last term, and the sums over j and the
+// queries' part go to dgp), then chunks in reverse for dk, dv, dg (G in
+// registers). delta_i comes out of the same pass over the keys as dq, since
+//   dq_i = phi'(q_i) up_i e^{b_i} [ X_i + S dout_i - delta_i (Y_i + z) ],
+//   X_i = sum_j e^{-b_j} (dout_i.v_j) phi(k_j),  Y_i = sum_j e^{-b_j} phi(k_j).
+// The decay's two factors are taken apart as in the forward pass (Gates).
 #pragma once
 
 #include "gated.h"
@@ -34,7 +38,7 @@ template <typename T, int D, int PARTS, int COPIES> struct BwdSmem {
     float zs[COPIES][D];
     Gates<SH::C> gates[2];
     float row[2][SH::CG][SH::C];     // per token sums for dg
-    float cols[2][SH::RG][SH::C];    // column sums of W per row group
+    float sum[2][SH::C];             // the keys' sums of W
     float part[SH::CG][SH::C];
     float dot[2][SH::NW];
 };
@@ -156,13 +160,15 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     const float* rec = prefix ? prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
     st.seed(rec, rec + D * D, warp, lane);
     st.template publish<LO>(sm.sop[0][0], sm.zs[0], warp, lane, sm.sop[0][BQ::PARTS - 1]);
+    const int turn = (blockIdx.x + blockIdx.y) % SH::RG;
+    const int rg = (warp + turn) % SH::RG, cg = warp / SH::RG;
+    const int i0 = rg * 16, col0 = cg * SH::NCOL;
+    const bool gater = rg == 0 && cg == 0;  // the warp with the fewest keys
     GateRegs<T, C> gr;
-    if (warp == 0) {
+    if (gater) {
         load_gates<T, C>(gr, gate, nullptr, nullptr, first, N, lane);
         scan_gates<T, C>(sm.gates[0], gr, end - first, lane);
     }
-    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
-    const int i0 = rg * 16, col0 = cg * SH::NCOL;
 
     // dgp of chunk c from the sums its warps left: a suffix sum over the chunk
     auto finish = [&](int c) {
@@ -172,11 +178,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 #pragma unroll
         for (int e = R - 1; e >= 0; --e) {
             const int i = lane * R + e;
-            float s = sm.row[c & 1][0][i];
-#pragma unroll
-            for (int r = 0; r < SH::RG; ++r)
-                if (r >= i / 16) s -= sm.cols[c & 1][r][i];
-            x[e] = s + run;
+            x[e] = sm.row[c & 1][0][i] + run;
             run = x[e];
         }
         float after = run;
@@ -198,7 +200,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         __syncthreads();
         if (c + 1 < nch) {
             fetch(c + 1);
-            if (warp == 0) load_gates<T, C>(gr, gate, nullptr, nullptr, first + (c + 1) * C, N, lane);
+            if (gater) load_gates<T, C>(gr, gate, nullptr, nullptr, first + (c + 1) * C, N, lane);
         }
         if (c > 0) finish(c - 1);
         const T *qt = sm.tiles[c & 1][0], *kt = sm.tiles[c & 1][1], *vt = sm.tiles[c & 1][2], *gt = sm.tiles[c & 1][3];
@@ -210,7 +212,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 
         // dout S^T, and q . z
         float acc[NT][4] = {}, oz[4] = {};
-#pragma unroll
+#pragma unroll 1
         for (int k0 = 0; k0 < D; k0 += 16) {
             FragA<T> a;
             load_a<LD>(a, gt, i0, k0, lane);
@@ -260,23 +262,28 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 s1 += sm.part[x][i0 + g + 8];
             }
         }
-        const float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
+        const bool deep = gs.deep;
+        float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
         const float hi0 = gs.hi[i0 + g], lo0 = gs.lo[i0 + g], hi1 = gs.hi[i0 + g + 8], lo1 = gs.lo[i0 + g + 8];
-        const float qz0 = f0 * quad_sum(t == 0 ? oz[0] + oz[1] : 0.f), qz1 = f1 * quad_sum(t == 0 ? oz[2] + oz[3] : 0.f);
-        s0 *= f0;
-        s1 *= f1;
-
-        // P = phi(q) phi(k)^T and dP = dout v^T of the keys up to this row group
-        float p[SH::RG][2][4], dp[SH::RG][2][4];
-        float den0 = 0.f, den1 = 0.f, num0 = 0.f, num1 = 0.f;
+        // per row, over all keys so far: den = q . z and so on, num = sum of weights times dout . v
+        float qz0 = t == 0 ? oz[0] + oz[1] : 0.f, qz1 = t == 0 ? oz[2] + oz[3] : 0.f;
+        float zf0 = 1.f, zf1 = 1.f;  // the state's factor next to the chunk's own keys
+        if (deep) {
 #pragma unroll
-        for (int jt = 0; jt < SH::RG; ++jt) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[jt][n][e] = dp[jt][n][e] = 0.f;
-            if (jt > rg) continue;
-#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[n][0] *= f0; acc[n][1] *= f0; acc[n][2] *= f1; acc[n][3] *= f1;
+            }
+            zf0 = f0;
+            zf1 = f1;
+            f0 = f1 = 1.f;
+        }
+        float den0 = qz0 * zf0, den1 = qz1 * zf1, num0 = 0.f, num1 = 0.f;
+        float xs0 = 0.f, xs1 = 0.f, ys0 = 0.f, ys1 = 0.f;  // row sums of the operands below, for the shift of phi(k)
+        float yk[NT][4] = {};
+#pragma unroll 1
+        for (int jt = 0; jt <= rg; ++jt) {
+            float p[2][4] = {}, dp[2][4] = {};
+#pragma unroll 1
             for (int k0 = 0; k0 < D; k0 += 16) {
                 FragA<T> a;
                 FragB<T> b[2];
@@ -285,117 +292,113 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 load_bt<LD>(b, kt, jt * 16, k0, lane);
                 phi_frag<PHI>(b[0]);
                 phi_frag<PHI>(b[1]);
-                mma_step(p[jt][0], a, b[0]);
-                mma_step(p[jt][1], a, b[1]);
+                mma_step(p[0], a, b[0]);
+                mma_step(p[1], a, b[1]);
                 load_a<LD>(a, gt, i0, k0, lane);
                 load_bt<LD>(b, vt, jt * 16, k0, lane);
-                mma_step(dp[jt][0], a, b[0]);
-                mma_step(dp[jt][1], a, b[1]);
+                mma_step(dp[0], a, b[0]);
+                mma_step(dp[1], a, b[1]);
             }
+            float w[2][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int jl = n * 8 + 2 * t + e, j = jt * 16 + jl;
-                    const float w0 = jt < rg || jl <= g ? p[jt][n][e] * decay(gs, hi0, lo0, j) : 0.f;
-                    const float w1 = jt < rg || jl <= g + 8 ? p[jt][n][2 + e] * decay(gs, hi1, lo1, j) : 0.f;
-                    den0 += w0;
-                    den1 += w1;
-                    num0 += w0 * dp[jt][n][e];
-                    num1 += w1 * dp[jt][n][2 + e];
-                }
-        }
-        den0 = quad_sum(den0);
-        den1 = quad_sum(den1);
-        num0 = quad_sum(num0);
-        num1 = quad_sum(num1);
-        float up0 = 1.f, up1 = 1.f, de0 = 0.f, de1 = 0.f;
-        if (normalize) {
-            up0 = 1.f / (den0 + qz0);
-            up1 = 1.f / (den1 + qz1);
-            de0 = (num0 + s0) * up0;  // out . dout
-            de1 = (num1 + s1) * up1;
-        }
-        const int row = first + c * C + i0 + g;
-        if (cg == 0 && t == 0) {
-            // the row sum of W and the queries' part with earlier keys
-            sm.row[c & 1][0][i0 + g] = row < end ? up0 * ((num0 - de0 * den0) + (s0 - de0 * qz0)) : 0.f;
-            sm.row[c & 1][0][i0 + g + 8] = row + 8 < end ? up1 * ((num1 - de1 * den1) + (s1 - de1 * qz1)) : 0.f;
-            if (normalize) {
-                if (row < end) {
-                    up[toff + row] = up0;
-                    col[toff + row] = -de0;
-                }
-                if (row + 8 < end) {
-                    up[toff + row + 8] = up1;
-                    col[toff + row + 8] = -de1;
-                }
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float2 z = *reinterpret_cast<const float2*>(zs + col0 + 8 * n + 2 * t);
-            acc[n][0] = f0 * up0 * (acc[n][0] - de0 * z.x);
-            acc[n][1] = f0 * up0 * (acc[n][1] - de0 * z.y);
-            acc[n][2] = f1 * up1 * (acc[n][2] - de1 * z.x);
-            acc[n][3] = f1 * up1 * (acc[n][3] - de1 * z.y);
-        }
-        float rs0 = 0.f, rs1 = 0.f;  // row sums of ds, for the shift of phi(k)
-#pragma unroll
-        for (int jt = 0; jt < SH::RG; ++jt) {
-            if (jt > rg) continue;
-            float ds[2][4], cs[2][2];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int jl = n * 8 + 2 * t + e, j = jt * 16 + jl;
-                    ds[n][e] = jt < rg || jl <= g ? up0 * (dp[jt][n][e] - de0) * decay(gs, hi0, lo0, j) : 0.f;
-                    ds[n][2 + e] = jt < rg || jl <= g + 8 ? up1 * (dp[jt][n][2 + e] - de1) * decay(gs, hi1, lo1, j) : 0.f;
-                    // rows past the last token hold no query
-                    cs[n][e] = (row < end ? p[jt][n][e] * ds[n][e] : 0.f) +
-                               (row + 8 < end ? p[jt][n][2 + e] * ds[n][2 + e] : 0.f);
-                }
-            if (cg == 0) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2; ++n) {
+                const int jl = n * 8 + 2 * t, j = jt * 16 + jl;
+                const float2 x = *reinterpret_cast<const float2*>(gs.inv + j);
+                w[n][0] = w[n][2] = x.x;
+                w[n][1] = w[n][3] = x.y;
+                if (deep) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = cs[n][e];
-                        x += __shfl_xor_sync(0xffffffffu, x, 4);
-                        x += __shfl_xor_sync(0xffffffffu, x, 8);
-                        x += __shfl_xor_sync(0xffffffffu, x, 16);
-                        if (g == 0) sm.cols[c & 1][rg][jt * 16 + n * 8 + 2 * t + e] = x;
+                        w[n][e] = decay(gs, hi0, lo0, j + e);
+                        w[n][2 + e] = decay(gs, hi1, lo1, j + e);
                     }
+                }
+                if (jt == rg) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (jl + e > g) w[n][e] = 0.f;
+                        if (jl + e > g + 8) w[n][2 + e] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float a0 = p[n][e] * w[n][e], a1 = p[n][2 + e] * w[n][2 + e];
+                    den0 += a0;
+                    den1 += a1;
+                    num0 = fmaf(a0, dp[n][e], num0);
+                    num1 = fmaf(a1, dp[n][2 + e], num1);
+                    dp[n][e] *= w[n][e];
+                    dp[n][2 + e] *= w[n][2 + e];
+                    xs0 += dp[n][e];
+                    xs1 += dp[n][2 + e];
+                    ys0 += w[n][e];
+                    ys1 += w[n][2 + e];
+                }
             }
-            rs0 += (ds[0][0] + ds[0][1]) + (ds[1][0] + ds[1][1]);
-            rs1 += (ds[0][2] + ds[0][3]) + (ds[1][2] + ds[1][3]);
-            FragA<T> a;
-            make_a(a, ds[0], ds[1]);  // bf16: rounded once, like every operand of the gradients' products
+            FragA<T> ax, ay;  // bf16: rounded once, like every operand of the gradients' products
+            make_a(ax, dp[0], dp[1]);
+            make_a(ay, w[0], w[1]);
 #pragma unroll
             for (int n = 0; n < NT / 2; ++n) {
                 FragB<T> b[2];
                 load_b<LD>(b, kt, jt * 16, col0 + 16 * n, lane);
                 base_frag<PHI>(b[0]);
                 base_frag<PHI>(b[1]);
-                mma_step(acc[2 * n], a, b[0]);
-                mma_step(acc[2 * n + 1], a, b[1]);
+                mma_step(acc[2 * n], ax, b[0]);
+                mma_step(acc[2 * n + 1], ax, b[1]);
+                if (normalize) {
+                    mma_step(yk[2 * n], ay, b[0]);
+                    mma_step(yk[2 * n + 1], ay, b[1]);
+                }
             }
         }
-        rs0 = shifted<PHI> ? quad_sum(rs0) : 0.f;
-        rs1 = shifted<PHI> ? quad_sum(rs1) : 0.f;
+        den0 = quad_sum(den0);
+        den1 = quad_sum(den1);
+        // the state's part of num: q . (S dout)
+        num0 = quad_sum(num0) + s0 * zf0;
+        num1 = quad_sum(num1) + s1 * zf1;
+        float up0 = f0, up1 = f1, de0 = 0.f, de1 = 0.f;  // up: e^{b_i} / den_i over the same factor
+        const int row = first + c * C + i0 + g;
+        if (normalize) {
+            up0 = 1.f / den0;
+            up1 = 1.f / den1;
+            de0 = num0 * up0;  // out . dout
+            de1 = num1 * up1;
+            if (cg == 0 && t == 0) {
+                if (row < end) {
+                    up[toff + row] = up0 / f0;
+                    col[toff + row] = -de0;
+                }
+                if (row + 8 < end) {
+                    up[toff + row + 8] = up1 / f1;
+                    col[toff + row + 8] = -de1;
+                }
+            }
+        }
+        if (cg == 0 && t == 0) {
+            // the row sum of W with the part with earlier keys: phi(q) . dphi(q),
+            // which a normalized output makes 0
+            sm.row[c & 1][0][i0 + g] = !normalize && row < end ? up0 * num0 : 0.f;
+            sm.row[c & 1][0][i0 + g + 8] = !normalize && row + 8 < end ? up1 * num1 : 0.f;
+        }
+        xs0 = shifted<PHI> ? quad_sum(xs0) - de0 * quad_sum(ys0) : 0.f;
+        xs1 = shifted<PHI> ? quad_sum(xs1) - de1 * quad_sum(ys1) : 0.f;
+        const float dz0 = de0 * zf0, dz1 = de1 * zf1;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float x, y;
+            const float2 z = *reinterpret_cast<const float2*>(zs + col0 + 8 * n + 2 * t);
             const T* qp = qt + (i0 + g) * LD + col0 + 8 * n + 2 * t;
             T* o = dq + (size_t)row * D + col0 + 8 * n + 2 * t;
             if (row < end) {
                 load_pair(qp, x, y);
-                store_pair(o, (acc[n][0] + rs0) * phi_grad(x, PHI), (acc[n][1] + rs0) * phi_grad(y, PHI));
+                store_pair(o, up0 * (acc[n][0] + xs0 - de0 * yk[n][0] - dz0 * z.x) * slope_f<PHI>(x),
+                           up0 * (acc[n][1] + xs0 - de0 * yk[n][1] - dz0 * z.y) * slope_f<PHI>(y));
             }
             if (row + 8 < end) {
                 load_pair(qp + 8 * LD, x, y);
-                store_pair(o + 8 * D, (acc[n][2] + rs1) * phi_grad(x, PHI), (acc[n][3] + rs1) * phi_grad(y, PHI));
+                store_pair(o + 8 * D, up1 * (acc[n][2] + xs1 - de1 * yk[n][2] - dz1 * z.x) * slope_f<PHI>(x),
+                           up1 * (acc[n][3] + xs1 - de1 * yk[n][3] - dz1 * z.y) * slope_f<PHI>(y));
             }
         }
         if (c + 1 < nch) {
@@ -403,7 +406,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             if (BQ::COPIES == 1) __syncthreads();  // every warp has read the operand
             const int nb = BQ::COPIES == 2 ? ((c + 1) & 1) : 0;
             st.template publish<LO>(sm.sop[nb][0], sm.zs[nb], warp, lane, sm.sop[nb][BQ::PARTS - 1]);
-            if (warp == 0) scan_gates<T, C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
+            if (gater) scan_gates<T, C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
         }
     }
     __syncthreads();
@@ -458,12 +461,14 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             gs.from_start[i] *= gs.up[i];
         }
     };
-    if (warp == 0) {
+    const int turn = (blockIdx.x + blockIdx.y) % SH::RG;
+    const int rg = (warp + turn) % SH::RG, cg = warp / SH::RG;
+    const int j0 = rg * 16, col0 = cg * SH::NCOL;
+    const bool gater = rg == SH::RG - 1 && cg == 0;  // the warp with the fewest queries
+    if (gater) {
         load_gates<T, C>(gr, gate, up, col, first + (nch - 1) * C, N, lane);
         scan(0);
     }
-    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
-    const int j0 = rg * 16, col0 = cg * SH::NCOL;
 
     // dg of step s: what the first sweep left, the keys in front and the outside
     auto finish = [&](int s) {
@@ -473,28 +478,36 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         float outside = 0.f;
 #pragma unroll
         for (int w = 0; w < SH::NW; ++w) outside += sm.dot[s & 1][w];
-        float x[R], own = 0.f;
+        // sums over the keys in front of i, and over those from i on
+        float x[R], w[R], own = 0.f, mine = 0.f;
 #pragma unroll
         for (int e = 0; e < R; ++e) {
             const int i = lane * R + e;
-            x[e] = own;  // the keys of this lane in front of i
+            x[e] = own;
 #pragma unroll
             for (int y = 0; y < SH::CG; ++y) own += sm.row[s & 1][y][i];
         }
-        float run = own;
+#pragma unroll
+        for (int e = R - 1; e >= 0; --e) {
+            mine += sm.sum[s & 1][lane * R + e];
+            w[e] = mine;
+        }
+        float run = own, after = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, run, o);
+            const float y = __shfl_up_sync(0xffffffffu, run, o), z = __shfl_down_sync(0xffffffffu, after, o);
             if (lane >= o) run += y;
+            if (lane + o < 32) after += z;
         }
         run -= own;
+        after -= mine;
 #pragma unroll
         for (int e = 0; e < R; ++e) {
             const int i = row0 + lane * R + e;
             if (i >= end) continue;
             // nothing passes a closed gate: its gradient is exactly 0
             const bool closed = to_f32<T>(gate[i]) < -104.f;  // e^g is 0 in fp32
-            dg[i] = from_f32<T>(closed ? 0.f : dgp[i] + run + x[e] + outside);
+            dg[i] = from_f32<T>(closed ? 0.f : (dgp[i] - (w[e] + after)) + (run + x[e]) + outside);
         }
     };
 
@@ -504,7 +517,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         __syncthreads();
         if (s + 1 < nch) {
             fetch(s + 1);
-            if (warp == 0) load_gates<T, C>(gr, gate, up, col, first + (c - 1) * C, N, lane);
+            if (gater) load_gates<T, C>(gr, gate, up, col, first + (c - 1) * C, N, lane);
         }
         if (s > 0) finish(s - 1);
         const T *qt = sm.tiles[s & 1][0], *kt = sm.tiles[s & 1][1], *vt = sm.tiles[s & 1][2], *gt = sm.tiles[s & 1][3];
@@ -520,7 +533,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 
         // keys with the queries behind the chunk: phi(k) G and v G^T + h
         float av[NT][4] = {}, ak[NT][4] = {};
-#pragma unroll
+#pragma unroll 1
         for (int k0 = 0; k0 < D; k0 += 16) {
             FragA<T> a;
             FragB<T> b[2];
@@ -540,7 +553,11 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
                 mma_step(ak[2 * n + 1], a, b[1]);
             }
         }
-        const float e0 = gs.to_end[j0 + g], e1 = gs.to_end[j0 + g + 8];
+        const bool deep = gs.deep;
+        // before the rows' own factors r (2^-b_j; deep: none, and the state's
+        // part takes the whole of its decay)
+        const float e0 = deep ? gs.to_end[j0 + g] : gs.all, e1 = deep ? gs.to_end[j0 + g + 8] : gs.all;
+        const float r0 = deep ? 1.f : gs.inv[j0 + g], r1 = deep ? 1.f : gs.inv[j0 + g + 8];
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -557,20 +574,21 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             load_pair(p + 8 * LD, x, y);
             s1 += phi_f<PHI>(x) * ak[n][2] + phi_f<PHI>(y) * ak[n][3];
         }
-        s0 = quad_sum(s0);
-        s1 = quad_sum(s1);
-        if (t == 0) {
-            sm.row[s & 1][cg][j0 + g] = s0;
-            sm.row[s & 1][cg][j0 + g + 8] = s1;
+        s0 = quad_sum(s0) * r0;
+        s1 = quad_sum(s1) * r1;
+        const int row = first + c * C + j0 + g;
+        if (t == 0) {  // a key past the last token holds nothing
+            sm.row[s & 1][cg][j0 + g] = row < end ? s0 : 0.f;
+            sm.row[s & 1][cg][j0 + g + 8] = row + 8 < end ? s1 : 0.f;
         }
 
         const float hi0 = gs.hi[j0 + g], lo0 = gs.lo[j0 + g], hi1 = gs.hi[j0 + g + 8], lo1 = gs.lo[j0 + g + 8];
         float rs0 = 0.f, rs1 = 0.f;  // row sums of the pairs' gradients, for the shift of phi(q)
-#pragma unroll
-        for (int it = 0; it < SH::RG; ++it) {
-            if (it < rg) continue;
+        float ws0 = 0.f, ws1 = 0.f;  // row sums of W
+#pragma unroll 1
+        for (int it = rg; it < SH::RG; ++it) {
             float p[2][4] = {}, dp[2][4] = {};
-#pragma unroll
+#pragma unroll 1
             for (int k0 = 0; k0 < D; k0 += 16) {
                 FragA<T> a;
                 FragB<T> b[2];
@@ -587,20 +605,34 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
                 mma_step(dp[1], a, b[1]);
             }
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2; ++n) {
+                const int il = n * 8 + 2 * t, i = it * 16 + il;
+                const float2 u = *reinterpret_cast<const float2*>(gs.from_start + i);  // with 1 / den_i in it
+                const float2 cl = *reinterpret_cast<const float2*>(gs.col + i);
+                float w[4] = {u.x, u.y, u.x, u.y};
+                if (deep) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int il = n * 8 + 2 * t + e, i = it * 16 + il;
-                    const float hi = gs.hi[i], lo = gs.lo[i], u = gs.up[i], cl = gs.col[i];
-                    const float w0 = it > rg || il >= g ? u * exp2_fast((hi - hi0) + (lo - lo0)) : 0.f;
-                    const float w1 = it > rg || il >= g + 8 ? u * exp2_fast((hi - hi1) + (lo - lo1)) : 0.f;
-                    p[n][e] *= w0;
-                    p[n][2 + e] *= w1;
-                    dp[n][e] = w0 * (dp[n][e] + cl);
-                    dp[n][2 + e] = w1 * (dp[n][2 + e] + cl);
+                    for (int e = 0; e < 2; ++e) {
+                        const float q = gs.up[i + e];
+                        w[e] = q * exp2_fast((gs.hi[i + e] - hi0) + (gs.lo[i + e] - lo0));
+                        w[2 + e] = q * exp2_fast((gs.hi[i + e] - hi1) + (gs.lo[i + e] - lo1));
+                    }
                 }
-            rs0 += (dp[0][0] + dp[0][1]) + (dp[1][0] + dp[1][1]);
-            rs1 += (dp[0][2] + dp[0][3]) + (dp[1][2] + dp[1][3]);
+                if (it == rg) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (il + e < g) w[e] = 0.f;
+                        if (il + e < g + 8) w[2 + e] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dp[n][e] = w[e] * (dp[n][e] + (e & 1 ? cl.y : cl.x));
+                    (e < 2 ? ws0 : ws1) += p[n][e] * dp[n][e];
+                    (e < 2 ? rs0 : rs1) += dp[n][e];
+                    p[n][e] *= w[e];
+                }
+            }
             FragA<T> ap, ad;  // bf16: rounded once
             make_a(ap, p[0], p[1]);
             make_a(ad, dp[0], dp[1]);
@@ -617,7 +649,14 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
                 mma_step(ak[2 * n + 1], ad, b[1]);
             }
         }
-        const int row = first + c * C + j0 + g;
+        if (cg == 0) {
+            ws0 = quad_sum(ws0) * r0;
+            ws1 = quad_sum(ws1) * r1;
+            if (t == 0) {
+                sm.sum[s & 1][j0 + g] = row < end ? ws0 : 0.f;
+                sm.sum[s & 1][j0 + g + 8] = row + 8 < end ? ws1 : 0.f;
+            }
+        }
         rs0 = shifted<PHI> ? quad_sum(rs0) : 0.f;
         rs1 = shifted<PHI> ? quad_sum(rs1) : 0.f;
 #pragma unroll
@@ -627,13 +666,13 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             const T* kp = kt + (j0 + g) * LD + cc;
             if (row < end) {
                 load_pair(kp, x, y);
-                store_pair(dk + (size_t)row * D + cc, (ak[n][0] + rs0) * phi_grad(x, PHI), (ak[n][1] + rs0) * phi_grad(y, PHI));
-                store_pair(dv + (size_t)row * D + cc, av[n][0], av[n][1]);
+                store_pair(dk + (size_t)row * D + cc, r0 * (ak[n][0] + rs0) * slope_f<PHI>(x), r0 * (ak[n][1] + rs0) * slope_f<PHI>(y));
+                store_pair(dv + (size_t)row * D + cc, r0 * av[n][0], r0 * av[n][1]);
             }
             if (row + 8 < end) {
                 load_pair(kp + 8 * LD, x, y);
-                store_pair(dk + (size_t)(row + 8) * D + cc, (ak[n][2] + rs1) * phi_grad(x, PHI), (ak[n][3] + rs1) * phi_grad(y, PHI));
-                store_pair(dv + (size_t)(row + 8) * D + cc, av[n][2], av[n][3]);
+                store_pair(dk + (size_t)(row + 8) * D + cc, r1 * (ak[n][2] + rs1) * slope_f<PHI>(x), r1 * (ak[n][3] + rs1) * slope_f<PHI>(y));
+                store_pair(dv + (size_t)(row + 8) * D + cc, r1 * av[n][2], r1 * av[n][3]);
             }
         }
         if (s + 1 < nch) {
@@ -641,7 +680,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             if (SH::SB == 1) __syncthreads();  // every warp has read the operand
             const int nb = SH::SB == 2 ? ((s + 1) & 1) : 0;
             st.publish(sm.sop[nb][0], sm.zs[nb], warp, lane);
-            if (warp == 0) scan(s + 1);
+            if (gater) scan(s + 1);
         }
     }
     __syncthreads();

@@ -12,14 +12,15 @@ namespace gated {
 // it into RG row groups of 16 tokens and CG column groups of NCOL channels.
 // The state S (d x d, fp32) lives in the warps' registers: SRT row tiles of
 // 16, each cut into SCG column groups of SN columns. SB: operand copies of S
-// in shared memory (one copy costs one more barrier per chunk).
+// in shared memory (one copy costs one more barrier per chunk, but leaves room
+// for a third CTA per SM at d = 64 in bf16).
 // fp32 rows are twice as long, so d >= 64 takes chunks of 32 tokens to keep
 // two stages of tiles within the shared memory of an SM.
 template <typename T, int D> struct Shape {
     static constexpr bool F32 = sizeof(T) == 4;
     static constexpr int C = F32 && D >= 64 ? 32 : 64;
     static constexpr int NW = D == 128 ? 8 : 4;
-    static constexpr int SB = F32 && D == 128 ? 1 : 2;
+    static constexpr int SB = (F32 && D == 128) || (!F32 && D == 64) ? 1 : 2;
     static constexpr int THREADS = NW * 32;
     static constexpr int LD = D + (F32 ? 8 : 8);
     static constexpr int EPV = 16 / sizeof(T);
@@ -34,17 +35,23 @@ template <typename T, int D> struct Shape {
 };
 
 // The gates of one chunk, from b_i = log2 of the product of the chunk's gates
-// up to token i. b is formed in 64 bits and kept as hi + lo, so that
-// b_i - b_j keeps 2^-24 of its own size however far the chunk has decayed; a
-// closed gate (-inf) counts as 2^-14000, far below any product that fp32 can
-// hold, and drops out of every difference behind it exactly.
+// up to token i. b is formed in 64 bits. The decay from key j to query i,
+// 2^(b_i - b_j), is used as the product of from_start_i and inv_j, one factor
+// per row and one per column, while no b of the chunk lies below -90 (deep = 0),
+// where both stay well inside fp32. In a deep chunk it is formed per pair from
+// b = hi + lo, which keeps 2^-24 of the difference however far the chunk has
+// decayed; a closed gate (-inf) counts as 2^-14000, far below any product that
+// fp32 can hold, and drops out of every difference behind it exactly.
 template <int C> struct alignas(16) Gates {
     float hi[C], lo[C];
     float from_start[C];  // 2^b_i; 0 past the last token
+    float inv[C];         // 2^-b_j
     float to_end[C];      // 2^(b_last - b_j); 0 past the last token
     float up[C], col[C];  // gradients: 1 / den_i and -(out_i . dout_i); 0 past the last token
     float all;            // 2^b_last
+    int deep;
 };
+constexpr float kDeep = -90.f;
 constexpr double kLog2e = 1.4426950408889634;
 constexpr double kClosed = -14000.0;
 
@@ -82,6 +89,13 @@ __device__ __forceinline__ void load_gates(GateRegs<T, C>& r, const T* g, const 
         }
     }
 }
+// 2^b from 64 bits: the fraction alone goes through the fp32 function.
+__device__ __forceinline__ float pow2(double b) {
+    const float n = fminf(fmaxf(rintf((float)b), -126.f), 128.f);  // 128: infinity
+    const float f = exp2_fast((float)(b - (double)n));
+    return b < -126.0 ? 0.f : f * __int_as_float(((int)n + 127) << 23);  // a NaN stays
+}
+
 // A whole warp. Returns the chunk's log2 sum (every lane).
 template <typename T, int C>
 __device__ __forceinline__ double scan_gates(Gates<C>& s, const GateRegs<T, C>& r, int valid, int lane) {
@@ -101,25 +115,32 @@ __device__ __forceinline__ double scan_gates(Gates<C>& s, const GateRegs<T, C>& 
     }
     const double before = run - x[R - 1];
     const double last = __shfl_sync(0xffffffffu, run, 31);
+    bool low = false;
 #pragma unroll
     for (int e = 0; e < R; ++e) {
         const int i = lane * R + e;
         const double b = before + x[e];
         const float hi = (float)b;
         const bool in = i < valid;
+        low = low || hi < kDeep;
         s.hi[i] = hi;
         s.lo[i] = (float)(b - (double)hi);
-        s.from_start[i] = in ? exp2_fast((float)b) : 0.f;
-        s.to_end[i] = in ? exp2_fast((float)(last - b)) : 0.f;
+        s.from_start[i] = in ? pow2(b) : 0.f;
+        s.inv[i] = pow2(-b);
+        s.to_end[i] = in ? pow2(last - b) : 0.f;
         s.up[i] = r.up[e];
         s.col[i] = r.col[e];
     }
-    if (lane == 0) s.all = exp2_fast((float)last);
+    low = __any_sync(0xffffffffu, low);
+    if (lane == 0) {
+        s.all = pow2(last);
+        s.deep = low;
+    }
     return last;
 }
 
-// The decay from key j to query i of a chunk, 0 for j > i. The differences of
-// -inf sums cannot occur: closed gates are finite here.
+// The decay between two tokens of a deep chunk, from what (hi, lo) of the one
+// and token j are apart.
 template <int C> __device__ __forceinline__ float decay(const Gates<C>& s, float hi_i, float lo_i, int j) {
     return exp2_fast((hi_i - s.hi[j]) + (lo_i - s.lo[j]));
 }

@@ -4,8 +4,9 @@
 // Chunk by chunk, with b_i the log of the product of a chunk's gates up to i:
 //   out_i = [ sum_{j <= i} e^{b_i - b_j} (phi(q_i).phi(k_j)) v_j + e^{b_i} phi(q_i) S ] / (the same with v = 1)
 //   S    <- e^{b_last} S + sum_j e^{b_last - b_j} phi(k_j) (x) v_j
-// Every exponent is a sum of gates between two tokens, so nothing overflows
-// however fast or slow the decay is.
+// e^{b_i - b_j} is taken as e^{b_i} e^{-b_j} where the chunk's sums allow it
+// (gated_common.cuh, Gates): one factor per key inside, one per query at the
+// end, and the state's part needs none of its own.
 
 #pragma once
 
@@ -32,7 +33,7 @@ template <typename T, int D> struct StateSmem {
 // The outputs of one block of a head's chunks, from the state in front of the
 // block (a record of `prefix`, or S_in / z_in, or nothing).
 template <typename T, int D, int PHI>
-__global__ void __launch_bounds__(Shape<T, D>::THREADS)
+__global__ void __launch_bounds__(Shape<T, D>::THREADS, sizeof(T) == 2 && D == 64 ? 3 : 1)
 gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
                    const float* prefix, const float* S_in, const float* z_in, int N, int block_tokens, int nblk,
                    int normalize, T* __restrict__ out, float* S_out, float* z_out) {
@@ -65,22 +66,25 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         st.seed(S_in ? S_in + (size_t)bh * D * D : nullptr, z_in ? z_in + (size_t)bh * D : nullptr, warp, lane);
     }
     st.publish(sm.sop[0], sm.zs[0], warp, lane);
+    // the warps' row groups differ in work (a group sees the keys before it):
+    // CTAs of an SM start them at different warps, and the gates go to the
+    // warp with the first group
+    const int turn = (blockIdx.x + blockIdx.y) % SH::RG;
+    const int rg = (warp + turn) % SH::RG, cg = warp / SH::RG;
+    const int i0 = rg * 16, col0 = cg * SH::NCOL;
+    const bool gater = rg == 0 && cg == 0;
     GateRegs<T, C> gr;
-    if (warp == 0) {
+    if (gater) {
         load_gates<T, C>(gr, gate, nullptr, nullptr, first, N, lane);
         scan_gates<T, C>(sm.gates[0], gr, end - first, lane);
     }
-    // the warps' row groups differ in work (a group sees the keys before it):
-    // CTAs of an SM start them at different warps
-    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
-    const int i0 = rg * 16, col0 = cg * SH::NCOL;
 
     for (int c = 0; c < nch; ++c) {
         cp_async_wait<0>();
         __syncthreads();
         if (c + 1 < nch) {
             fetch(c + 1);
-            if (warp == 0) load_gates<T, C>(gr, gate, nullptr, nullptr, first + (c + 1) * C, N, lane);
+            if (gater) load_gates<T, C>(gr, gate, nullptr, nullptr, first + (c + 1) * C, N, lane);
         }
         const T *qt = sm.tiles[c & 1][0], *kt = sm.tiles[c & 1][1], *vt = sm.tiles[c & 1][2];
         const Gates<C>& gs = sm.gates[c & 1];
@@ -88,9 +92,12 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         const T* sop = sm.sop[sb];
         const float* zs = sm.zs[sb];
 
+        // The loops over the channels and the key groups stay rolled (by pairs
+        // of steps): a block often has only a few chunks, and then the time to
+        // fetch the code counts (1 x 4 x 1531 x 32 fp32: FIGURE).
         constexpr int NT = SH::NCOL / 8;
         float o[NT][4] = {}, oz[4] = {};
-#pragma unroll
+#pragma unroll 2
         for (int k0 = 0; k0 < D; k0 += 16) {
             FragA<T> a;
             load_a<LD>(a, qt, i0, k0, lane);
@@ -108,19 +115,24 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 mma_step(oz, a, b);
             }
         }
-        const float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            o[n][0] *= f0; o[n][1] *= f0; o[n][2] *= f1; o[n][3] *= f1;
-        }
+        const bool deep = gs.deep;
+        float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
         // z's product sits in columns 0 and 1 (t == 0); the row sums below add over the quad
-        float den0 = (t == 0 ? oz[0] + oz[1] : 0.f) * f0, den1 = (t == 0 ? oz[2] + oz[3] : 0.f) * f1;
+        float den0 = t == 0 ? oz[0] + oz[1] : 0.f, den1 = t == 0 ? oz[2] + oz[3] : 0.f;
         const float hi0 = gs.hi[i0 + g], lo0 = gs.lo[i0 + g], hi1 = gs.hi[i0 + g + 8], lo1 = gs.lo[i0 + g + 8];
+        if (deep) {
 #pragma unroll
-        for (int jt = 0; jt < SH::RG; ++jt) {
-            if (jt > rg) break;
+            for (int n = 0; n < NT; ++n) {
+                o[n][0] *= f0; o[n][1] *= f0; o[n][2] *= f1; o[n][3] *= f1;
+            }
+            den0 *= f0;
+            den1 *= f1;
+            f0 = f1 = 1.f;
+        }
+#pragma unroll 1
+        for (int jt = 0; jt <= rg; ++jt) {
             float p[2][4] = {};
-#pragma unroll
+#pragma unroll 2
             for (int k0 = 0; k0 < D; k0 += 16) {
                 FragA<T> a;
                 FragB<T> b[2];
@@ -133,13 +145,26 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 mma_step(p[1], a, b[1]);
             }
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2; ++n) {
+                const int jl = n * 8 + 2 * t, j = jt * 16 + jl;
+                if (deep) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int jl = n * 8 + 2 * t + e, j = jt * 16 + jl;
-                    p[n][e] = jt < rg || jl <= g ? p[n][e] * decay(gs, hi0, lo0, j) : 0.f;
-                    p[n][2 + e] = jt < rg || jl <= g + 8 ? p[n][2 + e] * decay(gs, hi1, lo1, j) : 0.f;
+                    for (int e = 0; e < 2; ++e) {
+                        p[n][e] *= decay(gs, hi0, lo0, j + e);
+                        p[n][2 + e] *= decay(gs, hi1, lo1, j + e);
+                    }
+                } else {
+                    const float2 w = *reinterpret_cast<const float2*>(gs.inv + j);
+                    p[n][0] *= w.x; p[n][1] *= w.y; p[n][2] *= w.x; p[n][3] *= w.y;
                 }
+                if (jt == rg) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (jl + e > g) p[n][e] = 0.f;
+                        if (jl + e > g + 8) p[n][2 + e] = 0.f;
+                    }
+                }
+            }
             // bf16: the weights are rounded once, as in the chunked forms without a
             // gate, and the denominator sums the rounded ones, so that the
             // output is a mean of the values with these very weights
@@ -157,7 +182,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 mma_step(o[2 * n + 1], a, b[1]);
             }
         }
-        float r0 = 1.f, r1 = 1.f;
+        float r0 = f0, r1 = f1;  // the same factor over and under the line of a normalized output
         if (normalize) {
             r0 = 1.f / quad_sum(den0);
             r1 = 1.f / quad_sum(den1);
@@ -180,7 +205,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             if (c + 1 < nch) {
                 const int nb = SH::SB == 2 ? ((c + 1) & 1) : 0;
                 st.publish(sm.sop[nb], sm.zs[nb], warp, lane);
-                if (warp == 0) scan_gates<T, C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
+                if (gater) scan_gates<T, C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
             }
         }
     }

@@ -110,7 +110,24 @@ __device__ __forceinline__ void split_a(FragA<float>& hi, FragA<float>&, const f
 // ---- feature map on operands ------------------------------------------------------
 // Rounded to the operand's type: relu(x) + 1 in packed bf16 arithmetic equals
 // the fp32 value rounded once.
-template <int PHI> __device__ __forceinline__ float phi_f(float x) { return phi_apply(x, PHI); }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// e^x of x <= 0 as 2^(x log2 e): 2^-22 of the value, and 2^-24 |x| from the product's rounding.
+__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * 1.4426950408889634f); }
+template <int PHI> __device__ __forceinline__ float phi_f(float x) {
+    if (PHI == PHI_RELU1) return fmaxf(x, 0.f) + 1.f;
+    if (PHI == PHI_ELU1) return x > 0.f ? x + 1.f : exp_fast(x);
+    return x;
+}
+// d phi / dx, at 0 as in phi_grad (common.cuh)
+template <int PHI> __device__ __forceinline__ float slope_f(float x) {
+    if (PHI == PHI_RELU1) return x > 0.f ? 1.f : 0.f;
+    if (PHI == PHI_ELU1) return x > 0.f ? 1.f : exp_fast(x);
+    return 1.f;
+}
 template <int PHI> __device__ __forceinline__ uint32_t phi_pair(uint32_t w) {
     if (PHI == PHI_RELU1) {
         __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&w);
@@ -128,7 +145,7 @@ template <int PHI> __device__ __forceinline__ uint32_t phi_pair(uint32_t w) {
 template <int PHI> constexpr bool shifted = PHI != PHI_IDENTITY;
 template <int PHI> __device__ __forceinline__ float base_f(float x) {
     if (PHI == PHI_RELU1) return fmaxf(x, 0.f);
-    if (PHI == PHI_ELU1) return x > 0.f ? x : expf(x) - 1.f;
+    if (PHI == PHI_ELU1) return x > 0.f ? x : exp_fast(x) - 1.f;
     return x;
 }
 template <int PHI> __device__ __forceinline__ void base_frag(FragB<__nv_bfloat16>& b) {
@@ -285,11 +302,6 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ float quad_sum(float x) {  // over the 4 lanes that share a row
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 }  // namespace gated

@@ -103,9 +103,8 @@ typedef struct {
 /* Bytes of workspace `op` needs for `desc` (chunk is used by LA_OP_CAUSAL and
  * LA_OP_PREFIX only; it must be 64 or 128 for those and is ignored
  * otherwise). Returns 0 when the request is invalid or unsupported, and for
- * requests that need none (LA_OP_DECODE; LA_OP_GATED_CAUSAL when every head is
- * one block, that is for short rows or many heads). A valid request that
- * needs a workspace always gets a non-zero size. Host function; launches nothing. The work is
+ * ops that need none (LA_OP_DECODE). A valid request that needs a workspace
+ * always gets a non-zero size. Host function; launches nothing. The work is
  * split to fill the SMs of the current device, so the size is for that
  * device (with no CUDA device, for a 148-SM B200): a workspace sized on one
  * device can be too small for another, which the call then rejects with
@@ -219,7 +218,7 @@ LA_API la_status la_decode_step(const la_desc* desc, const void* q, const void* 
  * both or neither (NULL: an empty one): a prompt can be given in pieces.
  * S_out, z_out: float32 state after the last token, both or neither (NULL: not
  * wanted), ready for la_gated_decode_step. They may be S_in, z_in.
- * ws: op LA_OP_GATED_CAUSAL; may be NULL when la_workspace_size is 0. */
+ * ws: op LA_OP_GATED_CAUSAL. */
 LA_API la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, const void* v,
                                  const void* g, const float* S_in, const float* z_in, void* out,
                                  float* S_out, float* z_out, void* ws, size_t ws_bytes, void* stream);

@@ -441,10 +441,8 @@ def la_gated_causal(q, k, v, g, S_in=None, z_in=None, out=None, S_out=None, z_ou
                 args += (_arg("S", S, torch.float32, (B, H, d, d), i), _arg("z", z, torch.float32, (B, H, d), i))
         out = torch.empty_like(q) if out is None else out
         args.insert(6, _arg("out", out, dt, shape, i))
-        if ws is None and la_workspace_size(desc, "gated_causal"):
-            ws = workspace(desc, "gated_causal", device=q.device)
-        args += (None, 0) if ws is None else (_ws(ws, q).data_ptr(), ws.numel())
-        _check("la_gated_causal", lib().la_gated_causal(ctypes.byref(desc), *args, st))
+        ws = workspace(desc, "gated_causal", device=q.device) if ws is None else _ws(ws, q)
+        _check("la_gated_causal", lib().la_gated_causal(ctypes.byref(desc), *args, ws.data_ptr(), ws.numel(), st))
     return out
 
 

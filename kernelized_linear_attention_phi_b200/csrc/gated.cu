@@ -1,12 +1,60 @@
 // Gated linear attention: the scan of block states, the one-token step and
 // the choice of the element type's kernels (gated_bf16.cu, gated_f32.cu).
 
-#include "common.cuh"
+#include "gate_scan.cuh"
 #include "gated.h"
+#include "gated_common.cuh"
 #include "launch_util.h"
 
 namespace la {
 namespace {
+
+// The gates of every chunk of C tokens, as the sweeps take them (a warp per chunk).
+template <typename T, int C>
+__global__ void __launch_bounds__(128) gates_kernel(const T* __restrict__ gate, int N, int nch, uint8_t* __restrict__ out) {
+    using namespace gated;
+    constexpr int R = C / 32;
+    using Raw = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+    const int c = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32, bh = blockIdx.y;
+    pdl_wait();
+    if (c >= nch) return;
+    const Raw* g = reinterpret_cast<const Raw*>(gate) + (size_t)bh * N;
+    Raw raw[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const int i = c * C + lane * R + e;
+        raw[e] = i < N ? g[i] : Raw(0);
+    }
+    const GateSums<R> q = sum_gates<R>(raw, lane);
+    Gates<C>& s = *reinterpret_cast<Gates<C>*>(out + ((size_t)bh * nch + c) * kGateBytes<C>);
+    bool low = false;
+    const float whole = q.bad >> R ? NAN : 0.f;
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const int i = lane * R + e;
+        const float nan = q.bad & (1 << e) ? NAN : 0.f;
+        const float2 b = gate_float2(q.b[e]);
+        const bool in = c * C + i < N;
+        low = low || b.x < kDeep;
+        s.hi[i] = b.x + nan;
+        s.lo[i] = b.y;
+        s.from_start[i] = in ? gate_pow2(q.b[e]) + nan : 0.f;
+        s.inv[i] = gate_pow2(-q.b[e]) + nan;
+        s.to_end[i] = in ? gate_pow2(q.last - q.b[e]) + whole : 0.f;
+    }
+    low = __any_sync(0xffffffffu, low);
+    if (lane == 0) {
+        s.all = gate_pow2(q.last) + whole;
+        s.deep = low;
+    }
+}
+
+template <typename T, int C>
+cudaError_t launch_gates(const Problem& p, const void* g, uint8_t* out, cudaStream_t st) {
+    const int nch = (p.N + C - 1) / C;
+    return launch_pdl(gates_kernel<T, C>, dim3((unsigned)((nch + 3) / 4), (unsigned)p.bh()), dim3(128), 0, st,
+                      static_cast<const T*>(g), p.N, nch, out);
+}
 
 // Record blk of each head becomes the state in front of the block (REVERSE:
 // behind it), from S_in / z_in or zero; the state past the other end goes to
@@ -168,35 +216,45 @@ cudaError_t gated_scan(const Problem& p, bool reverse, float* rec, const float* 
     return launch_pdl(gated_scan_kernel<false>, grid, dim3(256), 0, st, rec, dec, nblk, dd, sf, S_in, z_in, S_out, z_out);
 }
 
+cudaError_t gated_gates(const Problem& p, const void* g, uint8_t* out, cudaStream_t st) {
+    if (p.dtype == DT_BF16) return launch_gates<__nv_bfloat16, 64>(p, g, out, st);
+    return gated_chunk(p) == 32 ? launch_gates<float, 32>(p, g, out, st) : launch_gates<float, 64>(p, g, out, st);
+}
+size_t gated_gate_bytes(const Problem& p) {
+    const size_t one = gated_chunk(p) == 32 ? gated::kGateBytes<32> : gated::kGateBytes<64>;
+    return (size_t)p.bh() * ((p.N + gated_chunk(p) - 1) / gated_chunk(p)) * one;
+}
+
 // fp32 d >= 64: chunks of 32 tokens (gated_common.cuh, Shape)
 int gated_chunk(const Problem& p) { return p.dtype == DT_F32 && p.d >= 64 ? 32 : 64; }
 size_t gated_chunk_state_bytes(const Problem& p) {
     return (size_t)p.d * p.d * p.elem_bytes() + (size_t)p.d * sizeof(float);
 }
 
-cudaError_t gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g, const float* prefix,
+cudaError_t gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const float* prefix,
                         const float* S_in, const float* z_in, int block_tokens, int nblk, void* out, float* S_out,
                         float* z_out, cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_sweep_t<float> : gated_sweep_t<__nv_bfloat16>;
-    return f(p, q, k, v, g, prefix, S_in, z_in, block_tokens, nblk, out, S_out, z_out, st);
+    return f(p, q, k, v, gates, prefix, S_in, z_in, block_tokens, nblk, out, S_out, z_out, st);
 }
-cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const void* y, const void* g, const float* up,
+cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* wq,
+                         const float* up,
                          const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
                          cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_states_t<float> : gated_states_t<__nv_bfloat16>;
-    return f(p, reverse, x, y, g, up, col, block_tokens, nblk, blk0, count, rec, dec, st);
+    return f(p, reverse, x, y, gates, wq, up, col, block_tokens, nblk, blk0, count, rec, dec, st);
 }
-cudaError_t gated_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
-                        const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+cudaError_t gated_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
+                        const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,
                         void* chunk_state, cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_bwd_q_t<float> : gated_bwd_q_t<__nv_bfloat16>;
-    return f(p, q, k, v, g, dout, prefix, block_tokens, nblk, dq, up, col, dgp, chunk_state, st);
+    return f(p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, wq, up, col, dgp, chunk_state, st);
 }
-cudaError_t gated_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
-                         const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
+cudaError_t gated_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates, const void* dout,
+                         const float* suffix, int block_tokens, int nblk, const float* wq, const float* up, const float* col,
                          const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_bwd_kv_t<float> : gated_bwd_kv_t<__nv_bfloat16>;
-    return f(p, q, k, v, g, dout, suffix, block_tokens, nblk, up, col, dgp, chunk_state, dk, dv, dg, st);
+    return f(p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, wq, up, col, dgp, chunk_state, dk, dv, dg, st);
 }
 
 }  // namespace la

@@ -126,9 +126,9 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
 
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS)
-gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
-                   const T* __restrict__ dout, const float* prefix, int N, int block_tokens, int nblk, int normalize,
-                   T* __restrict__ dq, float* __restrict__ up, float* __restrict__ col, float* __restrict__ dgp,
+gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                   const uint8_t* __restrict__ gates, const T* __restrict__ dout, const float* prefix, int N, int block_tokens, int nblk, int normalize,
+                   T* __restrict__ dq, float* __restrict__ wq, float* __restrict__ up, float* __restrict__ col, float* __restrict__ dgp,
                    uint8_t* __restrict__ chunk_state) {
     using SH = Shape<T, D>;
     using BQ = BwdQ<T, D, PHI>;
@@ -142,13 +142,14 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     const int nch = (end - first + C - 1) / C;
     const size_t off = (size_t)bh * N * D, toff = (size_t)bh * N;
     q += off; k += off; v += off; dout += off; dq += off;
-    gate += toff;
+    gates += ((size_t)bh * ((N + C - 1) / C) + first / C) * kGateBytes<C>;
     dgp += toff;
     uint8_t* states = chunk_state + ((size_t)bh * ((N + C - 1) / C) + first / C) * ChunkState<T, D>::BYTES;
     pdl_wait();
 
     auto fetch = [&](int c) {
         const int row0 = first + c * C;
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, nullptr, row0, N);
         load_tile<SH, T, D>(sm.tiles[c & 1][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[c & 1][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[c & 1][2], v, row0, N);
@@ -160,15 +161,8 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     const float* rec = prefix ? prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
     st.seed(rec, rec + D * D, warp, lane);
     st.template publish<LO>(sm.sop[0][0], sm.zs[0], warp, lane, sm.sop[0][BQ::PARTS - 1]);
-    const int turn = (blockIdx.x + blockIdx.y) % SH::RG;
-    const int rg = (warp + turn) % SH::RG, cg = warp / SH::RG;
+    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
     const int i0 = rg * 16, col0 = cg * SH::NCOL;
-    const bool gater = rg == 0 && cg == 0;  // the warp with the fewest keys
-    GateRegs<T, C> gr;
-    if (gater) {
-        load_gates<T, C>(gr, gate, nullptr, nullptr, first, N, lane);
-        scan_gates<T, C>(sm.gates[0], gr, end - first, lane);
-    }
 
     // dgp of chunk c from the sums its warps left: a suffix sum over the chunk
     auto finish = [&](int c) {
@@ -198,10 +192,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     for (int c = 0; c < nch; ++c) {
         cp_async_wait<0>();
         __syncthreads();
-        if (c + 1 < nch) {
-            fetch(c + 1);
-            if (gater) load_gates<T, C>(gr, gate, nullptr, nullptr, first + (c + 1) * C, N, lane);
-        }
+        if (c + 1 < nch) fetch(c + 1);
         if (c > 0) finish(c - 1);
         const T *qt = sm.tiles[c & 1][0], *kt = sm.tiles[c & 1][1], *vt = sm.tiles[c & 1][2], *gt = sm.tiles[c & 1][3];
         const Gates<C>& gs = sm.gates[c & 1];
@@ -212,7 +203,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 
         // dout S^T, and q . z
         float acc[NT][4] = {}, oz[4] = {};
-#pragma unroll 1
+#pragma unroll(SH::F32 ? 1 : D / 16)
         for (int k0 = 0; k0 < D; k0 += 16) {
             FragA<T> a;
             load_a<LD>(a, gt, i0, k0, lane);
@@ -283,7 +274,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 #pragma unroll 1
         for (int jt = 0; jt <= rg; ++jt) {
             float p[2][4] = {}, dp[2][4] = {};
-#pragma unroll 1
+#pragma unroll(SH::F32 ? 1 : D / 16)
             for (int k0 = 0; k0 < D; k0 += 16) {
                 FragA<T> a;
                 FragB<T> b[2];
@@ -365,11 +356,13 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             de0 = num0 * up0;  // out . dout
             de1 = num1 * up1;
             if (cg == 0 && t == 0) {
-                if (row < end) {
+                if (row < end) {  // e^{b_i} / den_i is what the second sweep takes; the bare 1 / den_i serves a deep chunk
+                    wq[toff + row] = deep ? up0 * zf0 : up0;
                     up[toff + row] = up0 / f0;
                     col[toff + row] = -de0;
                 }
                 if (row + 8 < end) {
+                    wq[toff + row + 8] = deep ? up1 * zf1 : up1;
                     up[toff + row + 8] = up1 / f1;
                     col[toff + row + 8] = -de1;
                 }
@@ -402,11 +395,10 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             }
         }
         if (c + 1 < nch) {
-            st.template update<PHI>(kt, vt, gs.to_end, nullptr, gs.all, warp, lane);
+            st.template update<PHI>(kt, vt, gs.to_end, nullptr, true, gs.all, warp, lane);
             if (BQ::COPIES == 1) __syncthreads();  // every warp has read the operand
             const int nb = BQ::COPIES == 2 ? ((c + 1) & 1) : 0;
             st.template publish<LO>(sm.sop[nb][0], sm.zs[nb], warp, lane, sm.sop[nb][BQ::PARTS - 1]);
-            if (gater) scan_gates<T, C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
         }
     }
     __syncthreads();
@@ -416,8 +408,8 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS)
 gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
-                    const T* __restrict__ dout, const float* suffix, int N, int block_tokens, int nblk,
-                    const float* up, const float* col, const float* __restrict__ dgp,
+                    const uint8_t* __restrict__ gates, const T* __restrict__ dout, const float* suffix, int N, int block_tokens, int nblk,
+                    const float* wq, const float* up, const float* col, const float* __restrict__ dgp,
                     const uint8_t* __restrict__ chunk_state, T* __restrict__ dk, T* __restrict__ dv, T* __restrict__ dg) {
     using SH = Shape<T, D>;
     constexpr int C = SH::C, LD = SH::LD, NT = SH::NCOL / 8;
@@ -430,16 +422,21 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     const size_t off = (size_t)bh * N * D, toff = (size_t)bh * N;
     q += off; k += off; v += off; dout += off; dk += off; dv += off;
     gate += toff;
+    gates += ((size_t)bh * ((N + C - 1) / C) + first / C) * kGateBytes<C>;
     dgp += toff;
     dg += toff;
-    if (up) up += toff;
-    if (col) col += toff;
+    if (wq) {
+        wq += toff;
+        up += toff;
+        col += toff;
+    }
     const uint8_t* states = chunk_state + ((size_t)bh * ((N + C - 1) / C) + first / C) * ChunkState<T, D>::BYTES;
     pdl_wait();
 
     // step s of the sweep is chunk nch - 1 - s
     auto fetch = [&](int s) {
         const int row0 = first + (nch - 1 - s) * C;
+        load_gates<C>(sm.gates[s & 1], gates + (size_t)(nch - 1 - s) * kGateBytes<C>, wq, up, col, row0, N);
         load_tile<SH, T, D>(sm.tiles[s & 1][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[s & 1][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[s & 1][2], v, row0, N);
@@ -451,24 +448,8 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     const float* rec = suffix ? suffix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
     st.seed(rec, rec + D * D, warp, lane);
     st.publish(sm.sop[0][0], sm.zs[0], warp, lane);
-    GateRegs<T, C> gr;
-    auto scan = [&](int s) {
-        Gates<C>& gs = sm.gates[s & 1];
-        scan_gates<T, C>(gs, gr, end - first - (nch - 1 - s) * C, lane);
-#pragma unroll
-        for (int e = 0; e < C / 32; ++e) {
-            const int i = lane * (C / 32) + e;
-            gs.from_start[i] *= gs.up[i];
-        }
-    };
-    const int turn = (blockIdx.x + blockIdx.y) % SH::RG;
-    const int rg = (warp + turn) % SH::RG, cg = warp / SH::RG;
+    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
     const int j0 = rg * 16, col0 = cg * SH::NCOL;
-    const bool gater = rg == SH::RG - 1 && cg == 0;  // the warp with the fewest queries
-    if (gater) {
-        load_gates<T, C>(gr, gate, up, col, first + (nch - 1) * C, N, lane);
-        scan(0);
-    }
 
     // dg of step s: what the first sweep left, the keys in front and the outside
     auto finish = [&](int s) {
@@ -515,10 +496,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         const int c = nch - 1 - s;
         cp_async_wait<0>();
         __syncthreads();
-        if (s + 1 < nch) {
-            fetch(s + 1);
-            if (gater) load_gates<T, C>(gr, gate, up, col, first + (c - 1) * C, N, lane);
-        }
+        if (s + 1 < nch) fetch(s + 1);
         if (s > 0) finish(s - 1);
         const T *qt = sm.tiles[s & 1][0], *kt = sm.tiles[s & 1][1], *vt = sm.tiles[s & 1][2], *gt = sm.tiles[s & 1][3];
         const Gates<C>& gs = sm.gates[s & 1];
@@ -533,7 +511,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 
         // keys with the queries behind the chunk: phi(k) G and v G^T + h
         float av[NT][4] = {}, ak[NT][4] = {};
-#pragma unroll 1
+#pragma unroll(SH::F32 ? 1 : D / 16)
         for (int k0 = 0; k0 < D; k0 += 16) {
             FragA<T> a;
             FragB<T> b[2];
@@ -588,7 +566,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 #pragma unroll 1
         for (int it = rg; it < SH::RG; ++it) {
             float p[2][4] = {}, dp[2][4] = {};
-#pragma unroll 1
+#pragma unroll(SH::F32 ? 1 : D / 16)
             for (int k0 = 0; k0 < D; k0 += 16) {
                 FragA<T> a;
                 FragB<T> b[2];
@@ -608,12 +586,13 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             for (int n = 0; n < 2; ++n) {
                 const int il = n * 8 + 2 * t, i = it * 16 + il;
                 const float2 u = *reinterpret_cast<const float2*>(gs.from_start + i);  // with 1 / den_i in it
-                const float2 cl = *reinterpret_cast<const float2*>(gs.col + i);
+                float2 cl = make_float2(0.f, 0.f);
+                if (wq) cl = *reinterpret_cast<const float2*>(gs.col + i);
                 float w[4] = {u.x, u.y, u.x, u.y};
                 if (deep) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float q = gs.up[i + e];
+                        const float q = wq ? gs.up[i + e] : 1.f;
                         w[e] = q * exp2_fast((gs.hi[i + e] - hi0) + (gs.lo[i + e] - lo0));
                         w[2 + e] = q * exp2_fast((gs.hi[i + e] - hi1) + (gs.lo[i + e] - lo1));
                     }
@@ -676,11 +655,10 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             }
         }
         if (s + 1 < nch) {
-            st.template update<PHI>(qt, gt, gs.from_start, gs.col, gs.all, warp, lane);
+            st.template update<PHI>(qt, gt, gs.from_start, gs.col, wq != nullptr, gs.all, warp, lane);
             if (SH::SB == 1) __syncthreads();  // every warp has read the operand
             const int nb = SH::SB == 2 ? ((s + 1) & 1) : 0;
             st.publish(sm.sop[nb][0], sm.zs[nb], warp, lane);
-            if (gater) scan(s + 1);
         }
     }
     __syncthreads();
@@ -688,8 +666,8 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 }
 
 template <typename T, int D, int PHI>
-cudaError_t launch_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
-                         const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+cudaError_t launch_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
+                         const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,
                          void* chunk_state, cudaStream_t st) {
     constexpr size_t smem = sizeof(typename BwdQ<T, D, PHI>::Smem);
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -697,13 +675,13 @@ cudaError_t launch_bwd_q(const Problem& p, const void* q, const void* k, const v
     if (e != cudaSuccess) return e;
     return launch_pdl(gated_bwd_q_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
                       smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-                      static_cast<const T*>(g), static_cast<const T*>(dout), prefix, p.N, block_tokens, nblk,
-                      p.normalize, static_cast<T*>(dq), up, col, dgp, static_cast<uint8_t*>(chunk_state));
+                      gates, static_cast<const T*>(dout), prefix, p.N, block_tokens, nblk,
+                      p.normalize, static_cast<T*>(dq), wq, up, col, dgp, static_cast<uint8_t*>(chunk_state));
 }
 
 template <typename T, int D, int PHI>
-cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
-                          const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
+cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates,
+                          const void* dout, const float* suffix, int block_tokens, int nblk, const float* wq, const float* up, const float* col,
                           const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     constexpr size_t smem = sizeof(BwdKvSmem<T, D>);
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -711,7 +689,7 @@ cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const 
     if (e != cudaSuccess) return e;
     return launch_pdl(gated_bwd_kv_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
                       smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-                      static_cast<const T*>(g), static_cast<const T*>(dout), suffix, p.N, block_tokens, nblk, up, col, dgp,
+                      static_cast<const T*>(g), gates, static_cast<const T*>(dout), suffix, p.N, block_tokens, nblk, wq, up, col, dgp,
                       static_cast<const uint8_t*>(chunk_state), static_cast<T*>(dk), static_cast<T*>(dv),
                       static_cast<T*>(dg));
 }
@@ -719,21 +697,21 @@ cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const 
 }  // namespace gated
 
 template <typename T>
-cudaError_t gated_bwd_q_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
-                          const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+cudaError_t gated_bwd_q_t(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
+                          const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,
                           void* chunk_state, cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
         return gated::launch_bwd_q<T, decltype(d)::value, decltype(phi)::value>(
-            p, q, k, v, g, dout, prefix, block_tokens, nblk, dq, up, col, dgp, chunk_state, st);
+            p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, wq, up, col, dgp, chunk_state, st);
     });
 }
 template <typename T>
-cudaError_t gated_bwd_kv_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const void* dout,
-                           const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
+cudaError_t gated_bwd_kv_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates,
+                           const void* dout, const float* suffix, int block_tokens, int nblk, const float* wq, const float* up, const float* col,
                            const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
         return gated::launch_bwd_kv<T, decltype(d)::value, decltype(phi)::value>(
-            p, q, k, v, g, dout, suffix, block_tokens, nblk, up, col, dgp, chunk_state, dk, dv, dg, st);
+            p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, wq, up, col, dgp, chunk_state, dk, dv, dg, st);
     });
 }
 

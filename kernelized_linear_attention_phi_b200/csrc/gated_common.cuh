@@ -2,6 +2,8 @@
 // logarithms, tile loads, and the state's update.
 #pragma once
 
+#include <cstddef>
+
 #include "gated_mma.cuh"
 #include "internal.h"
 
@@ -35,108 +37,44 @@ template <typename T, int D> struct Shape {
 };
 
 // The gates of one chunk, from b_i = log2 of the product of the chunk's gates
-// up to token i. b is formed in 64 bits. The decay from key j to query i,
-// 2^(b_i - b_j), is used as the product of from_start_i and inv_j, one factor
-// per row and one per column, while no b of the chunk lies below -90 (deep = 0),
-// where both stay well inside fp32. In a deep chunk it is formed per pair from
-// b = hi + lo, which keeps 2^-24 of the difference however far the chunk has
-// decayed; a closed gate (-inf) counts as 2^-14000, far below any product that
-// fp32 can hold, and drops out of every difference behind it exactly.
+// up to token i (gate_scan.cuh). The decay from key j to query i, 2^(b_i - b_j),
+// is used as the product of from_start_i and inv_j, one factor per row and one
+// per column, while no b of the chunk lies below -90 (deep = 0), where both stay
+// well inside fp32. In a deep chunk it is formed per pair from b = hi + lo.
+// They are computed once per call for all chunks (gates_kernel, gated.cu) and
+// come with the tiles: forming them inside a sweep puts a warp's scan on
+// every chunk's way.
 template <int C> struct alignas(16) Gates {
     float hi[C], lo[C];
-    float from_start[C];  // 2^b_i; 0 past the last token
+    float from_start[C];  // 2^b_i; 0 past the last token. Second sweep, normalized: times 1 / den_i
     float inv[C];         // 2^-b_j
     float to_end[C];      // 2^(b_last - b_j); 0 past the last token
-    float up[C], col[C];  // gradients: 1 / den_i and -(out_i . dout_i); 0 past the last token
     float all;            // 2^b_last
-    int deep;
+    int deep, pad[2];
+    float up[C], col[C];  // second sweep, normalized: 1 / den_i and -(out_i . dout_i); 0 past the last token
 };
+template <int C> constexpr int kGateBytes = (5 * C + 4) * 4;  // of a chunk's record in global memory
 constexpr float kDeep = -90.f;
-constexpr double kLog2e = 1.4426950408889634;
-constexpr double kClosed = -14000.0;
-
-// One lane's gates of a chunk, held from the load to the scan as they were
-// loaded (converting them at once would wait for the load).
-__device__ __forceinline__ uint32_t load_raw(const float* p) {
-    uint32_t r;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
+// Starts the copy of a chunk's gates; with wq (the second sweep of a normalized
+// call: wq, up, col of the head, from row0 on) those too.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ uint16_t load_raw(const __nv_bfloat16* p) {
-    uint16_t r;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ float raw_f32(uint32_t r) { return __uint_as_float(r); }
-__device__ __forceinline__ float raw_f32(uint16_t r) { return __uint_as_float((uint32_t)r << 16); }
-template <typename T, int C> struct GateRegs {
-    decltype(load_raw(static_cast<const T*>(nullptr))) g[C / 32];
-    float up[C / 32], col[C / 32];
-};
-template <typename T, int C>
-__device__ __forceinline__ void load_gates(GateRegs<T, C>& r, const T* g, const float* up, const float* col, int row0, int N,
-                                           int lane) {
-#pragma unroll
-    for (int e = 0; e < C / 32; ++e) {
-        const int i = row0 + lane * (C / 32) + e;
-        r.g[e] = 0;
-        r.up[e] = r.col[e] = 0.f;
-        if (i < N) {
-            r.g[e] = load_raw(g + i);
-            r.up[e] = 1.f;
-            if (up) r.up[e] = up[i];
-            if (col) r.col[e] = col[i];
-        }
+template <int C>
+__device__ __forceinline__ void load_gates(Gates<C>& s, const uint8_t* rec, const float* wq, const float* up, const float* col,
+                                           int row0, int N) {
+    static_assert(offsetof(Gates<C>, up) == kGateBytes<C>, "record");
+    const int u = threadIdx.x;
+    const bool weighted = u >= C / 2 && u < 3 * C / 4;  // 16-byte pieces of from_start
+    if (u < kGateBytes<C> / 16 && !(wq && weighted))
+        cp_async16(reinterpret_cast<uint8_t*>(&s) + u * 16, rec + u * 16, true);
+    if (wq && u < C) {
+        const bool in = row0 + u < N;
+        const int i = in ? row0 + u : 0;
+        cp_async4(s.from_start + u, wq + i, in);
+        cp_async4(s.up + u, up + i, in);
+        cp_async4(s.col + u, col + i, in);
     }
-}
-// 2^b from 64 bits: the fraction alone goes through the fp32 function.
-__device__ __forceinline__ float pow2(double b) {
-    const float n = fminf(fmaxf(rintf((float)b), -126.f), 128.f);  // 128: infinity
-    const float f = exp2_fast((float)(b - (double)n));
-    return b < -126.0 ? 0.f : f * __int_as_float(((int)n + 127) << 23);  // a NaN stays
-}
-
-// A whole warp. Returns the chunk's log2 sum (every lane).
-template <typename T, int C>
-__device__ __forceinline__ double scan_gates(Gates<C>& s, const GateRegs<T, C>& r, int valid, int lane) {
-    constexpr int R = C / 32;
-    double x[R];
-#pragma unroll
-    for (int e = 0; e < R; ++e) {
-        const double l = (double)raw_f32(r.g[e]) * kLog2e;
-        x[e] = l < kClosed ? kClosed : l;  // a NaN stays
-        if (e) x[e] += x[e - 1];
-    }
-    double run = x[R - 1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += y;
-    }
-    const double before = run - x[R - 1];
-    const double last = __shfl_sync(0xffffffffu, run, 31);
-    bool low = false;
-#pragma unroll
-    for (int e = 0; e < R; ++e) {
-        const int i = lane * R + e;
-        const double b = before + x[e];
-        const float hi = (float)b;
-        const bool in = i < valid;
-        low = low || hi < kDeep;
-        s.hi[i] = hi;
-        s.lo[i] = (float)(b - (double)hi);
-        s.from_start[i] = in ? pow2(b) : 0.f;
-        s.inv[i] = pow2(-b);
-        s.to_end[i] = in ? pow2(last - b) : 0.f;
-        s.up[i] = r.up[e];
-        s.col[i] = r.col[e];
-    }
-    low = __any_sync(0xffffffffu, low);
-    if (lane == 0) {
-        s.all = pow2(last);
-        s.deep = low;
-    }
-    return last;
 }
 
 // The decay between two tokens of a deep chunk, from what (hi, lo) of the one
@@ -230,12 +168,12 @@ template <typename T, int D> struct State {
         }
     }
     // S = all S + sum_j w_j phi(x_j) (x) y_j,  z = all z + sum_j w_j phi(x_j) c_j
-    // with x, y [C x D] tiles and w, c (c null: ones) of the chunk. w phi(x)
+    // with x, y [C x D] tiles and w, c (c null: ones) of the chunk; z only with `with_z`. w phi(x)
     // is formed in fp32 and multiplied as hi + lo operands, so a state of bf16
     // rows errs by 2^-17 of its terms, not by bf16's 2^-8.
     template <int PHI>
-    __device__ __forceinline__ void update(const T* x, const T* y, const float* w, const float* c, float all, int warp,
-                                           int lane) {
+    __device__ __forceinline__ void update(const T* x, const T* y, const float* w, const float* c, bool with_z, float all,
+                                           int warp, int lane) {
         if (!owns(warp)) return;
         const int t = lane & 3;
         constexpr int K = SH::C / 16;
@@ -281,7 +219,7 @@ template <typename T, int D> struct State {
                 S[2 * n + 1][e] = fmaf(S[2 * n + 1][e], all, s[1][e]);
             }
         }
-        if (col(warp) == 0) {
+        if (with_z && col(warp) == 0) {
             float s[4] = {};
 #pragma unroll
             for (int kt = 0; kt < K; ++kt) {

@@ -34,8 +34,8 @@ template <typename T, int D> struct StateSmem {
 // block (a record of `prefix`, or S_in / z_in, or nothing).
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, sizeof(T) == 2 && D == 64 ? 3 : 1)
-gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
-                   const float* prefix, const float* S_in, const float* z_in, int N, int block_tokens, int nblk,
+gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                   const uint8_t* __restrict__ gates, const float* prefix, const float* S_in, const float* z_in, int N, int block_tokens, int nblk,
                    int normalize, T* __restrict__ out, float* S_out, float* z_out) {
     using SH = Shape<T, D>;
     constexpr int C = SH::C, LD = SH::LD;
@@ -47,11 +47,12 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     const int nch = (end - first + C - 1) / C;
     const size_t off = (size_t)bh * N * D;
     q += off; k += off; v += off; out += off;
-    gate += (size_t)bh * N;
+    gates += ((size_t)bh * ((N + C - 1) / C) + first / C) * kGateBytes<C>;
     pdl_wait();
 
     auto fetch = [&](int c) {
         const int row0 = first + c * C;
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, nullptr, row0, N);
         load_tile<SH, T, D>(sm.tiles[c & 1][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[c & 1][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[c & 1][2], v, row0, N);
@@ -67,25 +68,15 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     }
     st.publish(sm.sop[0], sm.zs[0], warp, lane);
     // the warps' row groups differ in work (a group sees the keys before it):
-    // CTAs of an SM start them at different warps, and the gates go to the
-    // warp with the first group
-    const int turn = (blockIdx.x + blockIdx.y) % SH::RG;
-    const int rg = (warp + turn) % SH::RG, cg = warp / SH::RG;
+    // CTAs of an SM start them at different warps
+    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
     const int i0 = rg * 16, col0 = cg * SH::NCOL;
-    const bool gater = rg == 0 && cg == 0;
-    GateRegs<T, C> gr;
-    if (gater) {
-        load_gates<T, C>(gr, gate, nullptr, nullptr, first, N, lane);
-        scan_gates<T, C>(sm.gates[0], gr, end - first, lane);
-    }
 
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         cp_async_wait<0>();
         __syncthreads();
-        if (c + 1 < nch) {
-            fetch(c + 1);
-            if (gater) load_gates<T, C>(gr, gate, nullptr, nullptr, first + (c + 1) * C, N, lane);
-        }
+        if (c + 1 < nch) fetch(c + 1);
         const T *qt = sm.tiles[c & 1][0], *kt = sm.tiles[c & 1][1], *vt = sm.tiles[c & 1][2];
         const Gates<C>& gs = sm.gates[c & 1];
         const int sb = SH::SB == 2 ? (c & 1) : 0;
@@ -97,7 +88,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         // fetch the code counts (1 x 4 x 1531 x 32 fp32: FIGURE).
         constexpr int NT = SH::NCOL / 8;
         float o[NT][4] = {}, oz[4] = {};
-#pragma unroll 2
+#pragma unroll(SH::F32 ? 1 : D / 16)
         for (int k0 = 0; k0 < D; k0 += 16) {
             FragA<T> a;
             load_a<LD>(a, qt, i0, k0, lane);
@@ -132,7 +123,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 #pragma unroll 1
         for (int jt = 0; jt <= rg; ++jt) {
             float p[2][4] = {};
-#pragma unroll 2
+#pragma unroll(SH::F32 ? 1 : D / 16)
             for (int k0 = 0; k0 < D; k0 += 16) {
                 FragA<T> a;
                 FragB<T> b[2];
@@ -200,12 +191,11 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             }
         }
         if (c + 1 < nch || S_out) {
-            st.template update<PHI>(kt, vt, gs.to_end, nullptr, gs.all, warp, lane);
+            st.template update<PHI>(kt, vt, gs.to_end, nullptr, true, gs.all, warp, lane);
             if (SH::SB == 1) __syncthreads();  // every warp has read the operand
             if (c + 1 < nch) {
                 const int nb = SH::SB == 2 ? ((c + 1) & 1) : 0;
                 st.publish(sm.sop[nb], sm.zs[nb], warp, lane);
-                if (gater) scan_gates<T, C>(sm.gates[(c + 1) & 1], gr, end - first - (c + 1) * C, lane);
             }
         }
     }
@@ -218,8 +208,8 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 //   z part weighted by col_i = -(out_i . dout_i), chunks from the last to the first.
 template <typename T, int D, int PHI, bool REVERSE>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS)
-gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __restrict__ gate,
-                   const float* up, const float* col, int N, int block_tokens, int nblk, int blk0, float* __restrict__ rec,
+gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8_t* __restrict__ gates,
+                   const float* wq, const float* up, const float* col, int N, int block_tokens, int nblk, int blk0, float* __restrict__ rec,
                    float* __restrict__ dec) {
     using SH = Shape<T, D>;
     constexpr int C = SH::C;
@@ -231,13 +221,17 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __
     const int nch = (end - first + C - 1) / C;
     x += (size_t)bh * N * D;
     y += (size_t)bh * N * D;
-    gate += (size_t)bh * N;
-    if (up) up += (size_t)bh * N;
-    if (col) col += (size_t)bh * N;
+    gates += ((size_t)bh * ((N + C - 1) / C) + first / C) * kGateBytes<C>;
+    if (wq) {
+        wq += (size_t)bh * N;
+        up += (size_t)bh * N;
+        col += (size_t)bh * N;
+    }
     pdl_wait();
     auto chunk = [&](int c) { return REVERSE ? nch - 1 - c : c; };
     auto fetch = [&](int c) {
         const int row0 = first + chunk(c) * C;
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)chunk(c) * kGateBytes<C>, wq, up, col, row0, N);
         load_tile<SH, T, D>(sm.tiles[c & 1][0], x, row0, N);
         load_tile<SH, T, D>(sm.tiles[c & 1][1], y, row0, N);
         cp_async_commit();
@@ -245,44 +239,24 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const T* __
     fetch(0);
     State<T, D> st;
     st.seed(nullptr, nullptr, warp, lane);
-    // the gates: one warp (the last, which has the least to do when S has fewer row tiles than warps)
-    constexpr int GW = SH::NW - 1;
-    GateRegs<T, C> gr;
-    double total = 0.0;
-    auto scan = [&](int c) {
-        Gates<C>& s = sm.gates[c & 1];
-        total += scan_gates<T, C>(s, gr, end - first - chunk(c) * C, lane);
-        if (REVERSE) {
-#pragma unroll
-            for (int e = 0; e < C / 32; ++e) {
-                const int i = lane * (C / 32) + e;
-                s.from_start[i] *= s.up[i];
-            }
-        }
-    };
-    if (warp == GW) {
-        load_gates<T, C>(gr, gate, up, col, first + chunk(0) * C, N, lane);
-        scan(0);
-    }
+    float total = 1.f;
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
         cp_async_wait<0>();
         __syncthreads();
-        if (c + 1 < nch) {
-            fetch(c + 1);
-            if (warp == GW) load_gates<T, C>(gr, gate, up, col, first + chunk(c + 1) * C, N, lane);
-        }
+        if (c + 1 < nch) fetch(c + 1);
         const Gates<C>& gs = sm.gates[c & 1];
         st.template update<PHI>(sm.tiles[c & 1][0], sm.tiles[c & 1][1], REVERSE ? gs.from_start : gs.to_end,
-                                REVERSE ? gs.col : nullptr, gs.all, warp, lane);
-        if (c + 1 < nch && warp == GW) scan(c + 1);
+                                REVERSE ? gs.col : nullptr, !REVERSE || wq, gs.all, warp, lane);
+        total *= gs.all;
     }
     float* r = rec + ((size_t)bh * nblk + blk) * (size_t)(D * D + D);
     st.store(r, r + D * D, warp, lane);
-    if (warp == GW && lane == 0) dec[(size_t)bh * nblk + blk] = exp2_fast((float)total);
+    if (threadIdx.x == 0) dec[(size_t)bh * nblk + blk] = total;
 }
 
 template <typename T, int D, int PHI>
-cudaError_t launch_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g, const float* prefix,
+cudaError_t launch_sweep(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const float* prefix,
                          const float* S_in, const float* z_in, int block_tokens, int nblk, void* out, float* S_out,
                          float* z_out, cudaStream_t st) {
     constexpr size_t smem = sizeof(FwdSmem<T, D>);
@@ -291,13 +265,13 @@ cudaError_t launch_sweep(const Problem& p, const void* q, const void* k, const v
     if (e != cudaSuccess) return e;
     return launch_pdl(gated_sweep_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
                       smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-                      static_cast<const T*>(g), prefix, S_in, z_in, p.N, block_tokens, nblk, p.normalize,
+                      gates, prefix, S_in, z_in, p.N, block_tokens, nblk, p.normalize,
                       static_cast<T*>(out), S_out, z_out);
 }
 
 template <typename T, int D, int PHI>
-cudaError_t launch_states(const Problem& p, bool reverse, const void* x, const void* y, const void* g, const float* up,
-                          const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
+cudaError_t launch_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates,
+                          const float* wq, const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
                           cudaStream_t st) {
     constexpr size_t smem = sizeof(StateSmem<T, D>);
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -306,33 +280,33 @@ cudaError_t launch_states(const Problem& p, bool reverse, const void* x, const v
         const cudaError_t e = ensure_smem<gated_state_kernel<T, D, PHI, true>>(smem);
         if (e != cudaSuccess) return e;
         return launch_pdl(gated_state_kernel<T, D, PHI, true>, grid, dim3(Shape<T, D>::THREADS), smem, st,
-                          static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(g), up, col, p.N,
+                          static_cast<const T*>(x), static_cast<const T*>(y), gates, wq, up, col, p.N,
                           block_tokens, nblk, blk0, rec, dec);
     }
     const cudaError_t e = ensure_smem<gated_state_kernel<T, D, PHI, false>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(gated_state_kernel<T, D, PHI, false>, grid, dim3(Shape<T, D>::THREADS), smem, st,
-                      static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(g), up, col, p.N,
+                      static_cast<const T*>(x), static_cast<const T*>(y), gates, wq, up, col, p.N,
                       block_tokens, nblk, blk0, rec, dec);
 }
 
 }  // namespace gated
 
 template <typename T>
-cudaError_t gated_sweep_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const float* prefix,
+cudaError_t gated_sweep_t(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const float* prefix,
                           const float* S_in, const float* z_in, int block_tokens, int nblk, void* out, float* S_out,
                           float* z_out, cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
-        return gated::launch_sweep<T, decltype(d)::value, decltype(phi)::value>(p, q, k, v, g, prefix, S_in, z_in,
+        return gated::launch_sweep<T, decltype(d)::value, decltype(phi)::value>(p, q, k, v, gates, prefix, S_in, z_in,
                                                                                block_tokens, nblk, out, S_out, z_out, st);
     });
 }
 template <typename T>
-cudaError_t gated_states_t(const Problem& p, bool reverse, const void* x, const void* y, const void* g, const float* up,
-                           const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
+cudaError_t gated_states_t(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates,
+                           const float* wq, const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
                            cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
-        return gated::launch_states<T, decltype(d)::value, decltype(phi)::value>(p, reverse, x, y, g, up, col, block_tokens,
+        return gated::launch_states<T, decltype(d)::value, decltype(phi)::value>(p, reverse, x, y, gates, wq, up, col, block_tokens,
                                                                                 nblk, blk0, count, rec, dec, st);
     });
 }

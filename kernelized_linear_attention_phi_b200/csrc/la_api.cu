@@ -91,7 +91,7 @@ int prefix_nbins(const Problem& p, int kchunk) { return p.N / kchunk + 1; }
 struct WsLayout {
     size_t part = 0, sz = 0, perm = 0, msort = 0, bins = 0, total = 0;
     size_t grec = 0, gtot = 0, gn = 0, gden = 0;  // gradients
-    size_t dec = 0, up = 0, col = 0, dgp = 0, chunks = 0;  // gated forms
+    size_t dec = 0, gates = 0, wq = 0, up = 0, col = 0, dgp = 0, chunks = 0;  // gated forms
 };
 
 WsLayout ws_layout(const Problem& p, int op) {
@@ -161,11 +161,15 @@ WsLayout ws_layout(const Problem& p, int op) {
             off = round_up(off + (size_t)p.bh() * bp.nblk * rec, kAlign);
             L.dec = off;
             off = round_up(off + (size_t)p.bh() * bp.nblk * sizeof(float), kAlign);
-        } else if (!bwd) {
-            return L;
+        }
+        if (!tcf) {
+            L.gates = off;
+            off = round_up(off + gated_gate_bytes(p), kAlign);
         }
         if (bwd) {
             const size_t tokens = (size_t)p.bh() * p.N * sizeof(float);
+            L.wq = off;
+            off = round_up(off + tokens, kAlign);
             L.up = off;
             off = round_up(off + tokens, kAlign);
             L.col = off;
@@ -581,7 +585,7 @@ la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, con
         if (!aligned16(ptr)) return LA_ERR_MISALIGNED;
     const Problem p = to_problem(desc);
     const WsLayout L = ws_layout(p, LA_OP_GATED_CAUSAL);
-    if (L.total) LA_TRY(check_ws(L, ws, ws_bytes));
+    LA_TRY(check_ws(L, ws, ws_bytes));
     LA_TRY(check_device());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     timing_begin(st);
@@ -599,13 +603,15 @@ la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, con
         LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));
         return cuda_status(tc_gated_sweep(p, q, k, v, g, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, flags, st));
     }
+    uint8_t* gates = at<uint8_t>(ws, L.gates);
+    LA_TRY(cuda_status(gated_gates(p, g, gates, st)));
     if (bp.nblk == 1)
-        return cuda_status(gated_sweep(p, q, k, v, g, nullptr, S_in, z_in, bp.block_tokens, 1, out, S_out, z_out, st));
-    LA_TRY(cuda_status(gated_states(p, false, k, v, g, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
+        return cuda_status(gated_sweep(p, q, k, v, gates, nullptr, S_in, z_in, bp.block_tokens, 1, out, S_out, z_out, st));
+    LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
                                     S_out ? bp.nblk : bp.nblk - 1, part, dec, st)));
     LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));
-    return cuda_status(gated_sweep(p, q, k, v, g, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, nullptr, nullptr,
-                                   st));
+    return cuda_status(gated_sweep(p, q, k, v, gates, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, nullptr,
+                                   nullptr, st));
 }
 
 la_status la_gated_causal_backward(const la_desc* desc, const void* q, const void* k, const void* v, const void* g,
@@ -623,6 +629,9 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     timing_begin(st);
     const BlockPlan bp = gated_plan(p, true);
+    uint8_t* gates = at<uint8_t>(ws, L.gates);
+    LA_TRY(cuda_status(gated_gates(p, g, gates, st)));
+    float* wq = p.normalize ? at<float>(ws, L.wq) : nullptr;
     float* up = p.normalize ? at<float>(ws, L.up) : nullptr;
     float* col = p.normalize ? at<float>(ws, L.col) : nullptr;
     float* dgp = at<float>(ws, L.dgp);
@@ -631,18 +640,19 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
     if (bp.nblk > 1) {
         part = at<float>(ws, L.part);
         dec = at<float>(ws, L.dec);
-        LA_TRY(cuda_status(gated_states(p, false, k, v, g, nullptr, nullptr, bp.block_tokens, bp.nblk, 0, bp.nblk - 1,
-                                        part, dec, st)));
+        LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
+                                        bp.nblk - 1, part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
-    LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, g, dout, part, bp.block_tokens, bp.nblk, dq, up, col, dgp, chunks, st)));
+    LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, gates, dout, part, bp.block_tokens, bp.nblk, dq, wq, up, col, dgp, chunks,
+                                   st)));
     if (bp.nblk > 1) {  // the same records, from the other end
-        LA_TRY(cuda_status(gated_states(p, true, q, dout, g, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, part, dec,
-                                        st)));
+        LA_TRY(cuda_status(gated_states(p, true, q, dout, gates, wq, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, part,
+                                        dec, st)));
         LA_TRY(cuda_status(gated_scan(p, true, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
-    return cuda_status(gated_bwd_kv(p, q, k, v, g, dout, part, bp.block_tokens, bp.nblk, up, col, dgp, chunks, dk, dv, dg,
-                                    st));
+    return cuda_status(gated_bwd_kv(p, q, k, v, g, gates, dout, part, bp.block_tokens, bp.nblk, wq, up, col, dgp, chunks,
+                                    dk, dv, dg, st));
 }
 
 la_status la_gated_decode_step(const la_desc* desc, const void* q, const void* k, const void* v, const void* g,

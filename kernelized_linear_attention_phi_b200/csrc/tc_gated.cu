@@ -89,20 +89,22 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     // step i is chunk nci - 1 - i
     if (warp == 0) {
         const __nv_bfloat16* g = gate + (size_t)bh * N;
-        double after = 0.0;  // log2 of the gates behind the chunk, within the block
+        long long after = 0;  // the gates behind the chunk, within the block
+        bool bad = false;
         Gates2 gr = load_gates(g, first + (nci - 1) * C, end, lane);
         int issued = 0;
 #pragma unroll 1
         for (int i = 0; i < nci; ++i) {
             const int s = i % CF::STAGES, u = i / CF::STAGES, row = first + (nci - 1 - i) * C;
-            double b0, b1;
-            const double last = scan_gates(gr, lane, b0, b1);
+            const GateSums<2> gs = sum_gates<2>(gr.g, lane);
+            bad = bad || gs.bad & 4;
             if (i + 1 < nci) gr = load_gates(g, row - C, end, lane);
             if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(empty + s, (u - 1) & 1, err))) break;
             float* w = wts + s * C + 2 * lane;
-            w[0] = row + 2 * lane < end ? ex2((float)(after + (last - b0))) : 0.f;
-            w[1] = row + 2 * lane + 1 < end ? ex2((float)(after + (last - b1))) : 0.f;
-            after += last;
+            const float nan = bad ? NAN : 0.f;  // the block's state is NaN
+            w[0] = row + 2 * lane < end ? gate_pow2(after + (gs.last - gs.b[0])) + nan : 0.f;
+            w[1] = row + 2 * lane + 1 < end ? gate_pow2(after + (gs.last - gs.b[1])) + nan : 0.f;
+            after += gs.last;
             __syncwarp();
             if (elect_one()) {
                 mbar_arrive_expect_tx(full + s, CF::STAGE);
@@ -117,7 +119,7 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
             issued = i + 1;
         }
         if (lane == 0) {
-            dec[(size_t)bh * nblk + blk] = ex2((float)after);
+            dec[(size_t)bh * nblk + blk] = gate_pow2(after) + (bad ? NAN : 0.f);
             for (int i = max(0, issued - CF::STAGES); i < issued; ++i)
                 mbar_wait(full + i % CF::STAGES, (i / CF::STAGES) & 1, err, false);
         }
@@ -343,10 +345,10 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 #pragma unroll 1
         for (int ci = 0; ci < nci; ++ci) {
             const int j = ci & 1, s = ci % CF::VS, row = first + ci * C;
-            double b0, b1;
-            scan_gates(gr, lane, b0, b1);
+            const GateSums<2> sums = sum_gates<2>(gr.g, lane);
             if (ci + 1 < nci) gr = load_gates(g, row + C, end, lane);
-            const float f0 = (float)b0, f1 = (float)b1;
+            const float f0 = gate_float2(sums.b[0]).x + (sums.bad & 1 ? NAN : 0.f);
+            const float f1 = gate_float2(sums.b[1]).x + (sums.bad & 2 ? NAN : 0.f);
             const bool low = __any_sync(0xffffffffu, fminf(f0, f1) < kDeep);
             // chunk ci - 2's P and O^T are done, and with them (in order) all
             // that chunk ci - 4 needed its gates for

@@ -1,6 +1,7 @@
 // Pieces shared by the tcgen05 kernels of gated linear attention (bf16).
 #pragma once
 
+#include "gate_scan.cuh"
 #include "launch_util.h"
 #include "tc.h"
 #include "tc_common.cuh"
@@ -10,12 +11,6 @@ namespace tcg {
 
 using namespace tc;
 
-// Log-gates of a chunk of 64 tokens, in units of log2. A closed gate (-inf)
-// counts as 2^-160, which fp32 cannot hold: every product across it is 0. The
-// sums are formed in 64 bits; kept as fp32 they blur a decay by 2^-24 of the
-// chunk's whole sum, below the rounding of bf16 results even with some ten
-// closed gates in one chunk.
-constexpr float kClosedLog2 = -160.f;
 // Queries whose products reach below 2^-90 are scaled by 2^90 (tc_gated.cu).
 constexpr float kDeep = -90.f;
 
@@ -64,33 +59,15 @@ __device__ __forceinline__ float ex2(float x) {
 // The two gates of this lane (tokens row0 + 2 lane, + 1; 0 past the row's end),
 // as loaded: converting them here would wait for the load.
 struct Gates2 {
-    uint16_t a, b;
+    uint16_t g[2];
 };
 __device__ __forceinline__ Gates2 load_gates(const __nv_bfloat16* g, int row0, int end, int lane) {
     const int i = row0 + 2 * lane;
     const uint16_t* p = reinterpret_cast<const uint16_t*>(g) + i;
-    Gates2 r{0, 0};
-    if (i < end) asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r.a) : "l"(p));
-    if (i + 1 < end) asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r.b) : "l"(p + 1));
+    Gates2 r{{0, 0}};
+    if (i < end) asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r.g[0]) : "l"(p));
+    if (i + 1 < end) asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r.g[1]) : "l"(p + 1));
     return r;
-}
-// A whole warp: inclusive sums (log2) of this lane's two tokens over the chunk.
-// Returns the chunk's sum.
-__device__ __forceinline__ double scan_gates(const Gates2& g, int lane, double& b0, double& b1) {
-    constexpr double kLog2e = 1.4426950408889634;
-    double x = (double)__uint_as_float((uint32_t)g.a << 16) * kLog2e;
-    double y = (double)__uint_as_float((uint32_t)g.b << 16) * kLog2e;
-    x = x < kClosedLog2 ? kClosedLog2 : x;  // a NaN stays
-    y = y < kClosedLog2 ? kClosedLog2 : y;
-    double run = x + y;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += up;
-    }
-    b1 = run;
-    b0 = run - y;
-    return __shfl_sync(0xffffffffu, run, 31);
 }
 
 template <int PHI> __device__ __forceinline__ float phi_f32(float x) {

@@ -71,8 +71,7 @@ def test_gated_refusals(lib):
 def test_gated_workspace_sizes(lib):
     size = lambda op, **k: B.la_workspace_size(desc(**k), op)  # noqa: E731
     assert size("gated_causal") % 256 == 0 and size("gated_causal") > 0
-    assert size("gated_causal", N=200) == 0               # one block per head: no workspace
-    assert size("gated_causal", B_=64, H=32) == 0
+    assert size("gated_causal", N=1) > 256 and size("gated_causal", B_=64, H=32) > 256
     assert size("gated_causal", d=48) == 0 and size("gated_causal_bwd", N=0) == 0
     # the gradients keep a state per chunk of 64 tokens
     assert size("gated_causal_bwd") >= 2 * 3 * (-(-4000 // 64)) * (64 * 64 * 2 + 64 * 4)
@@ -127,7 +126,6 @@ def test_rope_workspace_size(lib):
 @pytest.mark.skipif(torch.cuda.is_available(), reason="only meaningful on a machine with no GPU")
 def test_valid_requests_reach_the_device_check(lib):
     assert forward(lib, desc()) == CUDA and backward(lib, desc()) == CUDA and step(lib, desc()) == CUDA
-    assert forward(lib, desc(N=200), ws=None, nbytes=0) == CUDA
     assert rope(lib, rope_desc()) == CUDA and rope(lib, rope_desc(), True) == CUDA
     assert rope(lib, rope_desc(rot=0, table_rows=0), cos=None, sin=None, at=None, wq=None, wk=None) == CUDA
     # strides of dimensions of size 1 are not looked at

@@ -33,7 +33,7 @@ namespace gated {
 // PARTS: operands of the state (2: rounded and remainder); COPIES of them.
 template <typename T, int D, int PARTS, int COPIES> struct BwdSmem {
     using SH = Shape<T, D>;
-    T tiles[2][4][SH::TILE];  // q, k, v, dout of two chunks
+    T tiles[SH::ST][4][SH::TILE];  // q, k, v, dout
     T sop[COPIES][PARTS][SH::SOP];
     float zs[COPIES][D];
     Gates<SH::C> gates[2];
@@ -125,7 +125,7 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
 }
 
 template <typename T, int D, int PHI>
-__global__ void __launch_bounds__(Shape<T, D>::THREADS)
+__global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                    const uint8_t* __restrict__ gates, const T* __restrict__ dout, const float* prefix, int N, int block_tokens, int nblk, int normalize,
                    T* __restrict__ dq, float* __restrict__ wq, float* __restrict__ up, float* __restrict__ col, float* __restrict__ dgp,
@@ -150,10 +150,10 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     auto fetch = [&](int c) {
         const int row0 = first + c * C;
         load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, nullptr, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][0], q, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][1], k, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][2], v, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][3], dout, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], q, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], k, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][2], v, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][3], dout, row0, N);
         cp_async_commit();
     };
     fetch(0);
@@ -192,9 +192,9 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     for (int c = 0; c < nch; ++c) {
         cp_async_wait<0>();
         __syncthreads();
-        if (c + 1 < nch) fetch(c + 1);
+        if (SH::ST == 2 && c + 1 < nch) fetch(c + 1);
         if (c > 0) finish(c - 1);
-        const T *qt = sm.tiles[c & 1][0], *kt = sm.tiles[c & 1][1], *vt = sm.tiles[c & 1][2], *gt = sm.tiles[c & 1][3];
+        const T *qt = sm.tiles[c % SH::ST][0], *kt = sm.tiles[c % SH::ST][1], *vt = sm.tiles[c % SH::ST][2], *gt = sm.tiles[c % SH::ST][3];
         const Gates<C>& gs = sm.gates[c & 1];
         const int sb = BQ::COPIES == 2 ? (c & 1) : 0;
         const T* sop = sm.sop[sb][0];
@@ -396,7 +396,8 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         }
         if (c + 1 < nch) {
             st.template update<PHI>(kt, vt, gs.to_end, nullptr, true, gs.all, warp, lane);
-            if (BQ::COPIES == 1) __syncthreads();  // every warp has read the operand
+            if (BQ::COPIES == 1) __syncthreads();  // every warp has read the operand and the tiles
+            if (SH::ST == 1) fetch(c + 1);
             const int nb = BQ::COPIES == 2 ? ((c + 1) & 1) : 0;
             st.template publish<LO>(sm.sop[nb][0], sm.zs[nb], warp, lane, sm.sop[nb][BQ::PARTS - 1]);
         }
@@ -406,7 +407,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 }
 
 template <typename T, int D, int PHI>
-__global__ void __launch_bounds__(Shape<T, D>::THREADS)
+__global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
                     const uint8_t* __restrict__ gates, const T* __restrict__ dout, const float* suffix, int N, int block_tokens, int nblk,
                     const float* wq, const float* up, const float* col, const float* __restrict__ dgp,
@@ -437,10 +438,10 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     auto fetch = [&](int s) {
         const int row0 = first + (nch - 1 - s) * C;
         load_gates<C>(sm.gates[s & 1], gates + (size_t)(nch - 1 - s) * kGateBytes<C>, wq, up, col, row0, N);
-        load_tile<SH, T, D>(sm.tiles[s & 1][0], q, row0, N);
-        load_tile<SH, T, D>(sm.tiles[s & 1][1], k, row0, N);
-        load_tile<SH, T, D>(sm.tiles[s & 1][2], v, row0, N);
-        load_tile<SH, T, D>(sm.tiles[s & 1][3], dout, row0, N);
+        load_tile<SH, T, D>(sm.tiles[s % SH::ST][0], q, row0, N);
+        load_tile<SH, T, D>(sm.tiles[s % SH::ST][1], k, row0, N);
+        load_tile<SH, T, D>(sm.tiles[s % SH::ST][2], v, row0, N);
+        load_tile<SH, T, D>(sm.tiles[s % SH::ST][3], dout, row0, N);
         cp_async_commit();
     };
     fetch(0);
@@ -496,9 +497,9 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         const int c = nch - 1 - s;
         cp_async_wait<0>();
         __syncthreads();
-        if (s + 1 < nch) fetch(s + 1);
+        if (SH::ST == 2 && s + 1 < nch) fetch(s + 1);
         if (s > 0) finish(s - 1);
-        const T *qt = sm.tiles[s & 1][0], *kt = sm.tiles[s & 1][1], *vt = sm.tiles[s & 1][2], *gt = sm.tiles[s & 1][3];
+        const T *qt = sm.tiles[s % SH::ST][0], *kt = sm.tiles[s % SH::ST][1], *vt = sm.tiles[s % SH::ST][2], *gt = sm.tiles[s % SH::ST][3];
         const Gates<C>& gs = sm.gates[s & 1];
         const int sb = SH::SB == 2 ? (s & 1) : 0;
         const T* sop = sm.sop[sb][0];
@@ -656,7 +657,8 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         }
         if (s + 1 < nch) {
             st.template update<PHI>(qt, gt, gs.from_start, gs.col, wq != nullptr, gs.all, warp, lane);
-            if (SH::SB == 1) __syncthreads();  // every warp has read the operand
+            if (SH::SB == 1) __syncthreads();  // every warp has read the operand and the tiles
+            if (SH::ST == 1) fetch(s + 1);
             const int nb = SH::SB == 2 ? ((s + 1) & 1) : 0;
             st.publish(sm.sop[nb][0], sm.zs[nb], warp, lane);
         }

@@ -14,15 +14,17 @@ namespace gated {
 // it into RG row groups of 16 tokens and CG column groups of NCOL channels.
 // The state S (d x d, fp32) lives in the warps' registers: SRT row tiles of
 // 16, each cut into SCG column groups of SN columns. SB: operand copies of S
-// in shared memory (one copy costs one more barrier per chunk, but leaves room
-// for a third CTA per SM at d = 64 in bf16).
+// in shared memory, ST: chunks of tiles. At d <= 64 one of each leaves room for
+// four CTAs per SM, whose work covers a chunk's loads (STAGEFIG); at
+// d = 128 an SM holds one CTA, which loads a chunk ahead.
 // fp32 rows are twice as long, so d >= 64 takes chunks of 32 tokens to keep
 // two stages of tiles within the shared memory of an SM.
 template <typename T, int D> struct Shape {
     static constexpr bool F32 = sizeof(T) == 4;
     static constexpr int C = F32 && D >= 64 ? 32 : 64;
     static constexpr int NW = D == 128 ? 8 : 4;
-    static constexpr int SB = (F32 && D == 128) || (!F32 && D == 64) ? 1 : 2;
+    static constexpr int SB = F32 || D <= 64 ? 1 : 2;
+    static constexpr int ST = D == 128 ? 2 : 1;
     static constexpr int THREADS = NW * 32;
     static constexpr int LD = D + (F32 ? 8 : 8);
     static constexpr int EPV = 16 / sizeof(T);

@@ -19,21 +19,21 @@ namespace gated {
 
 template <typename T, int D> struct FwdSmem {
     using SH = Shape<T, D>;
-    T tiles[2][3][SH::TILE];  // q, k, v of two chunks
+    T tiles[SH::ST][3][SH::TILE];  // q, k, v
     T sop[SH::SB][SH::SOP];
     float zs[SH::SB][D];
     Gates<SH::C> gates[2];
 };
 template <typename T, int D> struct StateSmem {
     using SH = Shape<T, D>;
-    T tiles[2][2][SH::TILE];
+    T tiles[SH::ST][2][SH::TILE];
     Gates<SH::C> gates[2];
 };
 
 // The outputs of one block of a head's chunks, from the state in front of the
 // block (a record of `prefix`, or S_in / z_in, or nothing).
 template <typename T, int D, int PHI>
-__global__ void __launch_bounds__(Shape<T, D>::THREADS, sizeof(T) == 2 && D == 64 ? 3 : 1)
+__global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? (sizeof(T) == 2 ? 4 : 3) : 1)
 gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                    const uint8_t* __restrict__ gates, const float* prefix, const float* S_in, const float* z_in, int N, int block_tokens, int nblk,
                    int normalize, T* __restrict__ out, float* S_out, float* z_out) {
@@ -53,9 +53,9 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     auto fetch = [&](int c) {
         const int row0 = first + c * C;
         load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, nullptr, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][0], q, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][1], k, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][2], v, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], q, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], k, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][2], v, row0, N);
         cp_async_commit();
     };
     fetch(0);
@@ -76,8 +76,8 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     for (int c = 0; c < nch; ++c) {
         cp_async_wait<0>();
         __syncthreads();
-        if (c + 1 < nch) fetch(c + 1);
-        const T *qt = sm.tiles[c & 1][0], *kt = sm.tiles[c & 1][1], *vt = sm.tiles[c & 1][2];
+        if (SH::ST == 2 && c + 1 < nch) fetch(c + 1);
+        const T *qt = sm.tiles[c % SH::ST][0], *kt = sm.tiles[c % SH::ST][1], *vt = sm.tiles[c % SH::ST][2];
         const Gates<C>& gs = sm.gates[c & 1];
         const int sb = SH::SB == 2 ? (c & 1) : 0;
         const T* sop = sm.sop[sb];
@@ -192,8 +192,9 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         }
         if (c + 1 < nch || S_out) {
             st.template update<PHI>(kt, vt, gs.to_end, nullptr, true, gs.all, warp, lane);
-            if (SH::SB == 1) __syncthreads();  // every warp has read the operand
+            if (SH::SB == 1) __syncthreads();  // every warp has read the operand and the tiles
             if (c + 1 < nch) {
+                if (SH::ST == 1) fetch(c + 1);
                 const int nb = SH::SB == 2 ? ((c + 1) & 1) : 0;
                 st.publish(sm.sop[nb], sm.zs[nb], warp, lane);
             }
@@ -232,8 +233,8 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8
     auto fetch = [&](int c) {
         const int row0 = first + chunk(c) * C;
         load_gates<C>(sm.gates[c & 1], gates + (size_t)chunk(c) * kGateBytes<C>, wq, up, col, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][0], x, row0, N);
-        load_tile<SH, T, D>(sm.tiles[c & 1][1], y, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], x, row0, N);
+        load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], y, row0, N);
         cp_async_commit();
     };
     fetch(0);
@@ -244,11 +245,15 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8
     for (int c = 0; c < nch; ++c) {
         cp_async_wait<0>();
         __syncthreads();
-        if (c + 1 < nch) fetch(c + 1);
+        if (SH::ST == 2 && c + 1 < nch) fetch(c + 1);
         const Gates<C>& gs = sm.gates[c & 1];
-        st.template update<PHI>(sm.tiles[c & 1][0], sm.tiles[c & 1][1], REVERSE ? gs.from_start : gs.to_end,
+        st.template update<PHI>(sm.tiles[c % SH::ST][0], sm.tiles[c % SH::ST][1], REVERSE ? gs.from_start : gs.to_end,
                                 REVERSE ? gs.col : nullptr, !REVERSE || wq, gs.all, warp, lane);
         total *= gs.all;
+        if (SH::ST == 1 && c + 1 < nch) {
+            __syncthreads();  // every warp has read the tiles
+            fetch(c + 1);
+        }
     }
     float* r = rec + ((size_t)bh * nblk + blk) * (size_t)(D * D + D);
     st.store(r, r + D * D, warp, lane);

@@ -90,18 +90,21 @@ inline bool small_noncausal(const Problem& p, int sms) {
 
 // Blocks of the gated forms. A head in one block needs no pass over K and V
 // for block states, but its chunks run one after the other in one CTA, so
-// heads are cut until the blocks fill `per_sm` CTAs per SM. Blocks hold at
-// least 256 tokens, in multiples of 64.
+// heads are cut until the blocks fill `per_sm` CTAs per SM. Blocks are multiples
+// of 64 tokens: down to one chunk, since few heads leave most SMs idle (gradients
+// of 2x4x1000x64 fp32: 204 us with blocks of 256 tokens, 67 with 64); at d = 128,
+// where a block's record is as large as 64 of its tokens, 128, or 256 on the
+// tensor cores.
 inline BlockPlan gated_plan(const Problem& p, int sms, int per_sm) {
+    const long long least = p.d < 128 ? 64 : p.dtype == 0 ? 128 : 256;
     const long long target = std::max(1LL, (long long)per_sm * sms / p.bh());
-    const long long bt = std::max(256LL, round_up(cdiv(p.N, target), 64));
+    const long long bt = std::max(least, round_up(cdiv(p.N, target), 64));
     return BlockPlan{(int)bt, (int)cdiv(p.N, bt)};
 }
 // CTAs per SM of the gated sweeps (shared memory and registers): forward, gradients.
 inline int gated_ctas_per_sm(const Problem& p, bool backward) {
     if (p.d == 128) return 1;
-    if (p.d == 64) return backward || p.dtype == 0 ? 2 : 3;
-    return backward ? 3 : 4;
+    return backward || (p.dtype == 0 && p.d == 64) ? 3 : 4;
 }
 
 }  // namespace plan

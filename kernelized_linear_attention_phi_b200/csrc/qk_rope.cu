@@ -152,7 +152,9 @@ template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_constant__ Args p) {
     using TU = Turn<T, D, PAIRS>;
     constexpr int EPV = TU::EPV, LPR = TU::LPR, RPB = kThreads / LPR;
-    constexpr int U = 2;  // two rows each of x and dy in flight
+    // one row each of x and dy: more only costs registers and with them warps
+    // (3x1777x(12+4)x128 fp32: 42 us with two rows, 36 with one)
+    constexpr int U = 1;
     __shared__ float red[RPB][D];
     const int l = threadIdx.x % LPR;
     const int which = (int)blockIdx.y >= p.s[0].groups;
@@ -219,22 +221,28 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_cons
     }
 }
 
-// dw of queries (block 0) and keys (block 1): rows of `part` in a fixed order.
+// dw: rows of `part` in a fixed order. A block adds 16 columns of the queries'
+// rows or of the keys' (64 slices of the rows, then the slices).
+constexpr int kColumns = 16, kSlices = 1024 / kColumns;
 __global__ void __launch_bounds__(1024)
 qk_rope_weights_kernel(const float* __restrict__ part, int rows_q, int rows_k, int d, float* dwq, float* dwk) {
-    __shared__ float red[1024];
-    const int slices = 1024 / d, a = threadIdx.x % d, s = threadIdx.x / d;
-    const int rows = blockIdx.x ? rows_k : rows_q;
-    const float* src = part + (blockIdx.x ? (size_t)rows_q * d : 0);
+    __shared__ float red[kSlices][kColumns + 1];
+    const int c = threadIdx.x % kColumns, s = threadIdx.x / kColumns;
+    const bool keys = (int)blockIdx.x >= d / kColumns;
+    const int a = (blockIdx.x % (d / kColumns)) * kColumns + c, rows = keys ? rows_k : rows_q;
+    const float* src = part + (keys ? (size_t)rows_q * d : 0) + a;
     pdl_wait();
     float sum = 0.f;
 #pragma unroll 8
-    for (int r = s; r < rows; r += slices) sum += src[(size_t)r * d + a];
-    red[threadIdx.x] = sum;
+    for (int r = s; r < rows; r += kSlices) sum += src[(size_t)r * d];
+    red[s][c] = sum;
     __syncthreads();
-    if (s == 0) {
-        for (int i = 1; i < slices; ++i) sum += red[i * d + a];
-        (blockIdx.x ? dwk : dwq)[a] = sum;
+    if (threadIdx.x < 32 * kColumns) {  // a warp per column
+        const int col = threadIdx.x / 32, l = threadIdx.x % 32;
+        float x = red[l][col] + red[l + 32][col];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (l == 0) (keys ? dwk : dwq)[(blockIdx.x % (d / kColumns)) * kColumns + col] = x;
     }
 }
 
@@ -259,8 +267,10 @@ Grid backward_grid(const la_rope_desc& p, int sms) {
     g.gq = (p.Hq + g.per - 1) / g.per;
     g.gk = (p.Hk + g.per - 1) / g.per;
     const long long rpb = kThreads / lanes_per_row(p), blocks = ((long long)p.B * p.N + rpb - 1) / rpb;
-    const long long fill = ((long long)sms * 8 + g.gq + g.gk - 1) / (g.gq + g.gk);
-    g.x = (int)(blocks < fill ? blocks : fill);
+    // as many rounds over the tokens for every CTA, at most 16 CTAs per SM in all
+    const long long fill = ((long long)sms * 16 + g.gq + g.gk - 1) / (g.gq + g.gk);
+    const long long rounds = (blocks + fill - 1) / fill;
+    g.x = (int)((blocks + rounds - 1) / rounds);
     return g;
 }
 
@@ -332,7 +342,7 @@ cudaError_t qk_norm_rope_backward(const la_rope_desc& p, const void* q, const la
                           dim3((unsigned)g.x, (unsigned)(g.gq + g.gk)), dim3(kThreads), 0, st, a);
     });
     if (e != cudaSuccess || dwq == nullptr) return e;
-    return launch_pdl(qk_rope_weights_kernel, dim3(2), dim3(1024), 0, st, static_cast<const float*>(part), g.gq * g.x,
+    return launch_pdl(qk_rope_weights_kernel, dim3(2 * (unsigned)p.d / kColumns), dim3(1024), 0, st, static_cast<const float*>(part), g.gq * g.x,
                       g.gk * g.x, p.d, dwq, dwk);
 }
 

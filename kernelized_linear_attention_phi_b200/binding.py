@@ -405,6 +405,13 @@ def _arg(name, t, dtype, shape, index):
     return t.data_ptr()
 
 
+def _scratch(ref, nbytes):
+    """A workspace that nobody but one call sees: its error word, which no one
+    can ask for afterwards, needs no clearing. (0 bytes: a request that the
+    library is about to refuse.)"""
+    return ref.new_empty((max(nbytes, 16),), dtype=torch.uint8)
+
+
 @functools.lru_cache(maxsize=256)
 def _gated_desc(shape, dtype, phi, normalize):
     if len(shape) != 4:
@@ -441,7 +448,7 @@ def la_gated_causal(q, k, v, g, S_in=None, z_in=None, out=None, S_out=None, z_ou
                 args += (_arg("S", S, torch.float32, (B, H, d, d), i), _arg("z", z, torch.float32, (B, H, d), i))
         out = torch.empty_like(q) if out is None else out
         args.insert(6, _arg("out", out, dt, shape, i))
-        ws = workspace(desc, "gated_causal", device=q.device) if ws is None else _ws(ws, q)
+        ws = _scratch(q, la_workspace_size(desc, "gated_causal")) if ws is None else _ws(ws, q)
         _check("la_gated_causal", lib().la_gated_causal(ctypes.byref(desc), *args, ws.data_ptr(), ws.numel(), st))
     return out
 
@@ -453,7 +460,7 @@ def la_gated_causal_backward(q, k, v, g, dout, dq=None, dk=None, dv=None, dg=Non
     shape, dt = q.shape, q.dtype
     desc = _gated_desc(shape, dt, phi, bool(normalize))
     with _on(q, stream) as st:
-        i, dev = q.get_device(), q.device
+        i = q.get_device()
         gates = tuple(shape[:3])
         args = [_arg("q", q, dt, shape, i), _arg("k", k, dt, shape, i), _arg("v", v, dt, shape, i),
                 _arg("g", g, dt, gates, i), _arg("dout", dout, dt, shape, i)]
@@ -463,7 +470,7 @@ def la_gated_causal_backward(q, k, v, g, dout, dq=None, dk=None, dv=None, dg=Non
         dg = torch.empty_like(g) if dg is None else dg
         args += (_arg("dq", dq, dt, shape, i), _arg("dk", dk, dt, shape, i), _arg("dv", dv, dt, shape, i),
                  _arg("dg", dg, dt, gates, i))
-        ws = workspace(desc, "gated_causal_bwd", device=dev) if ws is None else _ws(ws, q)
+        ws = _scratch(q, la_workspace_size(desc, "gated_causal_bwd")) if ws is None else _ws(ws, q)
         _check("la_gated_causal_backward", lib().la_gated_causal_backward(
             ctypes.byref(desc), *args, ws.data_ptr(), ws.numel(), st))
     return dq, dk, dv, dg
@@ -561,7 +568,7 @@ def la_qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, dq_out, dk_out,
     None."""
     with _on(q, stream) as st:
         desc, args = _rope_inputs(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-        i, dt, dev = q.get_device(), q.dtype, q.device
+        i, dt = q.get_device(), q.dtype
         B, N, Hq, d = q.shape
         args += (_arg("dq_out", dq_out, dt, (B, Hq, N, d), i), _arg("dk_out", dk_out, dt, (B, desc.Hk, N, d), i))
         dq = q.new_empty(q.shape) if dq is None else dq
@@ -580,8 +587,7 @@ def la_qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, dq_out, dk_out,
             args += (_arg("dq_weight", dq_weight, torch.float32, (d,), i),
                      _arg("dk_weight", dk_weight, torch.float32, (d,), i))
         if ws is None:
-            n = int(lib().la_qk_norm_rope_workspace_size(ctypes.byref(desc)))
-            ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+            ws = _scratch(q, int(lib().la_qk_norm_rope_workspace_size(ctypes.byref(desc))))
         else:
             _ws(ws, q)
         _check("la_qk_norm_rope_backward", lib().la_qk_norm_rope_backward(

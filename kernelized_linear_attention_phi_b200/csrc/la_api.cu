@@ -83,7 +83,7 @@ plan::BlockPlan block_plan(const Problem& p) { return plan::block_plan(p, device
 using plan::BlockPlan;
 using plan::SplitPlan;
 BlockPlan gated_plan(const Problem& p, bool backward) {
-    return plan::gated_plan(p, device_sms(), plan::gated_ctas_per_sm(p, backward));
+    return plan::gated_plan(p, device_sms(), plan::gated_ctas_per_sm(p, backward), backward);
 }
 
 int prefix_nbins(const Problem& p, int kchunk) { return p.N / kchunk + 1; }

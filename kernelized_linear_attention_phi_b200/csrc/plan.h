@@ -92,13 +92,18 @@ inline bool small_noncausal(const Problem& p, int sms) {
 // for block states, but its chunks run one after the other in one CTA, so
 // heads are cut until the blocks fill `per_sm` CTAs per SM. Blocks are multiples
 // of 64 tokens: down to one chunk, since few heads leave most SMs idle (gradients
-// of 2x4x1000x64 fp32: 204 us with blocks of 256 tokens, 67 with 64); at d = 128,
-// where a block's record is as large as 64 of its tokens, 128, or 256 on the
-// tensor cores.
-inline BlockPlan gated_plan(const Problem& p, int sms, int per_sm) {
-    const long long least = p.d < 128 ? 64 : p.dtype == 0 ? 128 : 256;
+// of 2x4x1000x64 fp32: 204 us with blocks of 256 tokens, 67 with 64), but 256
+// on the tensor cores, whose pipeline takes longer to fill (d = 128 bf16 forward).
+// A row of a few chunks stays in one block whatever the heads are: its chunks
+// in turn take less time than launching the block states and their scan (2x8
+// heads bf16 forward, 256 tokens: 16 us against 20; fp32 at d = 64 39 against 28,
+// so fewer there, and at d = 128 none).
+inline BlockPlan gated_plan(const Problem& p, int sms, int per_sm, bool backward) {
+    const bool tensor = p.d == 128 && p.dtype == 1 && !backward;
+    const long long whole = p.d == 128 ? 64 : backward || (p.dtype == 0 && p.d == 64) ? 128 : 256;
+    if (!tensor && p.N <= whole) return BlockPlan{(int)round_up(p.N, 64), 1};
     const long long target = std::max(1LL, (long long)per_sm * sms / p.bh());
-    const long long bt = std::max(least, round_up(cdiv(p.N, target), 64));
+    const long long bt = std::max(tensor ? 256LL : 64LL, round_up(cdiv(p.N, target), 64));
     return BlockPlan{(int)bt, (int)cdiv(p.N, bt)};
 }
 // CTAs per SM of the gated sweeps (shared memory and registers): forward, gradients.

@@ -84,7 +84,8 @@ def check_forward(q, k, v, g, dt, phi, normalize, state=None):
     B, H, N, d = q.shape
     S, z = torch.full((B, H, d, d), np.nan, device="cuda"), torch.full((B, H, d), np.nan, device="cuda")
     kw = {} if state is None else {"S_in": state[0], "z_in": state[1]}
-    out = la.la_gated_causal(q, k, v, g, S_out=S, z_out=z, phi=phi, normalize=normalize, **kw)
+    ws = la.workspace(la.make_desc(B, H, N, d, q.dtype, phi, normalize), "gated_causal")  # its error word is checked afterwards
+    out = la.la_gated_causal(q, k, v, g, S_out=S, z_out=z, phi=phi, normalize=normalize, ws=ws, **kw)
     alone = la.la_gated_causal(q, k, v, g, phi=phi, normalize=normalize, **kw)
     assert torch.equal(out, alone)
     kw = {} if state is None else {"S0": f64(state[0]), "z0": f64(state[1])}
@@ -98,7 +99,8 @@ def check_forward(q, k, v, g, dt, phi, normalize, state=None):
 def check_backward(q, k, v, g, dt, phi, normalize, seed=0):
     B, H, N, d = q.shape
     dout = upstream(q, seed)
-    got = la.la_gated_causal_backward(q, k, v, g, dout, phi=phi, normalize=normalize)
+    ws = la.workspace(la.make_desc(B, H, N, d, q.dtype, phi, normalize), "gated_causal_bwd")
+    got = la.la_gated_causal_backward(q, k, v, g, dout, phi=phi, normalize=normalize, ws=ws)
     ref, scale, around = G.heads(G.gated_backward, f64(q), f64(k), f64(v), f64(g), f64(dout), phi_kind=phi,
                                  normalize=normalize)
     _, dq, dv, dg = roundings(dt, d, N, phi, normalize)

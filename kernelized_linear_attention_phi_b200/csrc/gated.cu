@@ -239,10 +239,10 @@ cudaError_t gated_sweep(const Problem& p, const void* q, const void* k, const vo
 }
 cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* wq,
                          const float* up,
-                         const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
+                         const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                          cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_states_t<float> : gated_states_t<__nv_bfloat16>;
-    return f(p, reverse, x, y, gates, wq, up, col, block_tokens, nblk, blk0, count, rec, dec, st);
+    return f(p, reverse, x, y, gates, wq, up, col, block_tokens, nblk, blk0, count, exact, rec, dec, st);
 }
 cudaError_t gated_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
                         const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,

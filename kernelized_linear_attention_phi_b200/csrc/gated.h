@@ -25,10 +25,11 @@ cudaError_t gated_sweep(const Problem& p, const void* q, const void* k, const vo
 // Own states of `count` blocks from blk0 on: records rec[bh*nblk + blk] and the
 // products of the blocks' gates dec[bh*nblk + blk]. Forward: x = k, y = v, wq,
 // up and col null. Reverse (gradients): x = q, y = dout; wq, up, col as the
-// first sweep left them, null when not normalized.
+// first sweep left them, null when not normalized. exact: the terms of the
+// states keep all their bits (bf16), for a state that goes to the caller.
 cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* wq,
                          const float* up,
-                         const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
+                         const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                          cudaStream_t st);
 // In place: record blk becomes the state in front of block blk (reverse:
 // behind it). S_out / z_out (may be null, may alias S_in / z_in): the state
@@ -40,7 +41,7 @@ cudaError_t gated_scan(const Problem& p, bool reverse, float* rec, const float* 
 // states and outputs. An expired wait sets tc::FLAG_TIMEOUT in *err.
 bool tc_gated_supported(const Problem& p);
 cudaError_t tc_gated_states(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
-                            int count, float* part, float* dec, uint32_t* err, cudaStream_t st);
+                            int count, bool exact, float* part, float* dec, uint32_t* err, cudaStream_t st);
 cudaError_t tc_gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g,
                            const float* prefix, const float* S_in, const float* z_in, int block_tokens, int nblk, void* out,
                            uint32_t* err, cudaStream_t st);
@@ -73,7 +74,7 @@ cudaError_t gated_sweep_t(const Problem& p, const void* q, const void* k, const 
 template <typename T>
 cudaError_t gated_states_t(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* wq,
                          const float* up,
-                           const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
+                           const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                            cudaStream_t st);
 template <typename T>
 cudaError_t gated_bwd_q_t(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,

@@ -326,8 +326,14 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                     ys1 += w[n][2 + e];
                 }
             }
-            FragA<T> ax, ay;  // bf16: rounded once, like every operand of the gradients' products
-            make_a(ax, dp[0], dp[1]);
+            // bf16: rounded once, like every operand of the gradients' products, but
+            // for X under a positive map, from which delta Y is subtracted: that one
+            // in two parts (dq at 2 x 8 x 4096 x 64, relu + 1: 3.0e-3 off with one)
+            FragA<T> ax, xl, ay;
+            {
+                const float f[8] = {dp[0][0], dp[0][1], dp[0][2], dp[0][3], dp[1][0], dp[1][1], dp[1][2], dp[1][3]};
+                split_a(ax, xl, f);
+            }
             make_a(ay, w[0], w[1]);
 #pragma unroll
             for (int n = 0; n < NT / 2; ++n) {
@@ -337,6 +343,10 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 base_frag<PHI>(b[1]);
                 mma_step(acc[2 * n], ax, b[0]);
                 mma_step(acc[2 * n + 1], ax, b[1]);
+                if constexpr (LO) {
+                    mma_step(acc[2 * n], xl, b[0]);
+                    mma_step(acc[2 * n + 1], xl, b[1]);
+                }
                 if (normalize) {
                     mma_step(yk[2 * n], ay, b[0]);
                     mma_step(yk[2 * n + 1], ay, b[1]);

@@ -174,28 +174,31 @@ template <typename T, int D> struct State {
     // is formed in fp32 and multiplied as hi + lo operands, so a state of bf16
     // rows errs by 2^-17 of its terms, not by bf16's 2^-8.
     template <int PHI>
-    __device__ __forceinline__ void update(const T* x, const T* y, const float* w, const float* c, bool with_z, float all,
-                                           int warp, int lane) {
-        if (!owns(warp)) return;
+    __device__ __forceinline__ static void weighted(float (&f)[8], const T* x, const float* w, int k0, int warp, int lane) {
         const int t = lane & 3;
+        FragA<T> a;
+        load_at<SH::LD>(a, x, k0, row(warp), lane);
+        unpack(a, f);
+        const float2 w0 = *reinterpret_cast<const float2*>(w + k0 + 2 * t);
+        const float2 w1 = *reinterpret_cast<const float2*>(w + k0 + 8 + 2 * t);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            f[2 * r] = phi_f<PHI>(f[2 * r]) * w0.x;
+            f[2 * r + 1] = phi_f<PHI>(f[2 * r + 1]) * w0.y;
+            f[4 + 2 * r] = phi_f<PHI>(f[4 + 2 * r]) * w1.x;
+            f[5 + 2 * r] = phi_f<PHI>(f[5 + 2 * r]) * w1.y;
+        }
+    }
+    template <int PHI>
+    __device__ __forceinline__ void update(const T* x, const T* y, const float* w, const float* c, bool with_z, float all,
+                                           int warp, int lane, bool exact = false) {
+        if (!owns(warp)) return;
         constexpr int K = SH::C / 16;
         FragA<T> hi[K], lo[K];
 #pragma unroll
         for (int kt = 0; kt < K; ++kt) {
-            const int k0 = kt * 16;
-            FragA<T> a;
             float f[8];
-            load_at<SH::LD>(a, x, k0, row(warp), lane);
-            unpack(a, f);
-            const float2 w0 = *reinterpret_cast<const float2*>(w + k0 + 2 * t);
-            const float2 w1 = *reinterpret_cast<const float2*>(w + k0 + 8 + 2 * t);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                f[2 * r] = phi_f<PHI>(f[2 * r]) * w0.x;
-                f[2 * r + 1] = phi_f<PHI>(f[2 * r + 1]) * w0.y;
-                f[4 + 2 * r] = phi_f<PHI>(f[4 + 2 * r]) * w1.x;
-                f[5 + 2 * r] = phi_f<PHI>(f[5 + 2 * r]) * w1.y;
-            }
+            weighted<PHI>(f, x, w, kt * 16, warp, lane);
             split_a(hi[kt], lo[kt], f);
         }
         // A chunk's sum is formed from zero and then added: the matrix
@@ -241,6 +244,29 @@ template <typename T, int D> struct State {
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[e] = fmaf(z[e], all, s[e]);
+        }
+        if constexpr (!SH::F32) {
+            if (!exact) return;
+            // a state that a caller gets: the last bits of w phi(x) too
+#pragma unroll 1
+            for (int kt = 0; kt < K; ++kt) {
+                float f[8];
+                FragA<T> rest;
+                weighted<PHI>(f, x, w, kt * 16, warp, lane);
+                rest_a(rest, f);
+#pragma unroll
+                for (int n = 0; n < SH::SN / 16; ++n) {
+                    FragB<T> b[2];
+                    load_b<SH::LD>(b, y, kt * 16, col(warp) + 16 * n, lane);
+                    mma_step(S[2 * n], rest, b[0]);
+                    mma_step(S[2 * n + 1], rest, b[1]);
+                }
+                if (with_z && col(warp) == 0) {
+                    FragB<T> b;
+                    b.r[0] = b.r[1] = lane < 4 ? 0x3f803f80u : 0u;
+                    mma_step(z, rest, b);
+                }
+            }
         }
     }
 };

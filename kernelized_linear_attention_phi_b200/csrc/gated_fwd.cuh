@@ -191,7 +191,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             }
         }
         if (c + 1 < nch || S_out) {
-            st.template update<PHI>(kt, vt, gs.to_end, nullptr, true, gs.all, warp, lane);
+            st.template update<PHI>(kt, vt, gs.to_end, nullptr, true, gs.all, warp, lane, S_out != nullptr);
             if (SH::SB == 1) __syncthreads();  // every warp has read the operand and the tiles
             if (c + 1 < nch) {
                 if (SH::ST == 1) fetch(c + 1);
@@ -210,7 +210,8 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 template <typename T, int D, int PHI, bool REVERSE>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS)
 gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8_t* __restrict__ gates,
-                   const float* wq, const float* up, const float* col, int N, int block_tokens, int nblk, int blk0, float* __restrict__ rec,
+                   const float* wq, const float* up, const float* col, int N, int block_tokens, int nblk, int blk0, bool exact,
+                   float* __restrict__ rec,
                    float* __restrict__ dec) {
     using SH = Shape<T, D>;
     constexpr int C = SH::C;
@@ -248,7 +249,7 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8
         if (SH::ST == 2 && c + 1 < nch) fetch(c + 1);
         const Gates<C>& gs = sm.gates[c & 1];
         st.template update<PHI>(sm.tiles[c % SH::ST][0], sm.tiles[c % SH::ST][1], REVERSE ? gs.from_start : gs.to_end,
-                                REVERSE ? gs.col : nullptr, !REVERSE || wq, gs.all, warp, lane);
+                                REVERSE ? gs.col : nullptr, !REVERSE || wq, gs.all, warp, lane, !REVERSE && exact);
         total *= gs.all;
         if (SH::ST == 1 && c + 1 < nch) {
             __syncthreads();  // every warp has read the tiles
@@ -276,7 +277,7 @@ cudaError_t launch_sweep(const Problem& p, const void* q, const void* k, const v
 
 template <typename T, int D, int PHI>
 cudaError_t launch_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates,
-                          const float* wq, const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
+                          const float* wq, const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                           cudaStream_t st) {
     constexpr size_t smem = sizeof(StateSmem<T, D>);
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -286,13 +287,13 @@ cudaError_t launch_states(const Problem& p, bool reverse, const void* x, const v
         if (e != cudaSuccess) return e;
         return launch_pdl(gated_state_kernel<T, D, PHI, true>, grid, dim3(Shape<T, D>::THREADS), smem, st,
                           static_cast<const T*>(x), static_cast<const T*>(y), gates, wq, up, col, p.N,
-                          block_tokens, nblk, blk0, rec, dec);
+                          block_tokens, nblk, blk0, exact, rec, dec);
     }
     const cudaError_t e = ensure_smem<gated_state_kernel<T, D, PHI, false>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(gated_state_kernel<T, D, PHI, false>, grid, dim3(Shape<T, D>::THREADS), smem, st,
                       static_cast<const T*>(x), static_cast<const T*>(y), gates, wq, up, col, p.N,
-                      block_tokens, nblk, blk0, rec, dec);
+                      block_tokens, nblk, blk0, exact, rec, dec);
 }
 
 }  // namespace gated
@@ -308,11 +309,11 @@ cudaError_t gated_sweep_t(const Problem& p, const void* q, const void* k, const 
 }
 template <typename T>
 cudaError_t gated_states_t(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates,
-                           const float* wq, const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, float* rec, float* dec,
+                           const float* wq, const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                            cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
         return gated::launch_states<T, decltype(d)::value, decltype(phi)::value>(p, reverse, x, y, gates, wq, up, col, block_tokens,
-                                                                                nblk, blk0, count, rec, dec, st);
+                                                                                nblk, blk0, count, exact, rec, dec, st);
     });
 }
 

@@ -106,6 +106,15 @@ __device__ __forceinline__ void split_a(FragA<__nv_bfloat16>& hi, FragA<__nv_bfl
     }
 }
 __device__ __forceinline__ void split_a(FragA<float>& hi, FragA<float>&, const float (&f)[8]) { make_a(hi, f); }
+// The last 8 bits: what split_a leaves.
+__device__ __forceinline__ void rest_a(FragA<__nv_bfloat16>& rest, const float (&f)[8]) {
+    FragA<__nv_bfloat16> hi, lo;
+    split_a(hi, lo, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        rest.r[i] = pack_bf16((f[2 * i] - bf16_lo(hi.r[i])) - bf16_lo(lo.r[i]),
+                              (f[2 * i + 1] - bf16_hi(hi.r[i])) - bf16_hi(lo.r[i]));
+}
 
 // ---- feature map on operands ------------------------------------------------------
 // Rounded to the operand's type: relu(x) + 1 in packed bf16 arithmetic equals

@@ -599,7 +599,7 @@ la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, con
         const int count = S_out ? bp.nblk : bp.nblk - 1;
         if (count == 0)
             return cuda_status(tc_gated_sweep(p, q, k, v, g, nullptr, S_in, z_in, bp.block_tokens, 1, out, flags, st));
-        LA_TRY(cuda_status(tc_gated_states(p, k, v, g, bp.block_tokens, bp.nblk, count, part, dec, flags, st)));
+        LA_TRY(cuda_status(tc_gated_states(p, k, v, g, bp.block_tokens, bp.nblk, count, S_out != nullptr, part, dec, flags, st)));
         LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));
         return cuda_status(tc_gated_sweep(p, q, k, v, g, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, flags, st));
     }
@@ -608,7 +608,7 @@ la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, con
     if (bp.nblk == 1)
         return cuda_status(gated_sweep(p, q, k, v, gates, nullptr, S_in, z_in, bp.block_tokens, 1, out, S_out, z_out, st));
     LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
-                                    S_out ? bp.nblk : bp.nblk - 1, part, dec, st)));
+                                    S_out ? bp.nblk : bp.nblk - 1, S_out != nullptr, part, dec, st)));
     LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));
     return cuda_status(gated_sweep(p, q, k, v, gates, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, nullptr,
                                    nullptr, st));
@@ -641,14 +641,14 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
         part = at<float>(ws, L.part);
         dec = at<float>(ws, L.dec);
         LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
-                                        bp.nblk - 1, part, dec, st)));
+                                        bp.nblk - 1, false, part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
     LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, gates, dout, part, bp.block_tokens, bp.nblk, dq, wq, up, col, dgp, chunks,
                                    st)));
     if (bp.nblk > 1) {  // the same records, from the other end
-        LA_TRY(cuda_status(gated_states(p, true, q, dout, gates, wq, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, part,
-                                        dec, st)));
+        LA_TRY(cuda_status(gated_states(p, true, q, dout, gates, wq, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, false,
+                                        part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, true, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
     return cuda_status(gated_bwd_kv(p, q, k, v, g, gates, dout, part, bp.block_tokens, bp.nblk, wq, up, col, dgp, chunks,

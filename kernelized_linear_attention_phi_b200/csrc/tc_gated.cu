@@ -4,7 +4,8 @@
 //   S = sum_j w_j phi(k_j) (x) v_j,  w_j = product of the block's gates behind j,
 // with the weights relative to the block's end: the chunks run from the last
 // to the first, so w is a running product and S is never rescaled. w phi(K) is
-// formed in fp32 and multiplied as two bf16 operands (error 2^-17 of a term).
+// formed in fp32 and multiplied as two bf16 operands (error 2^-17 of a term), or
+// three for a state that the caller gets (none).
 //
 // Sweep (tc_gated_sweep_kernel): the transposed layout of the ungated d = 128
 // sweep (tc_sweep_t.cu): S^T and O^T have d_v = 128 lanes. Per chunk, with
@@ -36,7 +37,7 @@ struct GsCfg {
     static constexpr int FLUSH = 8;                 // chunks per accumulation in TMEM
     static constexpr int PREP = 512, RED = PREP / 32 * D * 4;
     static constexpr int NBAR = 3 * STAGES + 2;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 2 * TILE + RED + STAGES * C * 4 + 8 * NBAR + 16;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 4 * TILE + RED + STAGES * C * 4 + 8 * NBAR + 16;
     static constexpr int THREADS = 64 + PREP;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -48,14 +49,14 @@ struct GsCfg {
 template <int PHI>
 __global__ void __launch_bounds__(GsCfg::THREADS, 1)
 tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                      const __nv_bfloat16* __restrict__ gate, int N, int block_tokens, int nblk, float* __restrict__ part,
-                      float* __restrict__ dec, uint32_t* __restrict__ err) {
+                      const __nv_bfloat16* __restrict__ gate, int N, int block_tokens, int nblk, int exact,
+                      float* __restrict__ part, float* __restrict__ dec, uint32_t* __restrict__ err) {
     using CF = GsCfg;
     constexpr int D = CF::D, C = CF::C;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = align1024(smem_raw);
-    uint8_t* lo = stages + CF::STAGES * CF::STAGE;  // low parts of two chunks
-    float* red = reinterpret_cast<float*>(lo + 2 * CF::TILE);
+    uint8_t* lo = stages + CF::STAGES * CF::STAGE;  // low parts of two chunks, then their last bits
+    float* red = reinterpret_cast<float*>(lo + 4 * CF::TILE);
     float* wts = red + CF::RED / 4;  // [stage][C]
     uint64_t* full = reinterpret_cast<uint64_t*>(wts + CF::STAGES * C);
     uint64_t* tdone = full + CF::STAGES;
@@ -137,6 +138,10 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                 uint32_t add = i % CF::FLUSH > 0 ? 1u : 0u;
 #pragma unroll
                 for (int kk = 0; kk < C / 16; ++kk) {  // 16 tokens: 16 rows of 128 bytes
+                    if (exact) {
+                        mma_bf16(d, l0 + 2 * (CF::TILE >> 4) + kk * 128, v0 + kk * 128, id, add);
+                        add = 1u;
+                    }
                     mma_bf16(d, l0 + kk * 128, v0 + kk * 128, id, add);
                     add = 1u;
                     mma_bf16(d, k0 + kk * 128, v0 + kk * 128, id, 1u);
@@ -192,6 +197,14 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                 weighted8<PHI>(*kp, w[et >> 3], f, phi, hi, rest);
                 *kp = hi;
                 *reinterpret_cast<uint4*>(lt + bx * CF::BOX + et * 16) = rest;
+                if (exact) {  // a state that the caller gets keeps all bits of w phi(K)
+                    float a[8], b[8];
+                    unpack8(hi, a);
+                    unpack8(rest, b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a[e] = (f[e] - a[e]) - b[e];
+                    *reinterpret_cast<uint4*>(lt + 2 * CF::TILE + bx * CF::BOX + et * 16) = pack8(a);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) zk[bx][e] += f[e];
             }
@@ -718,7 +731,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 
 template <int PHI>
 cudaError_t launch_state(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
-                         int count, float* part, float* dec, uint32_t* err, cudaStream_t st) {
+                         int count, bool exact, float* part, float* dec, uint32_t* err, cudaStream_t st) {
     using CF = GsCfg;
     CUtensorMap mk, mv;
     cudaError_t e = make_map(&mk, k, CF::D, p.N, p.bh(), CF::C);
@@ -726,7 +739,7 @@ cudaError_t launch_state(const Problem& p, const void* k, const void* v, const v
     if (e == cudaSuccess) e = ensure_smem<tc_gated_state_kernel<PHI>>(CF::SMEM);
     if (e != cudaSuccess) return e;
     return launch_pdl(tc_gated_state_kernel<PHI>, dim3((unsigned)count, (unsigned)p.bh()), dim3(CF::THREADS), CF::SMEM, st,
-                      mk, mv, static_cast<const __nv_bfloat16*>(g), p.N, block_tokens, nblk, part, dec, err);
+                      mk, mv, static_cast<const __nv_bfloat16*>(g), p.N, block_tokens, nblk, (int)exact, part, dec, err);
 }
 
 template <int PHI>
@@ -751,11 +764,11 @@ cudaError_t launch_sweep(const Problem& p, const void* q, const void* k, const v
 bool tc_gated_supported(const Problem& p) { return p.dtype == DT_BF16 && p.d == 128; }
 
 cudaError_t tc_gated_states(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
-                            int count, float* part, float* dec, uint32_t* err, cudaStream_t st) {
+                            int count, bool exact, float* part, float* dec, uint32_t* err, cudaStream_t st) {
     auto* f = p.phi == PHI_RELU1  ? launch_state<PHI_RELU1>
               : p.phi == PHI_ELU1 ? launch_state<PHI_ELU1>
                                   : launch_state<PHI_IDENTITY>;
-    return f(p, k, v, g, block_tokens, nblk, count, part, dec, err, st);
+    return f(p, k, v, g, block_tokens, nblk, count, exact, part, dec, err, st);
 }
 
 cudaError_t tc_gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g,

@@ -12,8 +12,8 @@ of errors). With p = 2 for a feature map that rounds phi(q) and phi(k), else 0:
   dg   pair p, its gradient 3p + 1, state 1, phi(k) p / 2, result 1
 fp32 keeps 2^-22 in a product and 2^-23 in an addition to an accumulator; the
 longest way has 3 (d + N) / 8 additions, some 64 other operations, and at most
-three such sums in a row. A state's terms are split operands (bf16: 2^-17) in
-fp32 sums. fp32 sums over a chunk leave 2^-15 of its pairs in dg whatever dg is."""
+three such sums in a row. A state's terms keep 24 bits (fp32: 2^-22 of a
+product) in fp32 sums. fp32 sums over a chunk leave 2^-15 of its pairs in dg whatever dg is."""
 
 import numpy as np
 import pytest
@@ -44,7 +44,7 @@ def roundings(dt, d, N, phi, normalize):
 
 
 def state_tol(dt, d, N):
-    return 3 * (d + N) / 8 * 2.0 ** -23 + (2.0 ** -16 if dt == "bf16" else 2.0 ** -20)
+    return 3 * (d + N) / 8 * 2.0 ** -23 + 2.0 ** -20
 
 
 def gates(B, H, N, dt, seed, docs=0, span=30.0):
@@ -87,10 +87,12 @@ def check_forward(q, k, v, g, dt, phi, normalize, state=None):
     ws = la.workspace(la.make_desc(B, H, N, d, q.dtype, phi, normalize), "gated_causal")  # its error word is checked afterwards
     out = la.la_gated_causal(q, k, v, g, S_out=S, z_out=z, phi=phi, normalize=normalize, ws=ws, **kw)
     alone = la.la_gated_causal(q, k, v, g, phi=phi, normalize=normalize, **kw)
-    assert torch.equal(out, alone)
     kw = {} if state is None else {"S0": f64(state[0]), "z0": f64(state[1])}
     ref, scale = G.heads(G.gated, f64(q), f64(k), f64(v), f64(g), phi_kind=phi, normalize=normalize, **kw)
-    close("out", out, ref[0], scale[0], roundings(dt, d, N, phi, normalize)[0])
+    # a call that returns its state forms it from more bits: the outputs of the
+    # two calls may differ in their last place
+    for name, o in (("out", out), ("out without a state", alone)):
+        close(name, o, ref[0], scale[0], roundings(dt, d, N, phi, normalize)[0])
     close("S", S, ref[1], scale[1], state_tol(dt, d, N))
     close("z", z, ref[2], scale[2], state_tol(dt, d, N))
     return out, S, z

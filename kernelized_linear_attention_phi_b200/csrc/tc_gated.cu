@@ -34,7 +34,6 @@ struct GsCfg {
     static constexpr int D = 128, C = 64, NB = 2, BOX = C * 128, TILE = NB * BOX;
     static constexpr int STAGES = 4;
     static constexpr int STAGE = 2 * TILE;          // K (becomes the high part), V
-    static constexpr int FLUSH = 8;                 // chunks per accumulation in TMEM
     static constexpr int PREP = 512, RED = PREP / 32 * D * 4;
     static constexpr int NBAR = 3 * STAGES + 2;
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 4 * TILE + RED + STAGES * C * 4 + 8 * NBAR + 16;
@@ -42,10 +41,11 @@ struct GsCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-// Warp 0: TMA and gates; warp 1: MMA; warps 2..17: w phi(K) in two parts, z, and
-// the accumulators' sums (each FLUSH chunks' products are added to fp32
-// registers, so long blocks do not depend on how the tensor core rounds its
-// additions).
+// Warp 0: TMA and gates; warp 1: MMA; warps 2..17: w phi(K) in its parts, z, and
+// the accumulators' sums: the products of 8 chunks, or 4 for a state that the
+// caller gets, are added to fp32 registers, so long blocks do not depend on how
+// the tensor core rounds its additions (S at 1x16x16384x128: 3.4e-7 off with 2
+// chunks, 6.9e-7 with 4, over 1e-6 with 8; 1x16x131072x128 takes 283, 257, 246 us).
 template <int PHI>
 __global__ void __launch_bounds__(GsCfg::THREADS, 1)
 tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
@@ -67,6 +67,7 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     const int blk = blockIdx.x, bh = blockIdx.y;
     const int first = blk * block_tokens, end = min(N, first + block_tokens);
     const int nci = (end - first + C - 1) / C;
+    const int per = exact ? 2 : 3;  // log2 of the chunks per accumulation
     if (threadIdx.x == 0) {
         cta_abort_reset();
         for (int s = 0; s < CF::STAGES; ++s) {
@@ -129,13 +130,13 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
         const uint64_t kd = sdesc(smem_u32(stages), CF::BOX, 1024), ld = sdesc(smem_u32(lo), CF::BOX, 1024);
 #pragma unroll 1
         for (int i = 0; i < nci; ++i) {
-            const int s = i % CF::STAGES, f = i / CF::FLUSH;
+            const int s = i % CF::STAGES, f = i >> per;
             if (!__all_sync(0xffffffffu, mbar_wait(tdone + s, (i / CF::STAGES) & 1, err))) break;
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t k0 = kd + s * (CF::STAGE >> 4), v0 = k0 + (CF::TILE >> 4), l0 = ld + (i & 1) * (CF::TILE >> 4);
                 const uint32_t d = tmem + (f & 1) * D;
-                uint32_t add = i % CF::FLUSH > 0 ? 1u : 0u;
+                uint32_t add = i & ((1 << per) - 1) ? 1u : 0u;
 #pragma unroll
                 for (int kk = 0; kk < C / 16; ++kk) {  // 16 tokens: 16 rows of 128 bytes
                     if (exact) {
@@ -147,7 +148,7 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                     mma_bf16(d, k0 + kk * 128, v0 + kk * 128, id, 1u);
                 }
                 mma_commit(empty + s);
-                if (i + 1 == nci || (i + 1) % CF::FLUSH == 0) mma_commit(acc + (f & 1));
+                if (i + 1 == nci || ((i + 1) & ((1 << per) - 1)) == 0) mma_commit(acc + (f & 1));
             }
             __syncwarp();
         }
@@ -181,7 +182,7 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
         for (int i = 0;; ++i) {
             const int s = i % CF::STAGES, u = i / CF::STAGES;
             // accumulator f is taken during the first chunk of flush f + 1, or at the end
-            if (i > 0 && (i == nci || i % CF::FLUSH == 0)) take((i - 1) / CF::FLUSH);
+            if (i > 0 && (i == nci || (i & ((1 << per) - 1)) == 0)) take((i - 1) >> per);
             if (i == nci) break;
             mbar_wait(full + s, u & 1, err);
             // the low part's buffer: chunk i - 2's products have read it

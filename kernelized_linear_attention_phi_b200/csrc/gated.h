@@ -37,11 +37,13 @@ cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const vo
 // is not read.
 cudaError_t gated_scan(const Problem& p, bool reverse, float* rec, const float* dec, int nblk, const float* S_in,
                        const float* z_in, float* S_out, float* z_out, cudaStream_t st);
-// The same on tcgen05 tensor cores (tc_gated.cu): bf16, d = 128, forward
-// states and outputs. An expired wait sets tc::FLAG_TIMEOUT in *err.
+// The same on tcgen05 tensor cores (tc_gated.cu): bf16, d = 128, states and
+// outputs, from g itself (reverse states: up and col, null when not normalized).
+// An expired wait sets tc::FLAG_TIMEOUT in *err.
 bool tc_gated_supported(const Problem& p);
-cudaError_t tc_gated_states(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
-                            int count, bool exact, float* part, float* dec, uint32_t* err, cudaStream_t st);
+cudaError_t tc_gated_states(const Problem& p, bool reverse, const void* x, const void* y, const void* g, const float* up,
+                            const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* part,
+                            float* dec, uint32_t* err, cudaStream_t st);
 cudaError_t tc_gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g,
                            const float* prefix, const float* S_in, const float* z_in, int block_tokens, int nblk, void* out,
                            uint32_t* err, cudaStream_t st);

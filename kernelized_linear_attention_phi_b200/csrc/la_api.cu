@@ -599,7 +599,8 @@ la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, con
         const int count = S_out ? bp.nblk : bp.nblk - 1;
         if (count == 0)
             return cuda_status(tc_gated_sweep(p, q, k, v, g, nullptr, S_in, z_in, bp.block_tokens, 1, out, flags, st));
-        LA_TRY(cuda_status(tc_gated_states(p, k, v, g, bp.block_tokens, bp.nblk, count, S_out != nullptr, part, dec, flags, st)));
+        LA_TRY(cuda_status(tc_gated_states(p, false, k, v, g, nullptr, nullptr, bp.block_tokens, bp.nblk, 0, count,
+                                           S_out != nullptr, part, dec, flags, st)));
         LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));
         return cuda_status(tc_gated_sweep(p, q, k, v, g, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, flags, st));
     }
@@ -637,17 +638,29 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
     float* dgp = at<float>(ws, L.dgp);
     void* chunks = at<char>(ws, L.chunks);
     float *part = nullptr, *dec = nullptr;
+    // block states on the tensor cores where the blocks are long enough to fill
+    // their pipeline (4x16x8192x128: 141 -> TCFIG us each way)
+    const bool tcs = tc_gated_supported(p) && bp.block_tokens >= 256;
+    uint32_t* flags = at<uint32_t>(ws, 0);
     if (bp.nblk > 1) {
         part = at<float>(ws, L.part);
         dec = at<float>(ws, L.dec);
-        LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
+        if (tcs)
+            LA_TRY(cuda_status(tc_gated_states(p, false, k, v, g, nullptr, nullptr, bp.block_tokens, bp.nblk, 0, bp.nblk - 1,
+                                               false, part, dec, flags, st)));
+        else
+            LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
                                         bp.nblk - 1, false, part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
     LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, gates, dout, part, bp.block_tokens, bp.nblk, dq, wq, up, col, dgp, chunks,
                                    st)));
     if (bp.nblk > 1) {  // the same records, from the other end
-        LA_TRY(cuda_status(gated_states(p, true, q, dout, gates, wq, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, false,
+        if (tcs)
+            LA_TRY(cuda_status(tc_gated_states(p, true, q, dout, g, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, false,
+                                               part, dec, flags, st)));
+        else
+            LA_TRY(cuda_status(gated_states(p, true, q, dout, gates, wq, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, false,
                                         part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, true, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }

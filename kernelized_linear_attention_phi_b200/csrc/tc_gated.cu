@@ -36,7 +36,7 @@ struct GsCfg {
     static constexpr int STAGE = 2 * TILE;          // K (becomes the high part), V
     static constexpr int PREP = 512, RED = PREP / 32 * D * 4;
     static constexpr int NBAR = 3 * STAGES + 2;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 4 * TILE + RED + STAGES * C * 4 + 8 * NBAR + 16;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 4 * TILE + RED + STAGES * 2 * C * 4 + 8 * NBAR + 16;
     static constexpr int THREADS = 64 + PREP;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -46,25 +46,28 @@ struct GsCfg {
 // caller gets, are added to fp32 registers, so long blocks do not depend on how
 // the tensor core rounds its additions (S at 1x16x16384x128: 3.4e-7 off with 2
 // chunks, 6.9e-7 with 4, over 1e-6 with 8; 1x16x131072x128 takes 283, 257, 246 us).
-template <int PHI>
+// REVERSE (gradients): K = q, V = dout, chunks in order, weights the product of
+// the block's gates up to the query times up_i = 1 / den_i, and z weighted by
+// col_i = -(out_i . dout_i); without up and col (not normalized) 1 and 0.
+template <int PHI, bool REVERSE>
 __global__ void __launch_bounds__(GsCfg::THREADS, 1)
 tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                      const __nv_bfloat16* __restrict__ gate, int N, int block_tokens, int nblk, int exact,
-                      float* __restrict__ part, float* __restrict__ dec, uint32_t* __restrict__ err) {
+                      const __nv_bfloat16* __restrict__ gate, const float* __restrict__ up, const float* __restrict__ col,
+                      int N, int block_tokens, int nblk, int blk0, int exact, float* __restrict__ part, float* __restrict__ dec, uint32_t* __restrict__ err) {
     using CF = GsCfg;
     constexpr int D = CF::D, C = CF::C;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = align1024(smem_raw);
     uint8_t* lo = stages + CF::STAGES * CF::STAGE;  // low parts of two chunks, then their last bits
     float* red = reinterpret_cast<float*>(lo + 4 * CF::TILE);
-    float* wts = red + CF::RED / 4;  // [stage][C]
-    uint64_t* full = reinterpret_cast<uint64_t*>(wts + CF::STAGES * C);
+    float* wts = red + CF::RED / 4;  // [stage][weights C | of z C]
+    uint64_t* full = reinterpret_cast<uint64_t*>(wts + CF::STAGES * 2 * C);
     uint64_t* tdone = full + CF::STAGES;
     uint64_t* empty = tdone + CF::STAGES;
     uint64_t* acc = empty + CF::STAGES;  // [2] accumulator complete
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc + 2);
     const int warp = warp_index(), lane = threadIdx.x % 32;
-    const int blk = blockIdx.x, bh = blockIdx.y;
+    const int blk = blk0 + blockIdx.x, bh = blockIdx.y;
     const int first = blk * block_tokens, end = min(N, first + block_tokens);
     const int nci = (end - first + C - 1) / C;
     const int per = exact ? 2 : 3;  // log2 of the chunks per accumulation
@@ -88,24 +91,44 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
 
-    // step i is chunk nci - 1 - i
+    // step i is chunk nci - 1 - i, or i
+    auto row_of = [&](int i) { return first + (REVERSE ? i : nci - 1 - i) * C; };
     if (warp == 0) {
         const __nv_bfloat16* g = gate + (size_t)bh * N;
-        long long after = 0;  // the gates behind the chunk, within the block
+        long long after = 0;  // the block's gates behind the chunk, or in front of it
         bool bad = false;
-        Gates2 gr = load_gates(g, first + (nci - 1) * C, end, lane);
+        Gates2 gr = load_gates(g, row_of(0), end, lane);
+        float2 ur = make_float2(1.f, 1.f), cr = make_float2(0.f, 0.f);
+        auto load_sums = [&](int row) {
+            if (!REVERSE || up == nullptr) return;
+            const size_t at = (size_t)bh * N + row + 2 * lane;
+            const bool in0 = row + 2 * lane < end, in1 = row + 2 * lane + 1 < end;
+            ur = make_float2(in0 ? up[at] : 0.f, in1 ? up[at + 1] : 0.f);
+            cr = make_float2(in0 ? col[at] : 0.f, in1 ? col[at + 1] : 0.f);
+        };
+        load_sums(row_of(0));
         int issued = 0;
 #pragma unroll 1
         for (int i = 0; i < nci; ++i) {
-            const int s = i % CF::STAGES, u = i / CF::STAGES, row = first + (nci - 1 - i) * C;
+            const int s = i % CF::STAGES, u = i / CF::STAGES, row = row_of(i);
             const GateSums<2> gs = sum_gates<2>(gr.g, lane);
             bad = bad || gs.bad & 4;
-            if (i + 1 < nci) gr = load_gates(g, row - C, end, lane);
+            if (i + 1 < nci) gr = load_gates(g, row_of(i + 1), end, lane);
+            const float2 un = ur, cn = cr;
+            if (i + 1 < nci) load_sums(row_of(i + 1));
             if (u > 0 && !__all_sync(0xffffffffu, mbar_wait(empty + s, (u - 1) & 1, err))) break;
-            float* w = wts + s * C + 2 * lane;
+            float* w = wts + s * 2 * C + 2 * lane;
             const float nan = bad ? NAN : 0.f;  // the block's state is NaN
-            w[0] = row + 2 * lane < end ? gate_pow2(after + (gs.last - gs.b[0])) + nan : 0.f;
-            w[1] = row + 2 * lane + 1 < end ? gate_pow2(after + (gs.last - gs.b[1])) + nan : 0.f;
+            const bool in0 = row + 2 * lane < end, in1 = row + 2 * lane + 1 < end;
+            if (REVERSE) {
+                w[0] = in0 ? gate_pow2(after + gs.b[0]) * un.x + nan : 0.f;
+                w[1] = in1 ? gate_pow2(after + gs.b[1]) * un.y + nan : 0.f;
+                w[C] = cn.x;
+                w[C + 1] = cn.y;
+            } else {
+                w[0] = in0 ? gate_pow2(after + (gs.last - gs.b[0])) + nan : 0.f;
+                w[1] = in1 ? gate_pow2(after + (gs.last - gs.b[1])) + nan : 0.f;
+            }
             after += gs.last;
             __syncwarp();
             if (elect_one()) {
@@ -189,7 +212,8 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
             if (i >= 2) mbar_wait(empty + (i - 2) % CF::STAGES, ((i - 2) / CF::STAGES) & 1, err);
             uint8_t* kt = stages + s * CF::STAGE;
             uint8_t* lt = lo + (i & 1) * CF::TILE;
-            const float* w = wts + s * C;
+            const float* w = wts + s * 2 * C;
+            const float zw = REVERSE ? w[C + (et >> 3)] : 1.f;
 #pragma unroll
             for (int bx = 0; bx < CF::NB; ++bx) {  // each thread one 16-byte chunk per box: token et >> 3
                 uint4* kp = reinterpret_cast<uint4*>(kt + bx * CF::BOX + et * 16);
@@ -207,7 +231,7 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                     *reinterpret_cast<uint4*>(lt + 2 * CF::TILE + bx * CF::BOX + et * 16) = pack8(a);
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) zk[bx][e] += f[e];
+                for (int e = 0; e < 8; ++e) zk[bx][e] = REVERSE ? fmaf(f[e], zw, zk[bx][e]) : zk[bx][e] + f[e];
             }
             fence_async_smem();
             tc_fence_before();
@@ -730,17 +754,18 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     }
 }
 
-template <int PHI>
-cudaError_t launch_state(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
-                         int count, bool exact, float* part, float* dec, uint32_t* err, cudaStream_t st) {
+template <int PHI, bool REVERSE>
+cudaError_t launch_state(const Problem& p, const void* k, const void* v, const void* g, const float* up, const float* col,
+                         int block_tokens, int nblk, int blk0, int count, bool exact, float* part, float* dec, uint32_t* err, cudaStream_t st) {
     using CF = GsCfg;
     CUtensorMap mk, mv;
     cudaError_t e = make_map(&mk, k, CF::D, p.N, p.bh(), CF::C);
     if (e == cudaSuccess) e = make_map(&mv, v, CF::D, p.N, p.bh(), CF::C);
-    if (e == cudaSuccess) e = ensure_smem<tc_gated_state_kernel<PHI>>(CF::SMEM);
+    if (e == cudaSuccess) e = ensure_smem<tc_gated_state_kernel<PHI, REVERSE>>(CF::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tc_gated_state_kernel<PHI>, dim3((unsigned)count, (unsigned)p.bh()), dim3(CF::THREADS), CF::SMEM, st,
-                      mk, mv, static_cast<const __nv_bfloat16*>(g), p.N, block_tokens, nblk, (int)exact, part, dec, err);
+    return launch_pdl(tc_gated_state_kernel<PHI, REVERSE>, dim3((unsigned)count, (unsigned)p.bh()), dim3(CF::THREADS), CF::SMEM, st,
+                      mk, mv, static_cast<const __nv_bfloat16*>(g), up, col, p.N, block_tokens, nblk, blk0, (int)exact, part, dec,
+                      err);
 }
 
 template <int PHI>
@@ -764,12 +789,16 @@ cudaError_t launch_sweep(const Problem& p, const void* q, const void* k, const v
 
 bool tc_gated_supported(const Problem& p) { return p.dtype == DT_BF16 && p.d == 128; }
 
-cudaError_t tc_gated_states(const Problem& p, const void* k, const void* v, const void* g, int block_tokens, int nblk,
-                            int count, bool exact, float* part, float* dec, uint32_t* err, cudaStream_t st) {
-    auto* f = p.phi == PHI_RELU1  ? launch_state<PHI_RELU1>
-              : p.phi == PHI_ELU1 ? launch_state<PHI_ELU1>
-                                  : launch_state<PHI_IDENTITY>;
-    return f(p, k, v, g, block_tokens, nblk, count, exact, part, dec, err, st);
+cudaError_t tc_gated_states(const Problem& p, bool reverse, const void* x, const void* y, const void* g, const float* up,
+                            const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* part,
+                            float* dec, uint32_t* err, cudaStream_t st) {
+    auto* f = reverse ? (p.phi == PHI_RELU1  ? launch_state<PHI_RELU1, true>
+                         : p.phi == PHI_ELU1 ? launch_state<PHI_ELU1, true>
+                                             : launch_state<PHI_IDENTITY, true>)
+                      : (p.phi == PHI_RELU1  ? launch_state<PHI_RELU1, false>
+                         : p.phi == PHI_ELU1 ? launch_state<PHI_ELU1, false>
+                                             : launch_state<PHI_IDENTITY, false>);
+    return f(p, x, y, g, up, col, block_tokens, nblk, blk0, count, exact, part, dec, err, st);
 }
 
 cudaError_t tc_gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const void* g,

@@ -209,8 +209,12 @@ LA_API la_status la_decode_step(const la_desc* desc, const void* q, const void* 
  * element type. g = 0 keeps everything (la_causal_chunked); g = -inf, or any g
  * below -9700, closes the gate: nothing before the token reaches it or a later
  * one, so rows of several documents carry g = -inf at each document's first
- * token. A positive g amplifies, within what fp32 can hold; a NaN gate makes
- * NaN of its head from there on. */
+ * token. q, k and v must be finite, padding and what lies in front of a closed
+ * gate included: masked products are multiplied by 0, not skipped, and a NaN
+ * may reach its head up to 63 tokens in front of its own. A positive g amplifies, within what fp32 can
+ * hold; a NaN or +inf gate makes NaN of its head from there on. N is at most
+ * 2^30. The state in front of a row reaches a query whose gates have closed
+ * since with a weight of at most 2^-90 next to its own key's. */
 
 /* Every output of a row, and optionally the state around it.
  * q, k, v: [B,H,N,d] inputs, g: [B,H,N] input; out: [B,H,N,d] output.

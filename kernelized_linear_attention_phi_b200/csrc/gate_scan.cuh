@@ -1,10 +1,8 @@
-// Running sums of log-gates over a chunk of 64 tokens by one warp, in units of
-// log2 and fixed point: 33 bits in front of the point and 31 behind it, as an
-// integer and a fraction in two registers. Integer sums are exact, so the
-// decay between two tokens depends on nothing but the gates between them,
-// however far the chunk has decayed; a gate itself is held to 2^-32. (64-bit
-// floating point would serve too, but its instructions' latency stood in the
-// sweeps' way: FIGURE3.)
+// Running sums of the log-gates of a chunk by one warp, in units of log2 and
+// fixed point (31 bits behind the point). Integer sums are exact: the decay
+// between two tokens depends on the gates between them and on nothing else,
+// however far the chunk has decayed before, and a closed gate drops out of every
+// difference behind it. A gate itself is held to 2^-32.
 #pragma once
 
 #include "common.cuh"
@@ -22,7 +20,7 @@ __device__ __forceinline__ long long gate_bits(float g) {
     if (!(x >= kClosedBits)) return (long long)(int)kClosedBits << 31;  // -inf too (a NaN is dealt with by the caller)
     const float n = rintf(fminf(x, 16000.f));
     const float f = (fminf(x, 16000.f) - n) + rest;  // at most half, and a little
-    return ((long long)(int)n << 31) + (int)(f * 2147483648.f * 0.99999994f);
+    return ((long long)(int)n << 31) + (int)(f * 2147483648.f);
 }
 // 2^b: the fraction alone goes through the fp32 function.
 __device__ __forceinline__ float gate_pow2(long long b) {

@@ -14,11 +14,15 @@ namespace gated {
 // it into RG row groups of 16 tokens and CG column groups of NCOL channels.
 // The state S (d x d, fp32) lives in the warps' registers: SRT row tiles of
 // 16, each cut into SCG column groups of SN columns. SB: operand copies of S
-// in shared memory, ST: chunks of tiles. At d <= 64 one of each leaves room for
-// four CTAs per SM, whose work covers a chunk's loads (STAGEFIG); at
-// d = 128 an SM holds one CTA, which loads a chunk ahead.
-// fp32 rows are twice as long, so d >= 64 takes chunks of 32 tokens to keep
-// two stages of tiles within the shared memory of an SM.
+// in shared memory, ST: chunks of tiles. What bounds these kernels is the
+// latency of one warp's chain of loads, products and barriers (4x16x8192x64
+// bf16, forward: the tensor pipe busy a quarter of the time, issue slots a
+// third). At d <= 64 one S and one chunk leave room for three or four CTAs
+// per SM, which cover for each other (with two chunks and two or three CTAs the
+// forward sweep takes 121 us, so 109; dk and dv 254, so 223); twice the warps on
+// a chunk gain nothing, since each then repeats more (194 us). At d = 128 an
+// SM holds one CTA, which loads a chunk ahead. fp32 rows are twice as long, so
+// d >= 64 takes chunks of 32 tokens.
 template <typename T, int D> struct Shape {
     static constexpr bool F32 = sizeof(T) == 4;
     static constexpr int C = F32 && D >= 64 ? 32 : 64;
@@ -26,16 +30,15 @@ template <typename T, int D> struct Shape {
     static constexpr int SB = F32 || D <= 64 ? 1 : 2;
     static constexpr int ST = D == 128 ? 2 : 1;
     static constexpr int THREADS = NW * 32;
-    static constexpr int LD = D + (F32 ? 8 : 8);
+    static constexpr int LD = D + 8;
     static constexpr int EPV = 16 / sizeof(T);
-    static constexpr int RG = C / 16, CG = NW / RG, NCOL = D / CG < 16 ? 16 : D / CG;
-    static constexpr int CGU = D / NCOL;  // column groups with work
+    static constexpr int RG = C / 16, CG = NW / RG, NCOL = D / CG;
     static constexpr int SRT = D / 16 < NW ? D / 16 : NW;
     static constexpr int SCG = (NW / SRT) < (D / 16) ? (NW / SRT) : (D / 16);
     static constexpr int SN = D / SCG;
     static constexpr int TILE = C * LD;  // elements of a [C x D] tile
     static constexpr int SOP = D * LD;   // elements of the S operand
-    static_assert(RG * CG == NW && SRT * 16 == D, "tiles");
+    static_assert(RG * CG == NW && SRT * 16 == D && NCOL % 16 == 0, "tiles");
 };
 
 // The gates of one chunk, from b_i = log2 of the product of the chunk's gates

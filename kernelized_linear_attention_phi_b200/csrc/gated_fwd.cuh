@@ -83,9 +83,10 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         const T* sop = sm.sop[sb];
         const float* zs = sm.zs[sb];
 
-        // The loops over the channels and the key groups stay rolled (by pairs
-        // of steps): a block often has only a few chunks, and then the time to
-        // fetch the code counts (1 x 4 x 1531 x 32 fp32: FIGURE).
+        // The loop over the key groups stays rolled, in fp32 the channels' too: a
+        // block often has only a few chunks, and then the time to fetch the code
+        // counts (1x4x1531x32 fp32, elu + 1: 61 us unrolled, 23 rolled). bf16 gains
+        // by the channels' products side by side (4x16x8192x64: 139 us -> 129).
         constexpr int NT = SH::NCOL / 8;
         float o[NT][4] = {}, oz[4] = {};
 #pragma unroll(SH::F32 ? 1 : D / 16)

@@ -11,12 +11,15 @@
 //   fp32: mma.m16n8k8 in tf32 on two-part operands, x = hi + lo with hi the
 //     nearest tf32 value, as hi*hi + hi*lo + lo*hi: the dropped lo*lo and the
 //     rounding of lo are at most 2^-23 of the product and of either sign, so
-//     the sums are fp32 sums. The order of k inside a step is free, so logical k = 2t, 2t + 1
-//     take the instruction's k = t, t + 4 and both types share the layout.
-// These products are a few percent of the tensor pipe's time at the
-// intensity of this method (about 60 flop per byte), and the state and the
-// decayed products live in registers between them, where the decay needs
-// them every 64 tokens.
+//     the sums are fp32 sums. The order of k inside a step is free, so logical
+//     k = 2t, 2t + 1 take the instruction's k = t, t + 4 and both types share
+//     the layout.
+// These are not the tensor cores' fastest instructions, but at the intensity of
+// this method (about 60 flop per byte) they would keep up with memory: 8 cycles
+// for 16 x 8 x 16 on a quarter of an SM, 1300 cycles for a chunk at d = 64. The
+// state and the decayed products stay in registers between them, where the
+// decay changes them every chunk. d = 128 in bf16, where they would not keep up,
+// runs on tcgen05 going forward (tc_gated.cu).
 #pragma once
 
 #include "common.cuh"
@@ -52,11 +55,11 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Nearest tf32 (the instruction drops the low 13 bits itself; half of their
-// range is added before). What is left keeps its own top 11 bits, rounded too.
+// range is added before). The rest has 12 bits at most and the instruction
+// keeps 11: the bit that it drops is half a step, so rounding it would gain
+// nothing, and the NaN that it is where x is a NaN stays one.
 __device__ __forceinline__ uint32_t tf32_hi(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
-__device__ __forceinline__ uint32_t tf32_lo(float x) {
-    return __float_as_uint(x - __uint_as_float(tf32_hi(x))) + 0x1000u;
-}
+__device__ __forceinline__ uint32_t tf32_lo(float x) { return __float_as_uint(x - __uint_as_float(tf32_hi(x))); }
 __device__ __forceinline__ void mma_step(float (&c)[4], const FragA<float>& a, const FragB<float>& b) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -158,13 +161,12 @@ template <int PHI> __device__ __forceinline__ float base_f(float x) {
     return x;
 }
 template <int PHI> __device__ __forceinline__ void base_frag(FragB<__nv_bfloat16>& b) {
-    if (PHI == PHI_IDENTITY) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (PHI == PHI_RELU1) {
+        if constexpr (PHI == PHI_RELU1) {
             const __nv_bfloat162 x = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&b.r[i]), __float2bfloat162_rn(0.f));
             b.r[i] = *reinterpret_cast<const uint32_t*>(&x);
-        } else {
+        } else if constexpr (PHI == PHI_ELU1) {
             b.r[i] = pack_bf16(base_f<PHI>(bf16_lo(b.r[i])), base_f<PHI>(bf16_hi(b.r[i])));
         }
     }

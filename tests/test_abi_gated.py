@@ -59,6 +59,8 @@ def test_gated_refusals(lib):
         assert call(lib, desc(), ws=None) == WORKSPACE
         assert call(lib, desc(), nbytes=256) == WORKSPACE
         assert call(lib, desc(), ws=BAD) == MISALIGNED
+    for call in (forward, backward):  # rows past 2^30 tokens
+        assert call(lib, desc(B_=1, H=1, N=(1 << 30) + 1, d=16)) == UNSUPPORTED
     for one in ("S_in", "z_in", "S_out", "z_out"):
         assert forward(lib, desc(), {one: P}) == INVALID
     assert forward(lib, desc(), {"S_in": P, "z_in": BAD}) == MISALIGNED
@@ -72,6 +74,7 @@ def test_gated_workspace_sizes(lib):
     size = lambda op, **k: B.la_workspace_size(desc(**k), op)  # noqa: E731
     assert size("gated_causal") % 256 == 0 and size("gated_causal") > 0
     assert size("gated_causal", N=1) > 256 and size("gated_causal", B_=64, H=32) > 256
+    assert size("gated_causal", B_=1, H=1, N=(1 << 30) + 1, d=16) == 0
     assert size("gated_causal", d=48) == 0 and size("gated_causal_bwd", N=0) == 0
     # the gradients keep a state per chunk of 64 tokens
     assert size("gated_causal_bwd") >= 2 * 3 * (-(-4000 // 64)) * (64 * 64 * 2 + 64 * 4)

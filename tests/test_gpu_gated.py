@@ -168,6 +168,58 @@ def test_slow_gate_behind_a_closed_one():
     assert float((a - b).abs().max()) <= 64 * 2.0 ** -23 * float(a.abs().max())
 
 
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 32)])
+def test_gates_that_amplify(dt, d):
+    """Positive log-gates, up to a growth of e^40 over the row."""
+    q, k, v, g = inputs(1, 2, 400, d, dt, "relu1", seed=16)
+    g = (-g * 0.8).to(g.dtype).clamp(max=0.25)
+    check_forward(q, k, v, g, dt, "relu1", True)
+    check_backward(q, k, v, g, dt, "relu1", True)
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_nan_gate_reaches_its_own_head_from_there_on(dt, d, bad):
+    q, k, v, g = inputs(1, 2, 500, d, dt, "relu1", seed=17)
+    ref, scale = G.heads(G.gated, f64(q), f64(k), f64(v), f64(g), phi_kind="relu1", normalize=True)
+    want = la.la_gated_causal(q, k, v, g)
+    g[0, 1, 333] = bad
+    got = la.la_gated_causal(q, k, v, g)
+    assert torch.equal(got[0, 0], want[0, 0])
+    # its chunk takes the decays per pair: other roundings, within the same bounds
+    close("out", got[0, 1, :333], ref[0][0, 1, :333], scale[0][0, 1, :333], roundings(dt, d, 500, "relu1", True)[0])
+    assert bool(got[0, 1, 333:].isnan().all())
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 16), ("f32", 64)])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_a_nan_in_q_k_or_v_is_not_lost(dt, d, normalize):
+    """NaN as the device makes it (all bits set), which must pass the products'
+    parts. Up to 63 tokens in front of it may share its tile, none before them."""
+    phi = "elu1" if normalize else "identity"
+    q, k, v, g = inputs(1, 2, 500, d, dt, phi, seed=18)
+    nan = torch.full((), 0x7FFFFFFF, dtype=torch.int32, device="cuda").view(torch.float32).to(q.dtype)
+    for i, x in enumerate((q, k, v)):
+        x = x.clone()
+        x[0, 1, 333, 5] = nan
+        qkv_ = [x if j == i else y for j, y in enumerate((q, k, v))]
+        out = la.la_gated_causal(*qkv_, g, phi=phi, normalize=normalize)[0]
+        assert not out[0].isnan().any() and not out[1, :270].isnan().any()
+        if i == 0:
+            assert bool(out[1, 333].isnan().all()) and not out[1, 397:].isnan().any()
+        elif i == 1:
+            assert bool(out[1, 333:].isnan().all())
+        else:
+            assert bool(out[1, 333:, 5].isnan().all())
+
+
+@pytest.mark.parametrize("phi,normalize", [("relu1", True), ("identity", False)])
+def test_gradients_at_d128_with_long_blocks(phi, normalize):
+    """40 heads of 900 tokens: blocks of 300, whose states go through the tensor
+    cores in both directions."""
+    check_backward(*inputs(2, 20, 900, 128, "bf16", phi, seed=18, docs=2), "bf16", phi, normalize)
+
+
 def test_many_heads_in_one_block_and_few_in_many():
     check_forward(*inputs(3, 160, 130, 16, "bf16", "relu1", seed=12), "bf16", "relu1", True)
     check_backward(*inputs(1, 1, 1500, 64, "bf16", "relu1", seed=13), "bf16", "relu1", True)

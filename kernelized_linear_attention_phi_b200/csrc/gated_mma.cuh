@@ -55,21 +55,29 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Nearest tf32 (the instruction drops the low 13 bits itself; half of their
-// range is added before). The rest has 12 bits at most and the instruction
-// keeps 11: the bit that it drops is half a step, so rounding it would gain
-// nothing, and the NaN that it is where x is a NaN stays one.
+// range is added before). The rest has 12 bits m at most, 2^11 <= m < 2^12, and
+// the instruction keeps 11: m + m / 2^11 lies in [m + 1, m + 2), so an odd m is
+// cut to m + 1 and an even one to m, which rounds it; where x is a NaN, both
+// parts together keep one (an integer addition would carry out of it).
 __device__ __forceinline__ uint32_t tf32_hi(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
-__device__ __forceinline__ uint32_t tf32_lo(float x) { return __float_as_uint(x - __uint_as_float(tf32_hi(x))); }
+__device__ __forceinline__ uint32_t tf32_lo(float x) {
+    return __float_as_uint((x - __uint_as_float(tf32_hi(x))) * (1.f + 1.f / 2048));
+}
+// The instruction's own additions cut off what falls below the sum: the steps'
+// sums are added here, rounded to nearest.
 __device__ __forceinline__ void mma_step(float (&c)[4], const FragA<float>& a, const FragB<float>& b) {
+    float s[4] = {};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const float* x = a.r + 4 * h;
         const uint32_t h0 = tf32_hi(x[0]), h1 = tf32_hi(x[2]), h2 = tf32_hi(x[1]), h3 = tf32_hi(x[3]);
         const uint32_t y0 = tf32_hi(b.r[2 * h]), y1 = tf32_hi(b.r[2 * h + 1]);
-        mma_tf32(c, tf32_lo(x[0]), tf32_lo(x[2]), tf32_lo(x[1]), tf32_lo(x[3]), y0, y1);
-        mma_tf32(c, h0, h1, h2, h3, tf32_lo(b.r[2 * h]), tf32_lo(b.r[2 * h + 1]));
-        mma_tf32(c, h0, h1, h2, h3, y0, y1);
+        mma_tf32(s, tf32_lo(x[0]), tf32_lo(x[2]), tf32_lo(x[1]), tf32_lo(x[3]), y0, y1);
+        mma_tf32(s, h0, h1, h2, h3, tf32_lo(b.r[2 * h]), tf32_lo(b.r[2 * h + 1]));
+        mma_tf32(s, h0, h1, h2, h3, y0, y1);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] += s[e];
 }
 
 // ---- lane values of A and B operands as floats, and back -----------------------

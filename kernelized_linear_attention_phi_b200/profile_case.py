@@ -5,7 +5,8 @@ command to put under a profiler (ncu) when studying a single kernel.
         --op noncausal --B 1 --H 16 --N 16384 --d 64 --iters 3
 
 ``--op`` is one of kv_summary, noncausal, causal, prefix, decode,
-noncausal_bwd, causal_bwd. Inputs come from the seeded generators in
+noncausal_bwd, causal_bwd, gated_causal, gated_causal_bwd, gated_decode,
+qk_norm_rope, qk_norm_rope_bwd. Inputs come from the seeded generators in
 ``workloads``; nothing is checked or timed.
 """
 
@@ -22,7 +23,9 @@ from . import workloads as W
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", required=True, choices=["kv_summary", "noncausal", "causal", "prefix", "decode",
-                                                      "noncausal_bwd", "causal_bwd"])
+                                                      "noncausal_bwd", "causal_bwd", "gated_causal",
+                                                      "gated_causal_bwd", "gated_decode", "qk_norm_rope",
+                                                      "qk_norm_rope_bwd"])
     ap.add_argument("--B", type=int, default=1)
     ap.add_argument("--H", type=int, default=16)
     ap.add_argument("--N", type=int, default=16384)
@@ -46,6 +49,35 @@ def main():
         q1, k1, v1 = (t[0].contiguous() for t in W.decode_tokens(1, a.B, a.H, a.d, sigma, 1, a.dtype, dev))
         out = torch.empty_like(q1)
         fn = lambda: la.la_decode_step(q1, k1, v1, S, z, out, a.phi, norm)
+    elif a.op.startswith("gated"):
+        n = 1 if a.op == "gated_decode" else a.N
+        q, k, v = (t[:, :, :n].contiguous() for t in (q, k, v))
+        # gates around 1 - 1 / 50
+        g = -torch.rand(a.B, a.H, n, generator=torch.Generator().manual_seed(1)).to(device=dev, dtype=q.dtype) / 25
+        out = torch.empty_like(q)
+        if a.op == "gated_decode":
+            S = torch.zeros(a.B, a.H, a.d, a.d, device=dev)
+            z = torch.zeros(a.B, a.H, a.d, device=dev)
+            fn = lambda: la.la_gated_decode_step(q, k, v, g, S, z, out=out, phi=a.phi, normalize=norm)
+        else:
+            ws = la.workspace(desc, a.op)
+            dout = W.upstream_grad(a.B, a.H, n, a.d, 1, a.dtype, dev)
+            grads = [torch.empty_like(t) for t in (q, k, v, g)]
+            fn = {
+                "gated_causal": lambda: la.la_gated_causal(q, k, v, g, out=out, phi=a.phi, normalize=norm, ws=ws),
+                "gated_causal_bwd": lambda: la.la_gated_causal_backward(q, k, v, g, dout, *grads, phi=a.phi,
+                                                                        normalize=norm, ws=ws),
+            }[a.op]
+    elif a.op.startswith("qk_norm_rope"):
+        x, y = (t.transpose(1, 2).contiguous() for t in (q, k))  # [B, N, H, d]
+        w = torch.ones(a.d, device=dev)
+        angle = torch.arange(a.N, device=dev)[:, None] * 10000.0 ** (-torch.arange(a.d // 2, device=dev) * 2 / a.d)
+        tables = angle.cos(), angle.sin()
+        if a.op == "qk_norm_rope":
+            q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+            fn = lambda: la.la_qk_norm_rope(x, y, w, w, *tables, q_out=q_out, k_out=k_out)
+        else:
+            fn = lambda: la.la_qk_norm_rope_backward(x, y, w, w, *tables, q, k)
     elif a.op.endswith("_bwd"):
         ws = la.workspace(desc, a.op, a.chunk, dev)
         dout = W.upstream_grad(a.B, a.H, a.N, a.d, 1, a.dtype, dev)

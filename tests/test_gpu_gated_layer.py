@@ -89,3 +89,10 @@ def test_gradients_of_the_chain(dt, d):
         assert (np.abs(f64(into[i]) - want) <= own * at_dy + at_err).all(), name
         n = B * N * H
         assert (np.abs(f64(dw) - want_w) <= (d + 16 + n ** 0.5 + 64) * 2.0 ** -23 * at_dy_w + at_err_w).all(), name
+
+
+@pytest.mark.parametrize("op", ["gated_causal", "gated_causal_bwd", "gated_decode", "qk_norm_rope", "qk_norm_rope_bwd"])
+def test_the_profiling_command_runs_them(op, monkeypatch):
+    from kernelized_linear_attention_phi_b200 import profile_case
+    monkeypatch.setattr("sys.argv", ["profile_case", "--op", op, "--H", "2", "--N", "200", "--iters", "1"])
+    profile_case.main()

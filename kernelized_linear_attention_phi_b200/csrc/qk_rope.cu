@@ -118,11 +118,21 @@ __global__ void __launch_bounds__(kForward) qk_rope_kernel(const __grid_constant
     const T* x = static_cast<const T*>(sd.x) + b * sd.xs.b + n * sd.xs.n + l * EPV;
     T* y = static_cast<T*>(sd.y) + (b * sd.H * p.N + n) * D + l * EPV;
     pdl_wait();
-    float w[EPV];
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) w[e] = sd.w ? sd.w[l * EPV + e] : 1.f;
+    // y = r (x c w + x' s w'), x' and w' the pair's other channel: the weights are
+    // taken into the cosines and sines once per token, and a row's lanes exchange
+    // x as it was loaded
     TU turn;
     turn.load(p, token, l);
+    if (sd.w) {
+        const int from = (l + turn.partner - (int)threadIdx.x % 32) * EPV;
+        float w[EPV];
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) w[e] = sd.w[from + (PAIRS ? e ^ 1 : e)];
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) turn.s[e] *= w[e];
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) turn.c[e] *= sd.w[l * EPV + e];
+    }
     for (int h = h0; h < h1; h += kInFlight) {
         uint4 raw[kInFlight];
 #pragma unroll
@@ -131,18 +141,25 @@ __global__ void __launch_bounds__(kForward) qk_rope_kernel(const __grid_constant
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
             if (h + u >= h1) break;
-            float f[EPV], ss = 0.f;
+            float f[EPV], o[EPV], ss = 0.f;
             Vec16<T>::unpack(raw[u], f);
 #pragma unroll
             for (int e = 0; e < EPV; ++e) ss = fmaf(f[e], f[e], ss);
-            const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+            float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+            if (turn.bad) r = NAN;
+            if constexpr (PAIRS) {
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) f[e] = f[e] * r * w[e];
-            turn.template apply<false>(f);
-            if (turn.bad) {
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) f[e] = NAN;
+                for (int e = 0; e < EPV; ++e) o[e] = f[e ^ 1];
+            } else {
+                uint4 other;
+                other.x = __shfl_sync(0xffffffffu, raw[u].x, turn.partner);
+                other.y = __shfl_sync(0xffffffffu, raw[u].y, turn.partner);
+                other.z = __shfl_sync(0xffffffffu, raw[u].z, turn.partner);
+                other.w = __shfl_sync(0xffffffffu, raw[u].w, turn.partner);
+                Vec16<T>::unpack(other, o);
             }
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) f[e] = r * fmaf(f[e], turn.c[e], o[e] * turn.s[e]);
             if (in) *reinterpret_cast<uint4*>(y + (long long)(h + u) * p.N * D) = Vec16<T>::pack(f);
         }
     }

@@ -9,7 +9,9 @@
 namespace la {
 namespace {
 
-// The gates of every chunk of C tokens, as the sweeps take them (a warp per chunk).
+// The gates of every chunk of C tokens, as the sweeps take them (a warp per
+// chunk): once per call, so that no sweep waits for a scan between two chunks.
+// Little more than its launch (7 us for 16 rows of 4096, 11 for 64 of 8192).
 template <typename T, int C>
 __global__ void __launch_bounds__(128) gates_kernel(const T* __restrict__ gate, int N, int nch, uint8_t* __restrict__ out) {
     using namespace gated;
@@ -58,7 +60,8 @@ cudaError_t launch_gates(const Problem& p, const void* g, uint8_t* out, cudaStre
 
 // Record blk of each head becomes the state in front of the block (REVERSE:
 // behind it), from S_in / z_in or zero; the state past the other end goes to
-// S_out / z_out. One thread per entry of the state; S_out may be S_in.
+// S_out / z_out. One thread per entry of the state, its records' loads in flight
+// together; S_out may be S_in. Bound by launch and two round trips: 8 - 14 us.
 template <bool REVERSE>
 __global__ void __launch_bounds__(256)
 gated_scan_kernel(float* __restrict__ rec, const float* __restrict__ dec, int nblk, int dd, int sf, const float* S_in,
@@ -100,6 +103,7 @@ gated_scan_kernel(float* __restrict__ rec, const float* __restrict__ dec, int nb
 // d x d state through registers once (bandwidth bound: 2 d (d + 1) fp32 moved
 // per head and step, nothing else of note). The state's loads are issued
 // before the token's rows are needed, so one round trip covers both.
+// 64x32 heads of 128: 43.4 us for 273 MB, 6.3 TB/s, 96 % of a copy's rate.
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ float4 ld_cs(const float4* p) {

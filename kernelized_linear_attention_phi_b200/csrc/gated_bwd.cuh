@@ -124,6 +124,11 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16(a, b);
 }
 
+// First sweep. 4x16x8192x64 bf16: 209 us for 201 MB of rows and 71 MB of chunk
+// states (1.3 TB/s), fp32 650 us; 1x16x32768x128 bf16, identity: 422 us, 8 us for
+// a chunk of 64 tokens. A chunk's products follow from one another over four
+// barriers, and registers and shared memory leave an SM 8 warps at d = 128 (12 at 64)
+// to cover for it: shared memory 60 % busy, the tensor pipe 32 %, issue 25 %.
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
@@ -416,6 +421,8 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     finish(nch - 1);
 }
 
+// Second sweep, bound like the first. 4x16x8192x64 bf16: 223 us, fp32 745 us;
+// 1x16x32768x128 bf16, identity: 547 us (shared memory 65 % busy, the tensor pipe 29 %).
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,

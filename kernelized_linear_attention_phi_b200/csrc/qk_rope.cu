@@ -12,7 +12,10 @@
 // written), 16 bytes per lane, d / 8 (bf16) or d / 4 (fp32) lanes per row. The
 // lanes of a token keep its cosines and sines in registers and run over
 // several heads, so the tables (fp32, as wide as the rows) are read once per
-// head group and not once per row.
+// head group and not once per row. Forward, 4x16384x(16+16)x64 bf16: 92 us for
+// 541 MB, 90 % of a copy's rate. Backward, 3x1777x(12+4)x128 fp32: 35 us for
+// 132 MB (57 %); 2x4096x(8+8)x64 bf16: 25 us for 51 MB, of which some 6 are
+// the launch; registers (two rows and the sums of dw) hold it to 5 CTAs an SM.
 
 #include "common.cuh"
 #include "device.h"
@@ -23,7 +26,7 @@ namespace la {
 namespace {
 
 // Forward, small CTAs: tokens of many places in flight (4x16384x(16+16)x64 bf16:
-// 104 us with 256 threads, 95 with 128). Backward, larger ones: fewer rows of
+// 104 us with 256 threads, 95 with 128; 105 with 8 rows in flight, for 97). Backward, larger ones: fewer rows of
 // partial weight gradients.
 constexpr int kForward = 128, kThreads = 256;
 constexpr int kInFlight = 4;  // rows a lane loads before it uses the first
@@ -87,13 +90,20 @@ template <typename T, int D, bool PAIRS> struct Turn {
             }
         }
     }
-    // f <- R f, or R^T f (the angle's sign changes). Every lane of the warp calls it.
-    template <bool BACK> __device__ __forceinline__ void apply(float (&f)[EPV]) const {
-        float o[EPV];
+    // The pairs' other channels of a row as it was loaded (x its own, unpacked).
+    // Every lane of the warp calls it.
+    __device__ __forceinline__ void others(const uint4& raw, const float (&x)[EPV], float (&o)[EPV]) const {
+        if constexpr (PAIRS) {
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) o[e] = PAIRS ? f[e ^ 1] : __shfl_sync(0xffffffffu, f[e], partner);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) f[e] = f[e] * c[e] + o[e] * (BACK ? -s[e] : s[e]);
+            for (int e = 0; e < EPV; ++e) o[e] = x[e ^ 1];
+        } else {
+            uint4 u;
+            u.x = __shfl_sync(0xffffffffu, raw.x, partner);
+            u.y = __shfl_sync(0xffffffffu, raw.y, partner);
+            u.z = __shfl_sync(0xffffffffu, raw.z, partner);
+            u.w = __shfl_sync(0xffffffffu, raw.w, partner);
+            Vec16<T>::unpack(u, o);
+        }
     }
 };
 
@@ -147,17 +157,7 @@ __global__ void __launch_bounds__(kForward) qk_rope_kernel(const __grid_constant
             for (int e = 0; e < EPV; ++e) ss = fmaf(f[e], f[e], ss);
             float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
             if (turn.bad) r = NAN;
-            if constexpr (PAIRS) {
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) o[e] = f[e ^ 1];
-            } else {
-                uint4 other;
-                other.x = __shfl_sync(0xffffffffu, raw[u].x, turn.partner);
-                other.y = __shfl_sync(0xffffffffu, raw[u].y, turn.partner);
-                other.z = __shfl_sync(0xffffffffu, raw[u].z, turn.partner);
-                other.w = __shfl_sync(0xffffffffu, raw[u].w, turn.partner);
-                Vec16<T>::unpack(other, o);
-            }
+            turn.others(raw[u], f, o);
 #pragma unroll
             for (int e = 0; e < EPV; ++e) f[e] = r * fmaf(f[e], turn.c[e], o[e] * turn.s[e]);
             if (in) *reinterpret_cast<uint4*>(y + (long long)(h + u) * p.N * D) = Vec16<T>::pack(f);
@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_cons
     using TU = Turn<T, D, PAIRS>;
     constexpr int EPV = TU::EPV, LPR = TU::LPR, RPB = kThreads / LPR;
     // one row each of x and dy: more only costs registers and with them warps
-    // (3x1777x(12+4)x128 fp32: 42 us with two rows, 36 with one)
+    // (3x1777x(12+4)x128 fp32: 42 us with two rows, 36 with one; 2x4096x(8+8)x64
+    // bf16: 31 and 25)
     constexpr int U = 1;
     __shared__ float red[RPB][D];
     const int l = threadIdx.x % LPR;
@@ -205,19 +206,17 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_cons
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (h + u >= h1) break;
-                float f[EPV], g[EPV], ss = 0.f, m = 0.f;
+                float f[EPV], g[EPV], o[EPV], ss = 0.f, m = 0.f;
                 Vec16<T>::unpack(rx[u], f);
                 Vec16<T>::unpack(ry[u], g);
 #pragma unroll
                 for (int e = 0; e < EPV; ++e) ss = fmaf(f[e], f[e], ss);
-                const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-                turn.template apply<true>(g);
-                if (turn.bad) {
+                float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+                if (turn.bad) r = NAN;
+                turn.others(ry[u], g, o);
 #pragma unroll
-                    for (int e = 0; e < EPV; ++e) g[e] = NAN;
-                }
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) {
+                for (int e = 0; e < EPV; ++e) {  // g: v, R turned back
+                    g[e] = fmaf(g[e], turn.c[e], o[e] * -turn.s[e]);
                     f[e] *= r;
                     if (in) dw[e] = fmaf(g[e], f[e], dw[e]);
                     g[e] *= w[e];

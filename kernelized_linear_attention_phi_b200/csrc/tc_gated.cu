@@ -278,8 +278,8 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
 // "state" (phi on Q; S^T: the bf16 operand, and its decay in place), warps 14..17 "mask"
 // (P~, denominators), warps 18..21 "out" (O^T to the outputs). The transforms run a chunk ahead: the loop
 // from one S^T update to the next holds only the state warps' pass over S^T
-// and that update's products. 1x16x131072x128, identity: 451 us for 2147 MB, 4.8
-// TB/s, 73 % of a copy's rate; the rest is that loop, about 3,800 cycles a chunk.
+// and that update's products. 1x16x131072x128, relu + 1: 445 us for 2147 MB, 4.8
+// TB/s, 73 % of a copy's rate; the rest is that loop, about 3,750 cycles a chunk.
 struct GtCfg {
     static constexpr int D = 128, C = 64, NB = 2;
     static constexpr int BOX = C * 128;            // one 64-row x 64-column box (8 KB)

@@ -84,6 +84,13 @@ template <typename T, int D> struct ChunkState {
         float* z = reinterpret_cast<float*>(rec + (size_t)D * D * sizeof(T));
         for (int a = threadIdx.x; a < D; a += SH::THREADS) z[a] = zs[a];
     }
+    // Asks for the next chunk's record (d = 128, where no other CTA covers for the
+    // wait: 1x16x32768x128 547 -> 537 us; nothing gained at d = 64, fp32 loses 2 of 20).
+    __device__ __forceinline__ static void ahead(const uint8_t* rec) {
+        if constexpr (D == 128) {
+            for (int a = threadIdx.x * 128; a < (int)BYTES; a += SH::THREADS * 128) prefetch_l2(rec + a);
+        }
+    }
     // this thread's part of <S, G> + <z, h>
     __device__ __forceinline__ static float product(const uint8_t* rec, const State<T, D>& st, const float* zs) {
         float sum = 0.f;
@@ -422,7 +429,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 }
 
 // Second sweep, bound like the first. 4x16x8192x64 bf16: 223 us, fp32 745 us;
-// 1x16x32768x128 bf16, identity: 547 us (shared memory 65 % busy, the tensor pipe 29 %).
+// 1x16x32768x128 bf16, identity: 537 us (shared memory 65 % busy, the tensor pipe 29 %).
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
@@ -515,6 +522,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         cp_async_wait<0>();
         __syncthreads();
         if (SH::ST == 2 && s + 1 < nch) fetch(s + 1);
+        if (s + 1 < nch) ChunkState<T, D>::ahead(states + (size_t)(c - 1) * ChunkState<T, D>::BYTES);
         if (s > 0) finish(s - 1);
         const T *qt = sm.tiles[s % SH::ST][0], *kt = sm.tiles[s % SH::ST][1], *vt = sm.tiles[s % SH::ST][2], *gt = sm.tiles[s % SH::ST][3];
         const Gates<C>& gs = sm.gates[s & 1];

@@ -85,7 +85,7 @@ template <typename T, int D> struct ChunkState {
         for (int a = threadIdx.x; a < D; a += SH::THREADS) z[a] = zs[a];
     }
     // Asks for the next chunk's record (d = 128, where no other CTA covers for the
-    // wait: 1x16x32768x128 547 -> 537 us; nothing gained at d = 64, fp32 loses 2 of 20).
+    // wait: 2 % of the sweep; nothing gained at d = 64, fp32 loses 2 of 20).
     __device__ __forceinline__ static void ahead(const uint8_t* rec) {
         if constexpr (D == 128) {
             for (int a = threadIdx.x * 128; a < (int)BYTES; a += SH::THREADS * 128) prefetch_l2(rec + a);
@@ -132,8 +132,8 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
 }
 
 // First sweep. 4x16x8192x64 bf16: 209 us for 201 MB of rows and 71 MB of chunk
-// states (1.3 TB/s), fp32 650 us; 1x16x32768x128 bf16, identity: 422 us, 8 us for
-// a chunk of 64 tokens. A chunk's products follow from one another over four
+// states (1.3 TB/s), fp32 650 us; 1x16x32768x128 bf16, identity: 390 us, 7.5 us
+// for a chunk of 64 tokens. A chunk's products follow from one another over four
 // barriers, and registers and shared memory leave an SM 8 warps at d = 128 (12 at 64)
 // to cover for it: shared memory 60 % busy, the tensor pipe 32 %, issue 25 %.
 template <typename T, int D, int PHI>
@@ -173,12 +173,12 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     const float* rec = prefix ? prefix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
     st.seed(rec, rec + D * D, warp, lane);
     st.template publish<LO>(sm.sop[0][0], sm.zs[0], warp, lane, sm.sop[0][BQ::PARTS - 1]);
-    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
+    const int rg = row_group<SH>(warp), cg = warp / SH::RG;
     const int i0 = rg * 16, col0 = cg * SH::NCOL;
 
     // dgp of chunk c from the sums its warps left: a suffix sum over the chunk
     auto finish = [&](int c) {
-        if (warp != SH::NW - 1) return;
+        if (rg != 0 || cg != 0) return;  // a warp with one key group
         constexpr int R = C / 32;
         float x[R], run = 0.f;
 #pragma unroll
@@ -428,8 +428,8 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     finish(nch - 1);
 }
 
-// Second sweep, bound like the first. 4x16x8192x64 bf16: 223 us, fp32 745 us;
-// 1x16x32768x128 bf16, identity: 537 us (shared memory 65 % busy, the tensor pipe 29 %).
+// Second sweep, bound like the first. 4x16x8192x64 bf16: 219 us, fp32 745 us;
+// 1x16x32768x128 bf16, identity: 488 us (shared memory 65 % busy, the tensor pipe 29 %).
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
@@ -473,12 +473,13 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     const float* rec = suffix ? suffix + ((size_t)bh * nblk + blk) * (size_t)(D * D + D) : nullptr;
     st.seed(rec, rec + D * D, warp, lane);
     st.publish(sm.sop[0][0], sm.zs[0], warp, lane);
-    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
+    const int rg = row_group<SH>(warp), cg = warp / SH::RG;
     const int j0 = rg * 16, col0 = cg * SH::NCOL;
 
     // dg of step s: what the first sweep left, the keys in front and the outside
     auto finish = [&](int s) {
-        if (warp != SH::NW - 1) return;
+        // a warp with one query group (not a fixed one: 4x16x8192x128 622 us -> 597)
+        if (rg != SH::RG - 1 || cg != 0) return;
         constexpr int R = C / 32;
         const int row0 = first + (nch - 1 - s) * C;
         float outside = 0.f;

@@ -72,7 +72,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     st.publish(sm.sop[0], sm.zs[0], warp, lane);
     // the warps' row groups differ in work (a group sees the keys before it):
     // CTAs of an SM start them at different warps
-    const int rg = (warp + blockIdx.x + blockIdx.y) % SH::RG, cg = warp / SH::RG;
+    const int rg = row_group<SH>(warp), cg = warp / SH::RG;
     const int i0 = rg * 16, col0 = cg * SH::NCOL;
 
 #pragma unroll 1

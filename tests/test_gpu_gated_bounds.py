@@ -1,0 +1,62 @@
+"""Gated linear attention on the GPU under norm-wise bounds (gated_bounds.py):
+where results would be lost although every entry stays within an entry-wise
+bound, and inputs and gates at the ends of the range."""
+
+import pytest
+import torch
+
+import gated_bounds as GB
+from kernelized_linear_attention_phi_b200 import binding as la
+
+from gpu_util import DT, qkv
+
+pytestmark = pytest.mark.gpu
+
+MODES = [("relu1", True), ("relu1", False), ("identity", False), ("elu1", True)]
+KINDS = [("bf16", 16), ("bf16", 32), ("bf16", 64), ("bf16", 128), ("f32", 16), ("f32", 64), ("f32", 128)]
+
+
+def inputs(B, H, N, d, dt, phi, seed, span=30.0, sigma=1.0):
+    q, k, v = qkv(B, H, N, d, dt, seed=seed, sigma=sigma * (d ** -0.5 if phi == "identity" else 1.0))
+    gen = torch.Generator().manual_seed(seed + 77)
+    g = (-torch.exp(torch.randn(B, H, N, generator=gen)) / span).to(device="cuda", dtype=DT[dt])
+    dout = torch.randn(B, H, N, d, generator=gen).to(device="cuda", dtype=DT[dt])
+    return q, k, v, g, dout
+
+
+def rate(dt, d, lowest):
+    """A gate that takes every chunk's sum (of 32 tokens in fp32 with d >= 64, else 64) to 2^lowest."""
+    return lowest / 1.4427 / (32 if dt == "f32" and d >= 64 else 64)
+
+
+def check_out(dt, q, k, v, g, phi, normalize, window=64, **state):
+    kw = {n: s.double() for n, s in zip(("S0", "z0"), state.values())}
+    ref, like = GB.allowances(dt, *(x.double() for x in (q, k, v, g)), kind=phi, normalize=normalize, **kw)
+    out = la.la_gated_causal(q, k, v, g, phi=phi, normalize=normalize, **state)
+    x = GB.excess(out.double(), ref, like, 2, window)
+    assert x <= 1, x
+    return out
+
+
+def check_gradients(dt, q, k, v, g, dout, phi, normalize, window=128):
+    ref, like = GB.allowances(dt, *(x.double() for x in (q, k, v, g, dout)), kind=phi, normalize=normalize)
+    got = la.la_gated_causal_backward(q, k, v, g, dout, phi=phi, normalize=normalize)
+    x = [GB.excess(a.double(), r, l, 3 if i == 3 else 2, g.shape[2] if i == 3 else window)
+         for i, (a, r, l) in enumerate(zip(got, ref, like))]
+    assert max(x) <= 1, x
+    return got
+
+
+@pytest.mark.parametrize("dt,d", KINDS)
+@pytest.mark.parametrize("phi,normalize", MODES)
+def test_norms(dt, d, phi, normalize):
+    q, k, v, g, dout = inputs(1, 2, 900, d, dt, phi, seed=d)
+    check_out(dt, q, k, v, g, phi, normalize)
+    check_gradients(dt, q, k, v, g, dout, phi, normalize)
+
+
+@pytest.mark.parametrize("phi,normalize", MODES)
+def test_norms_of_long_blocks_at_d128(phi, normalize):
+    """40 heads of 900 tokens: the gradients' block states on the tensor cores, in both directions."""
+    q, k, v, g, dout = inputs(2, 20, 900, 128, "bf16", phi, seed=4)
+    check_gradients("bf16", q, k, v, g, dout, phi, normalize)

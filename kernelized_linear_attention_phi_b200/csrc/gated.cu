@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(128) gates_kernel(const T* __restrict__ gate, 
         const float nan = q.bad & (1 << e) ? NAN : 0.f;
         const float2 b = gate_float2(q.b[e]);
         const bool in = c * C + i < N;
-        low = low || b.x < kDeep;
+        low = low || !(fabsf(b.x) <= kDeep);
         s.hi[i] = b.x + nan;
         s.lo[i] = b.y;
         s.from_start[i] = in ? gate_pow2(q.b[e]) + nan : 0.f;
@@ -241,24 +241,23 @@ cudaError_t gated_sweep(const Problem& p, const void* q, const void* k, const vo
     auto* f = p.dtype == DT_F32 ? gated_sweep_t<float> : gated_sweep_t<__nv_bfloat16>;
     return f(p, q, k, v, gates, prefix, S_in, z_in, block_tokens, nblk, out, S_out, z_out, st);
 }
-cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* wq,
-                         const float* up,
+cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* up,
                          const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                          cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_states_t<float> : gated_states_t<__nv_bfloat16>;
-    return f(p, reverse, x, y, gates, wq, up, col, block_tokens, nblk, blk0, count, exact, rec, dec, st);
+    return f(p, reverse, x, y, gates, up, col, block_tokens, nblk, blk0, count, exact, rec, dec, st);
 }
 cudaError_t gated_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                        const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,
+                        const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
                         void* chunk_state, cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_bwd_q_t<float> : gated_bwd_q_t<__nv_bfloat16>;
-    return f(p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, wq, up, col, dgp, chunk_state, st);
+    return f(p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, up, col, dgp, chunk_state, st);
 }
 cudaError_t gated_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates, const void* dout,
-                         const float* suffix, int block_tokens, int nblk, const float* wq, const float* up, const float* col,
+                         const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
                          const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_bwd_kv_t<float> : gated_bwd_kv_t<__nv_bfloat16>;
-    return f(p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, wq, up, col, dgp, chunk_state, dk, dv, dg, st);
+    return f(p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, up, col, dgp, chunk_state, dk, dv, dg, st);
 }
 
 }  // namespace la

@@ -23,12 +23,11 @@ cudaError_t gated_sweep(const Problem& p, const void* q, const void* k, const vo
                         const float* S_in, const float* z_in, int block_tokens, int nblk, void* out, float* S_out,
                         float* z_out, cudaStream_t st);
 // Own states of `count` blocks from blk0 on: records rec[bh*nblk + blk] and the
-// products of the blocks' gates dec[bh*nblk + blk]. Forward: x = k, y = v, wq,
-// up and col null. Reverse (gradients): x = q, y = dout; wq, up, col as the
-// first sweep left them, null when not normalized. exact: the terms of the
+// products of the blocks' gates dec[bh*nblk + blk]. Forward: x = k, y = v, up,
+// col null. Reverse (gradients): x = q, y = dout; up, col as the first sweep
+// left them, null when not normalized. exact: the terms of the
 // states keep all their bits (bf16), for a state that goes to the caller.
-cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* wq,
-                         const float* up,
+cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* up,
                          const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                          cudaStream_t st);
 // In place: record blk becomes the state in front of block blk (reverse:
@@ -54,16 +53,15 @@ cudaError_t gated_decode(const Problem& p, const void* q, const void* k, const v
                          const float* z, float* S_out, float* z_out, void* out, cudaStream_t st);
 
 // Gradients, first sweep (chunks in order): dq, and per token (normalized only)
-// up = 1 / den, wq = e^(sum of the chunk's gates up to it) / den and
-// col = -(out . dout); dgp (what the chunk's queries give to
+// up = 1 / den and col = -(out . dout); dgp (what the chunk's queries give to
 // dg), and per chunk of gated_chunk(p) tokens the state in front of it
 // (chunk_state, gated_chunk_state_bytes(p) each).
 cudaError_t gated_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                        const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,
+                        const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
                         void* chunk_state, cudaStream_t st);
 // Second sweep (chunks in reverse): dk, dv, dg from the states behind the blocks.
 cudaError_t gated_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates, const void* dout,
-                         const float* suffix, int block_tokens, int nblk, const float* wq, const float* up, const float* col,
+                         const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
                          const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st);
 int gated_chunk(const Problem& p);
 size_t gated_chunk_state_bytes(const Problem& p);
@@ -74,17 +72,16 @@ cudaError_t gated_sweep_t(const Problem& p, const void* q, const void* k, const 
                           const float* S_in, const float* z_in, int block_tokens, int nblk, void* out, float* S_out,
                           float* z_out, cudaStream_t st);
 template <typename T>
-cudaError_t gated_states_t(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* wq,
-                         const float* up,
+cudaError_t gated_states_t(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates, const float* up,
                            const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                            cudaStream_t st);
 template <typename T>
 cudaError_t gated_bwd_q_t(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                          const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,
+                          const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
                           void* chunk_state, cudaStream_t st);
 template <typename T>
 cudaError_t gated_bwd_kv_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates, const void* dout,
-                           const float* suffix, int block_tokens, int nblk, const float* wq, const float* up, const float* col,
+                           const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
                            const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st);
 
 namespace gated {

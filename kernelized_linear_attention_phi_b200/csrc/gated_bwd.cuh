@@ -18,9 +18,8 @@
 // each chunk is written out for the last term, and the sums over j and the
 // queries' part go to dgp), then chunks in reverse for dk, dv, dg (G in
 // registers). delta_i comes out of the same pass over the keys as dq, since
-//   dq_i = phi'(q_i) up_i e^{b_i} [ X_i + S dout_i - delta_i (Y_i + z) ],
-//   X_i = sum_j e^{-b_j} (dout_i.v_j) phi(k_j),  Y_i = sum_j e^{-b_j} phi(k_j).
-// The decay's two factors are taken apart as in the forward pass (Gates).
+//   dq_i = phi'(q_i) up_i [ X_i + e^{b_i} S dout_i - delta_i (Y_i + e^{b_i} z) ],
+//   X_i = sum_j e^{b_i - b_j} (dout_i.v_j) phi(k_j),  Y_i = sum_j e^{b_i - b_j} phi(k_j).
 #pragma once
 
 #include "gated.h"
@@ -140,7 +139,7 @@ template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                    const uint8_t* __restrict__ gates, const T* __restrict__ dout, const float* prefix, int N, int block_tokens, int nblk, int normalize,
-                   T* __restrict__ dq, float* __restrict__ wq, float* __restrict__ up, float* __restrict__ col, float* __restrict__ dgp,
+                   T* __restrict__ dq, float* __restrict__ up, float* __restrict__ col, float* __restrict__ dgp,
                    uint8_t* __restrict__ chunk_state) {
     using SH = Shape<T, D>;
     using BQ = BwdQ<T, D, PHI>;
@@ -161,7 +160,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 
     auto fetch = [&](int c) {
         const int row0 = first + c * C;
-        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, nullptr, row0, N);
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][2], v, row0, N);
@@ -266,21 +265,15 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             }
         }
         const bool deep = gs.deep;
-        float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
+        const float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
         const float hi0 = gs.hi[i0 + g], lo0 = gs.lo[i0 + g], hi1 = gs.hi[i0 + g + 8], lo1 = gs.lo[i0 + g + 8];
         // per row, over all keys so far: den = q . z and so on, num = sum of weights times dout . v
-        float qz0 = t == 0 ? oz[0] + oz[1] : 0.f, qz1 = t == 0 ? oz[2] + oz[3] : 0.f;
-        float zf0 = 1.f, zf1 = 1.f;  // the state's factor next to the chunk's own keys
-        if (deep) {
+        float den0 = t == 0 ? f0 * (oz[0] + oz[1]) : 0.f, den1 = t == 0 ? f1 * (oz[2] + oz[3]) : 0.f;
+        float num0 = 0.f, num1 = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                acc[n][0] *= f0; acc[n][1] *= f0; acc[n][2] *= f1; acc[n][3] *= f1;
-            }
-            zf0 = f0;
-            zf1 = f1;
-            f0 = f1 = 1.f;
+        for (int n = 0; n < NT; ++n) {
+            acc[n][0] *= f0; acc[n][1] *= f0; acc[n][2] *= f1; acc[n][3] *= f1;
         }
-        float den0 = qz0 * zf0, den1 = qz1 * zf1, num0 = 0.f, num1 = 0.f;
         float xs0 = 0.f, xs1 = 0.f, ys0 = 0.f, ys1 = 0.f;  // row sums of the operands below, for the shift of phi(k)
         float yk[NT][4] = {};
 #pragma unroll 1
@@ -306,15 +299,15 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int jl = n * 8 + 2 * t, j = jt * 16 + jl;
-                const float2 x = *reinterpret_cast<const float2*>(gs.inv + j);
-                w[n][0] = w[n][2] = x.x;
-                w[n][1] = w[n][3] = x.y;
                 if (deep) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         w[n][e] = decay(gs, hi0, lo0, j + e);
                         w[n][2 + e] = decay(gs, hi1, lo1, j + e);
                     }
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(gs.inv + j);
+                    w[n][0] = f0 * x.x; w[n][1] = f0 * x.y; w[n][2] = f1 * x.x; w[n][3] = f1 * x.y;
                 }
                 if (jt == rg) {
 #pragma unroll
@@ -368,9 +361,9 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         den0 = quad_sum(den0);
         den1 = quad_sum(den1);
         // the state's part of num: q . (S dout)
-        num0 = quad_sum(num0) + s0 * zf0;
-        num1 = quad_sum(num1) + s1 * zf1;
-        float up0 = f0, up1 = f1, de0 = 0.f, de1 = 0.f;  // up: e^{b_i} / den_i over the same factor
+        num0 = quad_sum(num0) + s0 * f0;
+        num1 = quad_sum(num1) + s1 * f1;
+        float up0 = 1.f, up1 = 1.f, de0 = 0.f, de1 = 0.f;
         const int row = first + c * C + i0 + g;
         if (normalize) {
             up0 = 1.f / den0;
@@ -378,14 +371,12 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             de0 = num0 * up0;  // out . dout
             de1 = num1 * up1;
             if (cg == 0 && t == 0) {
-                if (row < end) {  // e^{b_i} / den_i is what the second sweep takes; the bare 1 / den_i serves a deep chunk
-                    wq[toff + row] = deep ? up0 * zf0 : up0;
-                    up[toff + row] = up0 / f0;
+                if (row < end) {
+                    up[toff + row] = up0;
                     col[toff + row] = -de0;
                 }
                 if (row + 8 < end) {
-                    wq[toff + row + 8] = deep ? up1 * zf1 : up1;
-                    up[toff + row + 8] = up1 / f1;
+                    up[toff + row + 8] = up1;
                     col[toff + row + 8] = -de1;
                 }
             }
@@ -398,7 +389,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         }
         xs0 = shifted<PHI> ? quad_sum(xs0) - de0 * quad_sum(ys0) : 0.f;
         xs1 = shifted<PHI> ? quad_sum(xs1) - de1 * quad_sum(ys1) : 0.f;
-        const float dz0 = de0 * zf0, dz1 = de1 * zf1;
+        const float dz0 = de0 * f0, dz1 = de1 * f1;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float x, y;
@@ -417,7 +408,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             }
         }
         if (c + 1 < nch) {
-            st.template update<PHI>(kt, vt, gs.to_end, nullptr, true, gs.all, warp, lane);
+            st.template update<PHI>(kt, vt, gs.to_end, nullptr, nullptr, true, gs.all, warp, lane);
             if (BQ::COPIES == 1) __syncthreads();  // every warp has read the operand and the tiles
             if (SH::ST == 1) fetch(c + 1);
             const int nb = BQ::COPIES == 2 ? ((c + 1) & 1) : 0;
@@ -434,7 +425,7 @@ template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
                     const uint8_t* __restrict__ gates, const T* __restrict__ dout, const float* suffix, int N, int block_tokens, int nblk,
-                    const float* wq, const float* up, const float* col, const float* __restrict__ dgp,
+                    const float* up, const float* col, const float* __restrict__ dgp,
                     const uint8_t* __restrict__ chunk_state, T* __restrict__ dk, T* __restrict__ dv, T* __restrict__ dg) {
     using SH = Shape<T, D>;
     constexpr int C = SH::C, LD = SH::LD, NT = SH::NCOL / 8;
@@ -450,8 +441,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     gates += ((size_t)bh * ((N + C - 1) / C) + first / C) * kGateBytes<C>;
     dgp += toff;
     dg += toff;
-    if (wq) {
-        wq += toff;
+    if (up) {
         up += toff;
         col += toff;
     }
@@ -461,7 +451,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     // step s of the sweep is chunk nch - 1 - s
     auto fetch = [&](int s) {
         const int row0 = first + (nch - 1 - s) * C;
-        load_gates<C>(sm.gates[s & 1], gates + (size_t)(nch - 1 - s) * kGateBytes<C>, wq, up, col, row0, N);
+        load_gates<C>(sm.gates[s & 1], gates + (size_t)(nch - 1 - s) * kGateBytes<C>, up, col, row0, N);
         load_tile<SH, T, D>(sm.tiles[s % SH::ST][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[s % SH::ST][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[s % SH::ST][2], v, row0, N);
@@ -559,10 +549,8 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             }
         }
         const bool deep = gs.deep;
-        // before the rows' own factors r (2^-b_j; deep: none, and the state's
-        // part takes the whole of its decay)
-        const float e0 = deep ? gs.to_end[j0 + g] : gs.all, e1 = deep ? gs.to_end[j0 + g + 8] : gs.all;
-        const float r0 = deep ? 1.f : gs.inv[j0 + g], r1 = deep ? 1.f : gs.inv[j0 + g + 8];
+        const float e0 = gs.to_end[j0 + g], e1 = gs.to_end[j0 + g + 8];
+        const float inv0 = gs.inv[j0 + g], inv1 = gs.inv[j0 + g + 8];
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -579,8 +567,8 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             load_pair(p + 8 * LD, x, y);
             s1 += phi_f<PHI>(x) * ak[n][2] + phi_f<PHI>(y) * ak[n][3];
         }
-        s0 = quad_sum(s0) * r0;
-        s1 = quad_sum(s1) * r1;
+        s0 = quad_sum(s0);
+        s1 = quad_sum(s1);
         const int row = first + c * C + j0 + g;
         if (t == 0) {  // a key past the last token holds nothing
             sm.row[s & 1][cg][j0 + g] = row < end ? s0 : 0.f;
@@ -612,17 +600,22 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int il = n * 8 + 2 * t, i = it * 16 + il;
-                const float2 u = *reinterpret_cast<const float2*>(gs.from_start + i);  // with 1 / den_i in it
                 float2 cl = make_float2(0.f, 0.f);
-                if (wq) cl = *reinterpret_cast<const float2*>(gs.col + i);
-                float w[4] = {u.x, u.y, u.x, u.y};
+                float w[4];
                 if (deep) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float q = wq ? gs.up[i + e] : 1.f;
-                        w[e] = q * exp2_fast((gs.hi[i + e] - hi0) + (gs.lo[i + e] - lo0));
-                        w[2 + e] = q * exp2_fast((gs.hi[i + e] - hi1) + (gs.lo[i + e] - lo1));
+                        w[e] = exp2_fast((gs.hi[i + e] - hi0) + (gs.lo[i + e] - lo0));
+                        w[2 + e] = exp2_fast((gs.hi[i + e] - hi1) + (gs.lo[i + e] - lo1));
                     }
+                } else {
+                    const float2 f = *reinterpret_cast<const float2*>(gs.from_start + i);
+                    w[0] = f.x * inv0; w[1] = f.y * inv0; w[2] = f.x * inv1; w[3] = f.y * inv1;
+                }
+                if (up) {
+                    cl = *reinterpret_cast<const float2*>(gs.col + i);
+                    const float2 u = *reinterpret_cast<const float2*>(gs.up + i);
+                    w[0] *= u.x; w[1] *= u.y; w[2] *= u.x; w[3] *= u.y;
                 }
                 if (it == rg) {
 #pragma unroll
@@ -656,8 +649,8 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             }
         }
         if (cg == 0) {
-            ws0 = quad_sum(ws0) * r0;
-            ws1 = quad_sum(ws1) * r1;
+            ws0 = quad_sum(ws0);
+            ws1 = quad_sum(ws1);
             if (t == 0) {
                 sm.sum[s & 1][j0 + g] = row < end ? ws0 : 0.f;
                 sm.sum[s & 1][j0 + g + 8] = row + 8 < end ? ws1 : 0.f;
@@ -672,17 +665,17 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
             const T* kp = kt + (j0 + g) * LD + cc;
             if (row < end) {
                 load_pair(kp, x, y);
-                store_pair(dk + (size_t)row * D + cc, r0 * (ak[n][0] + rs0) * slope_f<PHI>(x), r0 * (ak[n][1] + rs0) * slope_f<PHI>(y));
-                store_pair(dv + (size_t)row * D + cc, r0 * av[n][0], r0 * av[n][1]);
+                store_pair(dk + (size_t)row * D + cc, (ak[n][0] + rs0) * slope_f<PHI>(x), (ak[n][1] + rs0) * slope_f<PHI>(y));
+                store_pair(dv + (size_t)row * D + cc, av[n][0], av[n][1]);
             }
             if (row + 8 < end) {
                 load_pair(kp + 8 * LD, x, y);
-                store_pair(dk + (size_t)(row + 8) * D + cc, r1 * (ak[n][2] + rs1) * slope_f<PHI>(x), r1 * (ak[n][3] + rs1) * slope_f<PHI>(y));
-                store_pair(dv + (size_t)(row + 8) * D + cc, r1 * av[n][2], r1 * av[n][3]);
+                store_pair(dk + (size_t)(row + 8) * D + cc, (ak[n][2] + rs1) * slope_f<PHI>(x), (ak[n][3] + rs1) * slope_f<PHI>(y));
+                store_pair(dv + (size_t)(row + 8) * D + cc, av[n][2], av[n][3]);
             }
         }
         if (s + 1 < nch) {
-            st.template update<PHI>(qt, gt, gs.from_start, gs.col, wq != nullptr, gs.all, warp, lane);
+            st.template update<PHI>(qt, gt, gs.from_start, up ? gs.up : nullptr, gs.col, up != nullptr, gs.all, warp, lane);
             if (SH::SB == 1) __syncthreads();  // every warp has read the operand and the tiles
             if (SH::ST == 1) fetch(s + 1);
             const int nb = SH::SB == 2 ? ((s + 1) & 1) : 0;
@@ -695,7 +688,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 
 template <typename T, int D, int PHI>
 cudaError_t launch_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                         const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,
+                         const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
                          void* chunk_state, cudaStream_t st) {
     constexpr size_t smem = sizeof(typename BwdQ<T, D, PHI>::Smem);
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -704,12 +697,12 @@ cudaError_t launch_bwd_q(const Problem& p, const void* q, const void* k, const v
     return launch_pdl(gated_bwd_q_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
                       smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
                       gates, static_cast<const T*>(dout), prefix, p.N, block_tokens, nblk,
-                      p.normalize, static_cast<T*>(dq), wq, up, col, dgp, static_cast<uint8_t*>(chunk_state));
+                      p.normalize, static_cast<T*>(dq), up, col, dgp, static_cast<uint8_t*>(chunk_state));
 }
 
 template <typename T, int D, int PHI>
 cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates,
-                          const void* dout, const float* suffix, int block_tokens, int nblk, const float* wq, const float* up, const float* col,
+                          const void* dout, const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
                           const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     constexpr size_t smem = sizeof(BwdKvSmem<T, D>);
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -717,7 +710,7 @@ cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const 
     if (e != cudaSuccess) return e;
     return launch_pdl(gated_bwd_kv_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
                       smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-                      static_cast<const T*>(g), gates, static_cast<const T*>(dout), suffix, p.N, block_tokens, nblk, wq, up, col, dgp,
+                      static_cast<const T*>(g), gates, static_cast<const T*>(dout), suffix, p.N, block_tokens, nblk, up, col, dgp,
                       static_cast<const uint8_t*>(chunk_state), static_cast<T*>(dk), static_cast<T*>(dv),
                       static_cast<T*>(dg));
 }
@@ -726,20 +719,20 @@ cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const 
 
 template <typename T>
 cudaError_t gated_bwd_q_t(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                          const float* prefix, int block_tokens, int nblk, void* dq, float* wq, float* up, float* col, float* dgp,
+                          const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
                           void* chunk_state, cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
         return gated::launch_bwd_q<T, decltype(d)::value, decltype(phi)::value>(
-            p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, wq, up, col, dgp, chunk_state, st);
+            p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, up, col, dgp, chunk_state, st);
     });
 }
 template <typename T>
 cudaError_t gated_bwd_kv_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates,
-                           const void* dout, const float* suffix, int block_tokens, int nblk, const float* wq, const float* up, const float* col,
+                           const void* dout, const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
                            const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
         return gated::launch_bwd_kv<T, decltype(d)::value, decltype(phi)::value>(
-            p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, wq, up, col, dgp, chunk_state, dk, dv, dg, st);
+            p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, up, col, dgp, chunk_state, dk, dv, dg, st);
     });
 }
 

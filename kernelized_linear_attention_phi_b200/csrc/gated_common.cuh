@@ -52,15 +52,18 @@ template <typename SH> __device__ __forceinline__ int row_group(int warp) {
 
 // The gates of one chunk, from b_i = log2 of the product of the chunk's gates
 // up to token i (gate_scan.cuh). The decay from key j to query i, 2^(b_i - b_j),
-// is used as the product of from_start_i and inv_j, one factor per row and one
-// per column, while no b of the chunk lies below -90 (deep = 0), where both stay
-// well inside fp32. In a deep chunk it is formed per pair from b = hi + lo.
+// is the product of from_start_i and inv_j while every b of the chunk lies
+// within 90 of 0 (deep = 0). In a deep chunk it is formed per pair from
+// b = hi + lo. The two factors meet before either touches a product of tokens:
+// inv_j is up to 2^90, and (phi(q_i).phi(k_j)) inv_j v_j would leave fp32 for
+// products of some 2^37, as 2^-90 of a small upstream gradient would leave its
+// normal range.
 // They are computed once per call for all chunks (gates_kernel, gated.cu) and
 // come with the tiles: forming them inside a sweep puts a warp's scan on
 // every chunk's way.
 template <int C> struct alignas(16) Gates {
     float hi[C], lo[C];
-    float from_start[C];  // 2^b_i; 0 past the last token. Second sweep, normalized: times 1 / den_i
+    float from_start[C];  // 2^b_i; 0 past the last token
     float inv[C];         // 2^-b_j
     float to_end[C];      // 2^(b_last - b_j); 0 past the last token
     float all;            // 2^b_last
@@ -68,24 +71,20 @@ template <int C> struct alignas(16) Gates {
     float up[C], col[C];  // second sweep, normalized: 1 / den_i and -(out_i . dout_i); 0 past the last token
 };
 template <int C> constexpr int kGateBytes = (5 * C + 4) * 4;  // of a chunk's record in global memory
-constexpr float kDeep = -90.f;
-// Starts the copy of a chunk's gates; with wq (the second sweep of a normalized
-// call: wq, up, col of the head, from row0 on) those too.
+constexpr float kDeep = 90.f;
+// Starts the copy of a chunk's gates; with up (the second sweep of a normalized
+// call: up, col of the head, from row0 on) those too.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 template <int C>
-__device__ __forceinline__ void load_gates(Gates<C>& s, const uint8_t* rec, const float* wq, const float* up, const float* col,
-                                           int row0, int N) {
+__device__ __forceinline__ void load_gates(Gates<C>& s, const uint8_t* rec, const float* up, const float* col, int row0, int N) {
     static_assert(offsetof(Gates<C>, up) == kGateBytes<C>, "record");
     const int u = threadIdx.x;
-    const bool weighted = u >= C / 2 && u < 3 * C / 4;  // 16-byte pieces of from_start
-    if (u < kGateBytes<C> / 16 && !(wq && weighted))
-        cp_async16(reinterpret_cast<uint8_t*>(&s) + u * 16, rec + u * 16, true);
-    if (wq && u < C) {
+    if (u < kGateBytes<C> / 16) cp_async16(reinterpret_cast<uint8_t*>(&s) + u * 16, rec + u * 16, true);
+    if (up && u < C) {
         const bool in = row0 + u < N;
         const int i = in ? row0 + u : 0;
-        cp_async4(s.from_start + u, wq + i, in);
         cp_async4(s.up + u, up + i, in);
         cp_async4(s.col + u, col + i, in);
     }
@@ -181,18 +180,23 @@ template <typename T, int D> struct State {
             zs[row(warp) + g + 8] = z[2] + z[3];
         }
     }
-    // S = all S + sum_j w_j phi(x_j) (x) y_j,  z = all z + sum_j w_j phi(x_j) c_j
-    // with x, y [C x D] tiles and w, c (c null: ones) of the chunk; z only with `with_z`. w phi(x)
+    // S = all S + sum_j w_j u_j phi(x_j) (x) y_j,  z = all z + sum_j w_j u_j phi(x_j) c_j
+    // with x, y [C x D] tiles and w, u, c (u or c null: ones) of the chunk; z only with `with_z`. w u phi(x)
     // is formed in fp32 and multiplied as hi + lo operands, so a state of bf16
     // rows errs by 2^-17 of its terms, not by bf16's 2^-8.
     template <int PHI>
-    __device__ __forceinline__ static void weighted(float (&f)[8], const T* x, const float* w, int k0, int warp, int lane) {
+    __device__ __forceinline__ static void weighted(float (&f)[8], const T* x, const float* w, const float* u, int k0, int warp,
+                                                    int lane) {
         const int t = lane & 3;
         FragA<T> a;
         load_at<SH::LD>(a, x, k0, row(warp), lane);
         unpack(a, f);
-        const float2 w0 = *reinterpret_cast<const float2*>(w + k0 + 2 * t);
-        const float2 w1 = *reinterpret_cast<const float2*>(w + k0 + 8 + 2 * t);
+        float2 w0 = *reinterpret_cast<const float2*>(w + k0 + 2 * t);
+        float2 w1 = *reinterpret_cast<const float2*>(w + k0 + 8 + 2 * t);
+        if (u) {
+            w0.x *= u[k0 + 2 * t]; w0.y *= u[k0 + 2 * t + 1];
+            w1.x *= u[k0 + 8 + 2 * t]; w1.y *= u[k0 + 8 + 2 * t + 1];
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             f[2 * r] = phi_f<PHI>(f[2 * r]) * w0.x;
@@ -202,15 +206,15 @@ template <typename T, int D> struct State {
         }
     }
     template <int PHI>
-    __device__ __forceinline__ void update(const T* x, const T* y, const float* w, const float* c, bool with_z, float all,
-                                           int warp, int lane, bool exact = false) {
+    __device__ __forceinline__ void update(const T* x, const T* y, const float* w, const float* u, const float* c, bool with_z,
+                                           float all, int warp, int lane, bool exact = false) {
         if (!owns(warp)) return;
         constexpr int K = SH::C / 16;
         FragA<T> hi[K], lo[K];
 #pragma unroll
         for (int kt = 0; kt < K; ++kt) {
             float f[8];
-            weighted<PHI>(f, x, w, kt * 16, warp, lane);
+            weighted<PHI>(f, x, w, u, kt * 16, warp, lane);
             split_a(hi[kt], lo[kt], f);
         }
         // A chunk's sum is formed from zero and then added: the matrix
@@ -264,7 +268,7 @@ template <typename T, int D> struct State {
             for (int kt = 0; kt < K; ++kt) {
                 float f[8];
                 FragA<T> rest;
-                weighted<PHI>(f, x, w, kt * 16, warp, lane);
+                weighted<PHI>(f, x, w, u, kt * 16, warp, lane);
                 rest_a(rest, f);
 #pragma unroll
                 for (int n = 0; n < SH::SN / 16; ++n) {

@@ -5,8 +5,7 @@
 //   out_i = [ sum_{j <= i} e^{b_i - b_j} (phi(q_i).phi(k_j)) v_j + e^{b_i} phi(q_i) S ] / (the same with v = 1)
 //   S    <- e^{b_last} S + sum_j e^{b_last - b_j} phi(k_j) (x) v_j
 // e^{b_i - b_j} is taken as e^{b_i} e^{-b_j} where the chunk's sums allow it
-// (gated_common.cuh, Gates): one factor per key inside, one per query at the
-// end, and the state's part needs none of its own.
+// (gated_common.cuh, Gates).
 
 #pragma once
 
@@ -55,7 +54,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 
     auto fetch = [&](int c) {
         const int row0 = first + c * C;
-        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, nullptr, row0, N);
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][2], v, row0, N);
@@ -111,18 +110,13 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             }
         }
         const bool deep = gs.deep;
-        float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
+        const float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
         // z's product sits in columns 0 and 1 (t == 0); the row sums below add over the quad
-        float den0 = t == 0 ? oz[0] + oz[1] : 0.f, den1 = t == 0 ? oz[2] + oz[3] : 0.f;
+        float den0 = t == 0 ? f0 * (oz[0] + oz[1]) : 0.f, den1 = t == 0 ? f1 * (oz[2] + oz[3]) : 0.f;
         const float hi0 = gs.hi[i0 + g], lo0 = gs.lo[i0 + g], hi1 = gs.hi[i0 + g + 8], lo1 = gs.lo[i0 + g + 8];
-        if (deep) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                o[n][0] *= f0; o[n][1] *= f0; o[n][2] *= f1; o[n][3] *= f1;
-            }
-            den0 *= f0;
-            den1 *= f1;
-            f0 = f1 = 1.f;
+        for (int n = 0; n < NT; ++n) {
+            o[n][0] *= f0; o[n][1] *= f0; o[n][2] *= f1; o[n][3] *= f1;
         }
 #pragma unroll 1
         for (int jt = 0; jt <= rg; ++jt) {
@@ -150,7 +144,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                     }
                 } else {
                     const float2 w = *reinterpret_cast<const float2*>(gs.inv + j);
-                    p[n][0] *= w.x; p[n][1] *= w.y; p[n][2] *= w.x; p[n][3] *= w.y;
+                    p[n][0] *= f0 * w.x; p[n][1] *= f0 * w.y; p[n][2] *= f1 * w.x; p[n][3] *= f1 * w.y;
                 }
                 if (jt == rg) {
 #pragma unroll
@@ -177,7 +171,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 mma_step(o[2 * n + 1], a, b[1]);
             }
         }
-        float r0 = f0, r1 = f1;  // the same factor over and under the line of a normalized output
+        float r0 = 1.f, r1 = 1.f;
         if (normalize) {
             r0 = 1.f / quad_sum(den0);
             r1 = 1.f / quad_sum(den1);
@@ -195,7 +189,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             }
         }
         if (c + 1 < nch || S_out) {
-            st.template update<PHI>(kt, vt, gs.to_end, nullptr, true, gs.all, warp, lane, S_out != nullptr);
+            st.template update<PHI>(kt, vt, gs.to_end, nullptr, nullptr, true, gs.all, warp, lane, S_out != nullptr);
             if (SH::SB == 1) __syncthreads();  // every warp has read the operand and the tiles
             if (c + 1 < nch) {
                 if (SH::ST == 1) fetch(c + 1);
@@ -215,9 +209,8 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 template <typename T, int D, int PHI, bool REVERSE>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS)
 gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8_t* __restrict__ gates,
-                   const float* wq, const float* up, const float* col, int N, int block_tokens, int nblk, int blk0, bool exact,
-                   float* __restrict__ rec,
-                   float* __restrict__ dec) {
+                   const float* up, const float* col, int N, int block_tokens, int nblk, int blk0, bool exact,
+                   float* __restrict__ rec, float* __restrict__ dec) {
     using SH = Shape<T, D>;
     constexpr int C = SH::C;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -229,8 +222,7 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8
     x += (size_t)bh * N * D;
     y += (size_t)bh * N * D;
     gates += ((size_t)bh * ((N + C - 1) / C) + first / C) * kGateBytes<C>;
-    if (wq) {
-        wq += (size_t)bh * N;
+    if (up) {
         up += (size_t)bh * N;
         col += (size_t)bh * N;
     }
@@ -238,7 +230,7 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8
     auto chunk = [&](int c) { return REVERSE ? nch - 1 - c : c; };
     auto fetch = [&](int c) {
         const int row0 = first + chunk(c) * C;
-        load_gates<C>(sm.gates[c & 1], gates + (size_t)chunk(c) * kGateBytes<C>, wq, up, col, row0, N);
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)chunk(c) * kGateBytes<C>, up, col, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], x, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], y, row0, N);
         cp_async_commit();
@@ -254,7 +246,7 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8
         if (SH::ST == 2 && c + 1 < nch) fetch(c + 1);
         const Gates<C>& gs = sm.gates[c & 1];
         st.template update<PHI>(sm.tiles[c % SH::ST][0], sm.tiles[c % SH::ST][1], REVERSE ? gs.from_start : gs.to_end,
-                                REVERSE ? gs.col : nullptr, !REVERSE || wq, gs.all, warp, lane, !REVERSE && exact);
+                                REVERSE && up ? gs.up : nullptr, REVERSE ? gs.col : nullptr, !REVERSE || up, gs.all, warp, lane, !REVERSE && exact);
         total *= gs.all;
         if (SH::ST == 1 && c + 1 < nch) {
             __syncthreads();  // every warp has read the tiles
@@ -282,7 +274,7 @@ cudaError_t launch_sweep(const Problem& p, const void* q, const void* k, const v
 
 template <typename T, int D, int PHI>
 cudaError_t launch_states(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates,
-                          const float* wq, const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
+                          const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                           cudaStream_t st) {
     constexpr size_t smem = sizeof(StateSmem<T, D>);
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -291,13 +283,13 @@ cudaError_t launch_states(const Problem& p, bool reverse, const void* x, const v
         const cudaError_t e = ensure_smem<gated_state_kernel<T, D, PHI, true>>(smem);
         if (e != cudaSuccess) return e;
         return launch_pdl(gated_state_kernel<T, D, PHI, true>, grid, dim3(Shape<T, D>::THREADS), smem, st,
-                          static_cast<const T*>(x), static_cast<const T*>(y), gates, wq, up, col, p.N,
+                          static_cast<const T*>(x), static_cast<const T*>(y), gates, up, col, p.N,
                           block_tokens, nblk, blk0, exact, rec, dec);
     }
     const cudaError_t e = ensure_smem<gated_state_kernel<T, D, PHI, false>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(gated_state_kernel<T, D, PHI, false>, grid, dim3(Shape<T, D>::THREADS), smem, st,
-                      static_cast<const T*>(x), static_cast<const T*>(y), gates, wq, up, col, p.N,
+                      static_cast<const T*>(x), static_cast<const T*>(y), gates, up, col, p.N,
                       block_tokens, nblk, blk0, exact, rec, dec);
 }
 
@@ -314,10 +306,10 @@ cudaError_t gated_sweep_t(const Problem& p, const void* q, const void* k, const 
 }
 template <typename T>
 cudaError_t gated_states_t(const Problem& p, bool reverse, const void* x, const void* y, const uint8_t* gates,
-                           const float* wq, const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
+                           const float* up, const float* col, int block_tokens, int nblk, int blk0, int count, bool exact, float* rec, float* dec,
                            cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
-        return gated::launch_states<T, decltype(d)::value, decltype(phi)::value>(p, reverse, x, y, gates, wq, up, col, block_tokens,
+        return gated::launch_states<T, decltype(d)::value, decltype(phi)::value>(p, reverse, x, y, gates, up, col, block_tokens,
                                                                                 nblk, blk0, count, exact, rec, dec, st);
     });
 }

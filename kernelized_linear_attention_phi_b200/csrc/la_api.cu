@@ -92,7 +92,7 @@ int prefix_nbins(const Problem& p, int kchunk) { return p.N / kchunk + 1; }
 struct WsLayout {
     size_t part = 0, sz = 0, perm = 0, msort = 0, bins = 0, total = 0;
     size_t grec = 0, gtot = 0, gn = 0, gden = 0;  // gradients
-    size_t dec = 0, gates = 0, wq = 0, up = 0, col = 0, dgp = 0, chunks = 0;  // gated forms
+    size_t dec = 0, gates = 0, up = 0, col = 0, dgp = 0, chunks = 0;  // gated forms
 };
 
 WsLayout ws_layout(const Problem& p, int op) {
@@ -170,8 +170,6 @@ WsLayout ws_layout(const Problem& p, int op) {
         }
         if (bwd) {
             const size_t tokens = (size_t)p.bh() * p.N * sizeof(float);
-            L.wq = off;
-            off = round_up(off + tokens, kAlign);
             L.up = off;
             off = round_up(off + tokens, kAlign);
             L.col = off;
@@ -611,7 +609,7 @@ la_status la_gated_causal(const la_desc* desc, const void* q, const void* k, con
     LA_TRY(cuda_status(gated_gates(p, g, gates, st)));
     if (bp.nblk == 1)
         return cuda_status(gated_sweep(p, q, k, v, gates, nullptr, S_in, z_in, bp.block_tokens, 1, out, S_out, z_out, st));
-    LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
+    LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
                                     S_out ? bp.nblk : bp.nblk - 1, S_out != nullptr, part, dec, st)));
     LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, S_in, z_in, S_out, z_out, st)));
     return cuda_status(gated_sweep(p, q, k, v, gates, part, nullptr, nullptr, bp.block_tokens, bp.nblk, out, nullptr,
@@ -636,7 +634,6 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
     const BlockPlan bp = gated_plan(p, true);
     uint8_t* gates = at<uint8_t>(ws, L.gates);
     LA_TRY(cuda_status(gated_gates(p, g, gates, st)));
-    float* wq = p.normalize ? at<float>(ws, L.wq) : nullptr;
     float* up = p.normalize ? at<float>(ws, L.up) : nullptr;
     float* col = p.normalize ? at<float>(ws, L.col) : nullptr;
     float* dgp = at<float>(ws, L.dgp);
@@ -653,22 +650,22 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
             LA_TRY(cuda_status(tc_gated_states(p, false, k, v, g, nullptr, nullptr, bp.block_tokens, bp.nblk, 0, bp.nblk - 1,
                                                false, part, dec, flags, st)));
         else
-            LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
+            LA_TRY(cuda_status(gated_states(p, false, k, v, gates, nullptr, nullptr, bp.block_tokens, bp.nblk, 0,
                                         bp.nblk - 1, false, part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
-    LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, gates, dout, part, bp.block_tokens, bp.nblk, dq, wq, up, col, dgp, chunks,
+    LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, gates, dout, part, bp.block_tokens, bp.nblk, dq, up, col, dgp, chunks,
                                    st)));
     if (bp.nblk > 1) {  // the same records, from the other end
         if (tcs)
             LA_TRY(cuda_status(tc_gated_states(p, true, q, dout, g, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, false,
                                                part, dec, flags, st)));
         else
-            LA_TRY(cuda_status(gated_states(p, true, q, dout, gates, wq, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, false,
+            LA_TRY(cuda_status(gated_states(p, true, q, dout, gates, up, col, bp.block_tokens, bp.nblk, 1, bp.nblk - 1, false,
                                         part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, true, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
-    return cuda_status(gated_bwd_kv(p, q, k, v, g, gates, dout, part, bp.block_tokens, bp.nblk, wq, up, col, dgp, chunks,
+    return cuda_status(gated_bwd_kv(p, q, k, v, g, gates, dout, part, bp.block_tokens, bp.nblk, up, col, dgp, chunks,
                                     dk, dv, dg, st));
 }
 

@@ -60,3 +60,28 @@ def test_norms_of_long_blocks_at_d128(phi, normalize):
     """40 heads of 900 tokens: the gradients' block states on the tensor cores, in both directions."""
     q, k, v, g, dout = inputs(2, 20, 900, 128, "bf16", phi, seed=4)
     check_gradients("bf16", q, k, v, g, dout, phi, normalize)
+
+
+@pytest.mark.parametrize("dt,d", [x for x in KINDS if x != ("bf16", 128)])
+@pytest.mark.parametrize("phi,normalize", MODES)
+@pytest.mark.parametrize("lowest", [-88.0, -50.0, -120.0])
+def test_large_values_under_fast_gates(dt, d, phi, normalize, lowest):
+    """Values of thousands and an upstream of 65536 under gates that close a chunk by 50 to 120 bits: no
+    factor of a decay stands next to a product of tokens for longer than the decay itself."""
+    q, k, v, g, dout = inputs(1, 2, 200, d, dt, phi, seed=11, sigma=4000.0 * (d ** 0.5 if phi == "identity" else 1.0))
+    g.fill_(rate(dt, d, lowest))
+    check_out(dt, q, k, v, g, phi, normalize)
+    q, k, v = (x / 32 for x in (q, k, v))
+    if phi == "elu1":  # e^-4000 has no digits to compare: features between e^-30 and 125
+        q, k = q.clamp(min=-30), k.clamp(min=-30)
+    check_gradients(dt, q, k, v, g, dout * 65536, phi, normalize)
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 32), ("f32", 64)])
+@pytest.mark.parametrize("phi,normalize", MODES)
+def test_small_upstream_under_fast_gates(dt, d, phi, normalize):
+    """A loss's mean over many tokens makes upstream gradients of 2^-40: a decay of 2^-88 next to them
+    leaves fp32's normal range."""
+    q, k, v, g, dout = inputs(1, 2, 200, d, dt, phi, seed=12)
+    g.fill_(rate(dt, d, -88.0))
+    check_gradients(dt, q, k, v, g, dout * 2.0 ** -40, phi, normalize)

@@ -10,15 +10,20 @@
 // Sweep (tc_gated_sweep_kernel): the transposed layout of the ungated d = 128
 // sweep (tc_sweep_t.cu): S^T and O^T have d_v = 128 lanes. Per chunk, with
 // b_i = log2 of the product of the chunk's gates up to i:
-//   O^T  = S_prev^T phi(Q)^T                     query i unscaled
-//   O^T += V^T P~^T,  P~_ij = (phi(q_i).phi(k_j)) 2^(-b_j)   j <= i
-//   out_i = 2^(b_i) O_i / den_i,  den_i = 2^(b_i) (phi(q_i).z_prev + sum_j P~_ij)
+//   Q'   = 2^(n_i) phi(Q),  n_i = b_i rounded to a whole number within [-90, 0], or 0 (below)
+//   O^T  = S_prev^T Q'^T
+//   O^T += V^T P~^T,  P~_ij = (q'_i.phi(k_j)) 2^(-b_j)   j <= i
+//   out_i = 2^(b_i - n_i) O_i / den_i,  den_i likewise (q'_i.z_prev + sum_j P~_ij)
 //   S^T  = 2^(b_last) S^T + V^T (w phi(K)),  w_j = 2^(b_last - b_j)
 // so that one accumulator takes both parts and the decay of a weight is one
-// factor per key (and of a normalized output none at all). 2^(-b_j) is bounded:
-// where b_i < -90 the scale 2^(b_i) becomes 2^(-90), P~_ij = P_ij 2^(b_i + 90 -
-// b_j), which leaves the state in front a weight of 2^(-90) next to the
-// query's own key instead of the smaller true one.
+// factor per key (and of a normalized output none at all). 2^(n_i) costs no
+// bits of phi(q) and keeps what 2^(-b_j) multiplies as small as the decay makes
+// the weight: without it products of some 2^37 left fp32. A chunk whose b all
+// lie above -16 has no such factors and keeps n_i = 0, which spares the identity
+// map its pass over Q (1x16x131072x128: sweep 467 us with the pass in every
+// chunk, 433 with the choice; the other maps pass over Q anyway). Where b_i < -90,
+// P~_ij = (q'_i.phi(k_j)) 2^(b_i + 90 - b_j), which leaves the state in front a
+// weight of 2^(-90) next to the query's own key instead of the smaller true one.
 
 #include "tc_gated.cuh"
 
@@ -287,12 +292,12 @@ struct GtCfg {
     static constexpr int TILE = NB * BOX;
     static constexpr int QK = TILE + NB * KBOX;    // Q, K' of a chunk: two slots, free after its P and O^T
     static constexpr int VS = 3;                   // V slots: free after its O^T += V^T P~^T, a chunk later
-    static constexpr int GS = 4;                   // gate slots [b | 2^-b]
+    static constexpr int GS = 4;                   // gate slots [b | 2^-b | 2^n twice, bf16]
     static constexpr int PT = C * C * 2;           // P~ [query][key], K-major (x2)
     static constexpr int STG = TILE;               // output staging tile
     static constexpr int KW = 2 * TILE;            // w phi(K), high and low part (x2)
     static constexpr int INV = 2 * C * 4;          // output scale per query row (x2)
-    static constexpr int GATES = GS * 2 * C * 4;
+    static constexpr int GATES = GS * 3 * C * 4;
     static constexpr int NBAR = 2 + 2 + 2 * VS + GS + 2 + 2 + 2 + 5 * 2;
     static constexpr size_t SMEM = 1024 + 2 * (size_t)QK + VS * TILE + 2 * PT + STG + 2 * KW + INV + GATES +
                                    8 * NBAR + 16;
@@ -322,7 +327,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     uint8_t* kws = stg + CF::STG;
     float* inv = reinterpret_cast<float*>(kws + 2 * CF::KW);
     float* gates = inv + 2 * C;
-    uint64_t* fullqk = reinterpret_cast<uint64_t*>(gates + CF::GS * 2 * C);
+    uint64_t* fullqk = reinterpret_cast<uint64_t*>(gates + CF::GS * 3 * C);
     uint64_t* emptyqk = fullqk + 2;
     uint64_t* fullv = emptyqk + 2;
     uint64_t* emptyv = fullv + CF::VS;
@@ -389,15 +394,18 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             const float f0 = gate_float2(sums.b[0]).x + (sums.bad & 1 ? NAN : 0.f);
             const float f1 = gate_float2(sums.b[1]).x + (sums.bad & 2 ? NAN : 0.f);
             const bool low = __any_sync(0xffffffffu, fminf(f0, f1) < kDeep);
+            const bool steep = __any_sync(0xffffffffu, fminf(f0, f1) < kSteep);
             // chunk ci - 2's P and O^T are done, and with them (in order) all
             // that chunk ci - 4 needed its gates for
             if (ci >= 2 && !__all_sync(0xffffffffu, mbar_wait(emptyqk + j, ((ci >> 1) - 1) & 1, err))) break;
-            float* gs = gates + (ci % CF::GS) * 2 * C + 2 * lane;
+            float* gs = gates + (ci % CF::GS) * 3 * C + 2 * lane;
             gs[0] = f0;
             gs[1] = f1;
             // 2^-b, or in its first place infinity: some query lies below kDeep
             gs[C] = lane == 0 && low ? INFINITY : ex2(-f0);
             gs[C + 1] = ex2(-f1);
+            gs[2 * C] = __uint_as_float(whole_pow2(f0, steep));
+            gs[2 * C + 1] = __uint_as_float(whole_pow2(f1, steep));
             __syncwarp();
             if (elect_one()) {
                 mbar_arrive(gfull + ci % CF::GS);
@@ -527,7 +535,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             uint8_t* kt = qks + j * CF::QK + CF::TILE;
             uint8_t* kw = kws + j * CF::KW;
             mbar_wait(fullqk + j, k & 1, err);
-            const float* gs = gates + (ci % CF::GS) * 2 * C;
+            const float* gs = gates + (ci % CF::GS) * 3 * C;
             const float blast = gs[C - 1];
             float w[2];
 #pragma unroll
@@ -602,15 +610,19 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 #pragma unroll 1
         for (int ci = 0; ci < nci; ++ci) {
             const int et = threadIdx.x - (64 + CF::TRANSFORM);
-            if (PHI != PHI_IDENTITY) {  // phi on the chunk's queries, while the last update runs
+            const float* gs = gates + (ci % CF::GS) * 3 * C;
+            mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
+            const float all = ex2(gs[C - 1]);
+            // phi on the chunk's queries and their scales, while the last update runs
+            const uint32_t* pow2 = reinterpret_cast<const uint32_t*>(gs + 2 * C);
+            if (PHI != PHI_IDENTITY || __any_sync(0xffffffffu, pow2[lane] != kOne2 || pow2[lane + 32] != kOne2)) {
                 mbar_wait(fullqk + (ci & 1), (ci >> 1) & 1, err);
                 uint4* q = reinterpret_cast<uint4*>(qks + (ci & 1) * CF::QK);
 #pragma unroll 2
-                for (int x = et; x < CF::TILE / 16; x += CF::STATE) q[x] = phi_round8<PHI>(q[x]);
+                for (int x = et; x < CF::TILE / 16; x += CF::STATE)  // 8 pieces of 16 bytes per row of a box
+                    q[x] = scale8(phi_round8<PHI>(q[x]), pow2[(x / 8) % C]);
                 fence_async_smem();
             }
-            mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
-            const float all = ex2(gates[(ci % CF::GS) * 2 * C + C - 1]);
             if (ci > 0) {
                 mbar_wait(bsdone, (ci - 1) & 1, err);
                 tc_fence_after();
@@ -649,7 +661,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             const uint32_t lane_s = lane_base + static_cast<uint32_t>(slot) * (16u << 16);
             uint8_t* pts = pt + slot * CF::PT;
             mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
-            const float* gs = gates + (ci % CF::GS) * 2 * C;
+            const float* gs = gates + (ci % CF::GS) * 3 * C;
             const float bi = gs[i];
             const bool deep = isinf(gs[C]);  // some query of the chunk lies below kDeep
             const float own = bi - fmaxf(bi, kDeep);
@@ -693,7 +705,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             }
             // the scales of chunk ci - 2 have been read
             if (use > 0) mbar_wait(bofree + slot, (use - 1) & 1, err);
-            if (lane < 16) inv[slot * C + i] = normalize ? __fdividef(1.f, rs) : ex2(fmaxf(bi, kDeep));
+            if (lane < 16) inv[slot * C + i] = normalize ? __frcp_rn(rs) : ex2(fmaxf(bi, kDeep) - whole_bits(__float_as_uint(gs[2 * C + i])));
             warp_arrive(binv + slot, lane);
         }
     } else {

@@ -11,7 +11,7 @@ namespace tcg {
 
 using namespace tc;
 
-// Queries whose products reach below 2^-90 are scaled by 2^90 (tc_gated.cu).
+// The decays of queries below 2^-90 are taken apart from the state's (tc_gated.cu).
 constexpr float kDeep = -90.f;
 
 // Brings a box of a tensor map towards L2, ahead of its load.
@@ -54,6 +54,27 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^n as two bf16 in one word, n the whole part of a query's decay b that its
+// features take (0 unless the chunk is steep), and n from the word.
+constexpr float kSteep = -16.f;
+constexpr uint32_t kOne2 = 0x3f803f80u;
+__device__ __forceinline__ uint32_t whole_pow2(float b, bool steep) {
+    return steep ? (uint32_t)((int)rintf(fmaxf(fminf(b, 0.f), kDeep)) + 127) * 0x00800080u : kOne2;
+}
+__device__ __forceinline__ float whole_bits(uint32_t word) { return (float)((int)(word >> 23) - 127); }
+// Eight bf16 values times 2^n (exact while they stay in the normal range).
+__device__ __forceinline__ uint4 scale8(const uint4& x, uint32_t pow2) {
+    const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&pow2);
+    uint4 r = x;
+    uint32_t* w = &r.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(w + i), s);
+        w[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    return r;
 }
 
 // The two gates of this lane (tokens row0 + 2 lane, + 1; 0 past the row's end),

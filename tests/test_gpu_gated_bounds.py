@@ -62,7 +62,7 @@ def test_norms_of_long_blocks_at_d128(phi, normalize):
     check_gradients("bf16", q, k, v, g, dout, phi, normalize)
 
 
-@pytest.mark.parametrize("dt,d", [x for x in KINDS if x != ("bf16", 128)])
+@pytest.mark.parametrize("dt,d", KINDS)
 @pytest.mark.parametrize("phi,normalize", MODES)
 @pytest.mark.parametrize("lowest", [-88.0, -50.0, -120.0])
 def test_large_values_under_fast_gates(dt, d, phi, normalize, lowest):
@@ -85,3 +85,15 @@ def test_small_upstream_under_fast_gates(dt, d, phi, normalize):
     q, k, v, g, dout = inputs(1, 2, 200, d, dt, phi, seed=12)
     g.fill_(rate(dt, d, -88.0))
     check_gradients(dt, q, k, v, g, dout * 2.0 ** -40, phi, normalize)
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_denominators_near_the_largest_float(dt, d):
+    """Two tokens that see themselves alone, with phi(q).phi(k) between 2^126 and 2^127: each output is its value."""
+    q = torch.full((1, 1, 2, d), 1.125 * 2.0 ** 63 / d ** 0.5, device="cuda").to(DT[dt])
+    v = torch.linspace(-0.25, 0.25, 2 * d, device="cuda").view(1, 1, 2, d).to(DT[dt])
+    g = torch.full((1, 1, 2), float("-inf"), device="cuda", dtype=DT[dt])
+    assert 2.0 ** 126 < float((q.double() * q.double()).sum(-1).max()) < 2.0 ** 127
+    out = la.la_gated_causal(q, q, v, g)
+    step = torch.finfo(DT[dt]).eps
+    assert float((out.double() - v.double()).abs().max()) <= 0.25 * (step if dt == "bf16" else 8 * step)

@@ -292,12 +292,12 @@ struct GtCfg {
     static constexpr int TILE = NB * BOX;
     static constexpr int QK = TILE + NB * KBOX;    // Q, K' of a chunk: two slots, free after its P and O^T
     static constexpr int VS = 3;                   // V slots: free after its O^T += V^T P~^T, a chunk later
-    static constexpr int GS = 4;                   // gate slots [b | 2^-b | 2^n twice, bf16]
+    static constexpr int GS = 4;                   // gate slots [b | 2^-b | 2^n twice, bf16 | what fp32 left of b]
     static constexpr int PT = C * C * 2;           // P~ [query][key], K-major (x2)
     static constexpr int STG = TILE;               // output staging tile
     static constexpr int KW = 2 * TILE;            // w phi(K), high and low part (x2)
     static constexpr int INV = 2 * C * 4;          // output scale per query row (x2)
-    static constexpr int GATES = GS * 3 * C * 4;
+    static constexpr int GATES = GS * 4 * C * 4;
     static constexpr int NBAR = 2 + 2 + 2 * VS + GS + 2 + 2 + 2 + 5 * 2;
     static constexpr size_t SMEM = 1024 + 2 * (size_t)QK + VS * TILE + 2 * PT + STG + 2 * KW + INV + GATES +
                                    8 * NBAR + 16;
@@ -327,7 +327,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
     uint8_t* kws = stg + CF::STG;
     float* inv = reinterpret_cast<float*>(kws + 2 * CF::KW);
     float* gates = inv + 2 * C;
-    uint64_t* fullqk = reinterpret_cast<uint64_t*>(gates + CF::GS * 3 * C);
+    uint64_t* fullqk = reinterpret_cast<uint64_t*>(gates + CF::GS * 4 * C);
     uint64_t* emptyqk = fullqk + 2;
     uint64_t* fullv = emptyqk + 2;
     uint64_t* emptyv = fullv + CF::VS;
@@ -391,21 +391,23 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             const int j = ci & 1, s = ci % CF::VS, row = first + ci * C;
             const GateSums<2> sums = sum_gates<2>(gr.g, lane);
             if (ci + 1 < nci) gr = load_gates(g, row + C, end, lane);
-            const float f0 = gate_float2(sums.b[0]).x + (sums.bad & 1 ? NAN : 0.f);
-            const float f1 = gate_float2(sums.b[1]).x + (sums.bad & 2 ? NAN : 0.f);
+            // in two floats: behind closed gates (14000 bits each) one would not
+            // hold what lies between two tokens
+            const float2 b0 = gate_float2(sums.b[0]), b1 = gate_float2(sums.b[1]);
+            const float f0 = b0.x + (sums.bad & 1 ? NAN : 0.f), f1 = b1.x + (sums.bad & 2 ? NAN : 0.f);
             const bool low = __any_sync(0xffffffffu, fminf(f0, f1) < kDeep);
             const bool steep = __any_sync(0xffffffffu, fminf(f0, f1) < kSteep);
+            // 2^-b, or in its first place infinity: some query lies below kDeep
+            const float2 inv2 = make_float2(lane == 0 && low ? INFINITY : ex2(-f0), ex2(-f1));
+            const float2 pow2 = make_float2(__uint_as_float(whole_pow2(f0, steep)), __uint_as_float(whole_pow2(f1, steep)));
             // chunk ci - 2's P and O^T are done, and with them (in order) all
             // that chunk ci - 4 needed its gates for
             if (ci >= 2 && !__all_sync(0xffffffffu, mbar_wait(emptyqk + j, ((ci >> 1) - 1) & 1, err))) break;
-            float* gs = gates + (ci % CF::GS) * 3 * C + 2 * lane;
-            gs[0] = f0;
-            gs[1] = f1;
-            // 2^-b, or in its first place infinity: some query lies below kDeep
-            gs[C] = lane == 0 && low ? INFINITY : ex2(-f0);
-            gs[C + 1] = ex2(-f1);
-            gs[2 * C] = __uint_as_float(whole_pow2(f0, steep));
-            gs[2 * C + 1] = __uint_as_float(whole_pow2(f1, steep));
+            float2* gs = reinterpret_cast<float2*>(gates + (ci % CF::GS) * 4 * C) + lane;
+            gs[0] = make_float2(f0, f1);
+            gs[C / 2] = inv2;
+            gs[C] = pow2;
+            gs[3 * C / 2] = make_float2(b0.y, b1.y);
             __syncwarp();
             if (elect_one()) {
                 mbar_arrive(gfull + ci % CF::GS);
@@ -535,13 +537,13 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             uint8_t* kt = qks + j * CF::QK + CF::TILE;
             uint8_t* kw = kws + j * CF::KW;
             mbar_wait(fullqk + j, k & 1, err);
-            const float* gs = gates + (ci % CF::GS) * 3 * C;
-            const float blast = gs[C - 1];
+            const float* gs = gates + (ci % CF::GS) * 4 * C;
+            const float blast = gs[C - 1], rest = gs[4 * C - 1];
             float w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = (et >> 3) + 32 * i;
-                w[i] = r < kvalid ? ex2(blast - gs[r]) : 0.f;
+                w[i] = r < kvalid ? ex2((blast - gs[r]) + (rest - gs[3 * C + r])) : 0.f;
             }
             const float all = ex2(blast);
             if (k > 0) mbar_wait(kwfree + j, (k - 1) & 1, err);  // chunk ci - 2's update has read kw
@@ -610,7 +612,7 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
 #pragma unroll 1
         for (int ci = 0; ci < nci; ++ci) {
             const int et = threadIdx.x - (64 + CF::TRANSFORM);
-            const float* gs = gates + (ci % CF::GS) * 3 * C;
+            const float* gs = gates + (ci % CF::GS) * 4 * C;
             mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
             const float all = ex2(gs[C - 1]);
             // phi on the chunk's queries and their scales, while the last update runs
@@ -661,10 +663,9 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             const uint32_t lane_s = lane_base + static_cast<uint32_t>(slot) * (16u << 16);
             uint8_t* pts = pt + slot * CF::PT;
             mbar_wait(gfull + ci % CF::GS, (ci / CF::GS) & 1, err);
-            const float* gs = gates + (ci % CF::GS) * 3 * C;
+            const float* gs = gates + (ci % CF::GS) * 4 * C;
             const float bi = gs[i];
             const bool deep = isinf(gs[C]);  // some query of the chunk lies below kDeep
-            const float own = bi - fmaxf(bi, kDeep);
             mbar_wait(bpfull + slot, use & 1, err);
             tc_fence_after();
             uint32_t r[32], zq[8];
@@ -672,10 +673,14 @@ tc_gated_sweep_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_const
             tmem_ld16x2<32>(tmem + CF::COL_P + lane_s + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
             if (normalize) tmem_ld8x2<8>(tmem + CF::COL_P + lane_s + C, zq);
             tmem_ld_wait();
-            if (deep) {  // the factors per pair; the table's are not used then
+            if (deep) {  // the factors per pair, from both floats; the table's are not used then
+                const bool below = bi < kDeep;
+                const float hi = below ? bi : 0.f, lo = below ? gs[3 * C + i] : 0.f, up = below ? -kDeep : 0.f;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    r[e] = __float_as_uint(__uint_as_float(r[e]) * ex2(own - gs[32 * half + e]));
+                for (int e = 0; e < 32; ++e) {
+                    const int j = 32 * half + e;
+                    r[e] = __float_as_uint(__uint_as_float(r[e]) * ex2((hi - gs[j]) + (lo - gs[3 * C + j]) + up));
+                }
             }
             float rs = 0.f;
 #pragma unroll

@@ -97,3 +97,40 @@ def test_denominators_near_the_largest_float(dt, d):
     out = la.la_gated_causal(q, q, v, g)
     step = torch.finfo(DT[dt]).eps
     assert float((out.double() - v.double()).abs().max()) <= 0.25 * (step if dt == "bf16" else 8 * step)
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("phi,normalize", [("relu1", True), ("identity", False)])
+@pytest.mark.parametrize("closed", [1, 16, 40, 63])
+def test_closed_gates_in_front_inside_the_chunk(dt, d, phi, normalize, closed):
+    """Padding in front of a document: `closed` tokens of closed gates, then the document from inside the
+    chunk on. Its results are those of the document alone."""
+    q, k, v, g, dout = inputs(1, 2, 256, d, dt, phi, seed=13)
+    g[:, :, :closed + 1] = float("-inf")
+    out = check_out(dt, q, k, v, g, phi, normalize, window=32)
+    got = check_gradients(dt, q, k, v, g, dout, phi, normalize)
+    alone = [x[:, :, closed:].contiguous() for x in (q, k, v, g, dout)]
+    ref, like = GB.allowances(dt, *(x.double() for x in alone[:4]), kind=phi, normalize=normalize)
+    assert GB.excess(out[:, :, closed:].double(), ref, like, 2, 32) <= 1
+    ref, like = GB.allowances(dt, *(x.double() for x in alone), kind=phi, normalize=normalize)
+    for i in range(3):
+        assert GB.excess(got[i][:, :, closed:].double(), ref[i], like[i], 2, 128) <= 1
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("length", [2, 4, 13])
+def test_rows_of_short_documents(dt, d, length):
+    q, k, v, g, dout = inputs(1, 2, 300, d, dt, "relu1", seed=14)
+    g[:, :, ::length] = float("-inf")
+    check_out(dt, q, k, v, g, "relu1", True)
+    check_gradients(dt, q, k, v, g, dout, "relu1", True)
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_closed_gates_behind_a_state(dt, d):
+    """Documents inside a row that starts from a state."""
+    q, k, v, g, _ = inputs(1, 2, 200, d, dt, "relu1", seed=15)
+    g[:, :, 5] = g[:, :, 7:30] = float("-inf")
+    S = torch.randn(1, 2, d, d, device="cuda", generator=torch.Generator("cuda").manual_seed(3)) * 4
+    z = torch.rand(1, 2, d, device="cuda", generator=torch.Generator("cuda").manual_seed(4)) * 20 + 20
+    check_out(dt, q, k, v, g, "relu1", True, window=32, S_in=S, z_in=z)

@@ -134,7 +134,7 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
                 w[0] = in0 ? gate_pow2(after + (gs.last - gs.b[0])) + nan : 0.f;
                 w[1] = in1 ? gate_pow2(after + (gs.last - gs.b[1])) + nan : 0.f;
             }
-            after += gs.last;
+            after = gate_add(after, gs.last);
             __syncwarp();
             if (elect_one()) {
                 mbar_arrive_expect_tx(full + s, CF::STAGE);

@@ -9,6 +9,18 @@
 
 namespace la {
 
+// relu(x) with a NaN left as it is, as in the other feature maps (max.f32 would
+// drop it, and a head would go on as if the token's features were ones).
+__device__ __forceinline__ float relu_nan(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t relu_nan_x2(uint32_t w) {  // two bf16
+    const __nv_bfloat162 x = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(0.f));
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
 // Gates below this many bits count as closed: fp32 cannot hold any product
 // across one (and 64 of them stay far inside the integer part).
 constexpr float kClosedBits = -14000.f;

@@ -115,6 +115,11 @@ __device__ __forceinline__ void st_cs(float4* p, float4 v) {
     asm volatile("st.global.cs.v4.f32 [%0], {%1,%2,%3,%4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
+// phi_apply, but a NaN with its sign set stays one too.
+__device__ __forceinline__ float phi_step(float x, int phi) {
+    return phi == PHI_RELU1 ? relu_nan(x) + 1.f : phi_apply(x, phi);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 gated_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
@@ -140,7 +145,7 @@ gated_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     float dpart = 0.f;
     if (tid < D) {
         const float zo = z[bh * D + tid];
-        const float pk = phi_apply(to_f32<T>(k[bh * D + tid]), phi), pq = phi_apply(to_f32<T>(q[bh * D + tid]), phi);
+        const float pk = phi_step(to_f32<T>(k[bh * D + tid]), phi), pq = phi_step(to_f32<T>(q[bh * D + tid]), phi);
         spk[tid] = pk;
         spq[tid] = pq;
         sv[tid] = to_f32<T>(v[bh * D + tid]);

@@ -23,6 +23,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "gate_scan.cuh"
 
 namespace la {
 namespace gated {
@@ -138,7 +139,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // e^x of x <= 0 as 2^(x log2 e): 2^-22 of the value, and 2^-24 |x| from the product's rounding.
 __device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * 1.4426950408889634f); }
 template <int PHI> __device__ __forceinline__ float phi_f(float x) {
-    if (PHI == PHI_RELU1) return fmaxf(x, 0.f) + 1.f;
+    if (PHI == PHI_RELU1) return relu_nan(x) + 1.f;
     if (PHI == PHI_ELU1) return x > 0.f ? x + 1.f : exp_fast(x);
     return x;
 }
@@ -150,9 +151,9 @@ template <int PHI> __device__ __forceinline__ float slope_f(float x) {
 }
 template <int PHI> __device__ __forceinline__ uint32_t phi_pair(uint32_t w) {
     if (PHI == PHI_RELU1) {
-        __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&w);
-        x = __hadd2_rn(__hmax2(x, __float2bfloat162_rn(0.f)), __float2bfloat162_rn(1.f));
-        return *reinterpret_cast<uint32_t*>(&x);
+        w = relu_nan_x2(w);
+        const __nv_bfloat162 x = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(1.f));
+        return *reinterpret_cast<const uint32_t*>(&x);
     }
     if (PHI == PHI_ELU1) return pack_bf16(phi_f<PHI>(bf16_lo(w)), phi_f<PHI>(bf16_hi(w)));
     return w;
@@ -164,7 +165,7 @@ template <int PHI> __device__ __forceinline__ uint32_t phi_pair(uint32_t w) {
 // that all rows share, which the gradients of q cancel.
 template <int PHI> constexpr bool shifted = PHI != PHI_IDENTITY;
 template <int PHI> __device__ __forceinline__ float base_f(float x) {
-    if (PHI == PHI_RELU1) return fmaxf(x, 0.f);
+    if (PHI == PHI_RELU1) return relu_nan(x);
     if (PHI == PHI_ELU1) return x > 0.f ? x : exp_fast(x) - 1.f;
     return x;
 }
@@ -172,8 +173,7 @@ template <int PHI> __device__ __forceinline__ void base_frag(FragB<__nv_bfloat16
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if constexpr (PHI == PHI_RELU1) {
-            const __nv_bfloat162 x = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&b.r[i]), __float2bfloat162_rn(0.f));
-            b.r[i] = *reinterpret_cast<const uint32_t*>(&x);
+            b.r[i] = relu_nan_x2(b.r[i]);
         } else if constexpr (PHI == PHI_ELU1) {
             b.r[i] = pack_bf16(base_f<PHI>(bf16_lo(b.r[i])), base_f<PHI>(bf16_hi(b.r[i])));
         }

@@ -92,17 +92,29 @@ __device__ __forceinline__ Gates2 load_gates(const __nv_bfloat16* g, int row0, i
 }
 
 template <int PHI> __device__ __forceinline__ float phi_f32(float x) {
-    if constexpr (PHI == PHI_RELU1) return fmaxf(x, 0.f) + 1.f;
+    if constexpr (PHI == PHI_RELU1) return relu_nan(x) + 1.f;
     if constexpr (PHI == PHI_ELU1) return x > 0.f ? x + 1.f : ex2(x * 1.4426950408889634f);
     return x;
+}
+// x + 1 of eight bf16 values, rounded to bf16.
+__device__ __forceinline__ uint4 plus_one8(const uint4& x) {
+    uint4 r = x;
+    uint32_t* w = &r.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 y = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(w + i), __float2bfloat162_rn(1.f));
+        w[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    return r;
 }
 // phi(x) of eight bf16 values (rounded to bf16), and w phi(x) in fp32 (f), as a
 // bf16 part and the bf16 of what it leaves.
 template <int PHI>
 __device__ __forceinline__ void weighted8(const uint4& x, float w, float (&f)[8], uint4& phi, uint4& hi, uint4& lo) {
     if constexpr (PHI == PHI_RELU1) {  // w (relu(x) + 1) = w relu(x) + w; relu(x) is exact in bf16
-        phi = phi8<PHI>(x);
-        unpack8(relu_x8(x), f);
+        const uint4 r = make_uint4(relu_nan_x2(x.x), relu_nan_x2(x.y), relu_nan_x2(x.z), relu_nan_x2(x.w));
+        phi = plus_one8(r);
+        unpack8(r, f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], w, w);
     } else {
@@ -133,7 +145,9 @@ template <int PHI> __device__ __forceinline__ uint4 phi_round8(const uint4& x) {
         for (int e = 0; e < 8; ++e) f[e] = phi_f32<PHI>(f[e]);
         return pack8(f);
     }
-    return phi8<PHI>(x);
+    if constexpr (PHI == PHI_RELU1)
+        return plus_one8(make_uint4(relu_nan_x2(x.x), relu_nan_x2(x.y), relu_nan_x2(x.z), relu_nan_x2(x.w)));
+    return x;
 }
 
 }  // namespace tcg

@@ -134,3 +134,30 @@ def test_closed_gates_behind_a_state(dt, d):
     S = torch.randn(1, 2, d, d, device="cuda", generator=torch.Generator("cuda").manual_seed(3)) * 4
     z = torch.rand(1, 2, d, device="cuda", generator=torch.Generator("cuda").manual_seed(4)) * 20 + 20
     check_out(dt, q, k, v, g, "relu1", True, window=32, S_in=S, z_in=z)
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("bf16", 128), ("f32", 16), ("f32", 64)])
+@pytest.mark.parametrize("sign", [0, 1])
+@pytest.mark.parametrize("phi,normalize", MODES)
+def test_a_nan_of_either_sign_reaches_prompt_step_and_gradients(dt, d, sign, phi, normalize):
+    """The same NaN in q or k for every entry point and map (relu as a plain maximum would make 0 of it)."""
+    q, k, v, g, dout = inputs(1, 1, 200, d, dt, phi, seed=16)
+    word, top = (0x7FC0, 15) if dt == "bf16" else (0x7FC00000, 31)
+    nan = torch.tensor(word - (sign << top), dtype=torch.int16 if dt == "bf16" else torch.int32).view(DT[dt]).cuda()
+    for i in range(2):
+        a = [q.clone(), k.clone(), v, g]
+        a[i][0, 0, 150, 5] = nan
+        assert bool(a[i][0, 0, 150, 5].isnan()) and bool(a[i][0, 0, 150, 5].signbit()) == bool(sign)
+        out = la.la_gated_causal(*a, phi=phi, normalize=normalize)[0, 0]
+        assert not out[:128].isnan().any() and bool(out[150].isnan().all())
+        assert bool(out[151:].isnan().all()) if i else not out[151:].isnan().any()
+        dq, dk, dv, dg = (x[0, 0] for x in la.la_gated_causal_backward(*a, dout, phi=phi, normalize=normalize))
+        if normalize:  # the denominator
+            assert bool(dq[150].isnan().all())
+        elif i == 0:  # every earlier value meets phi(q)
+            assert bool(dv[:128].isnan().all())
+        else:  # every later query's channel meets phi(k)
+            assert bool(dq[150:, 5].isnan().all())
+        one = [x[:, :, 150:151].clone() for x in a]
+        S, z = torch.zeros(1, 1, d, d, device="cuda"), torch.zeros(1, 1, d, device="cuda")
+        assert bool(la.la_gated_decode_step(*one, S, z, phi=phi, normalize=normalize).isnan().all())

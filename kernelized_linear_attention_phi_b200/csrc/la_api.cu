@@ -223,6 +223,39 @@ la_status check_rope(const la_rope_desc* d) {
     return LA_OK;
 }
 
+// Whether two rows of a [B, N, H, d] view share an element (strides >= d).
+bool rows_overlap(const la_rope_desc& d, const la_strides& s, int H) {
+    struct Dim {
+        long long size, stride;
+    } dim[3] = {{d.B, s.b}, {d.N, s.n}, {H, s.h}};
+    for (Dim& x : dim)
+        if (x.size == 1) x.stride = 0;
+    std::sort(dim, dim + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    __int128 extent = d.d;  // the usual views nest: each stride steps over all that lies below it
+    bool nested = true;
+    for (const Dim& x : dim) {
+        if (x.size == 1) continue;
+        nested = nested && x.stride >= extent;
+        extent += (__int128)x.stride * (x.size - 1);
+    }
+    if (nested) return false;
+    // others: a difference of indexes, not all 0, that moves by less than a row;
+    // the longest dimension's part follows from those of the other two
+    std::sort(dim, dim + 3, [](const Dim& a, const Dim& b) { return a.size < b.size; });
+    const Dim &x = dim[0], &y = dim[1], &z = dim[2];
+    for (long long i = 0; i < x.size; ++i)
+        for (long long j = i ? 1 - y.size : 0; j < y.size; ++j) {
+            const __int128 at = (__int128)i * x.stride + (__int128)j * y.stride;
+            const __int128 mag = at < 0 ? -at : at;
+            // k * stride next to mag on either side (the sign of k is free); k = 0 alone
+            // is no difference of rows
+            const __int128 k = mag / z.stride, low = mag - k * z.stride;
+            if (k < z.size && low < d.d && (i || j || k)) return true;
+            if (k + 1 < z.size && z.stride - low < d.d) return true;
+        }
+    return false;
+}
+
 // A [B, N, H, d] view: strides in multiples of 16 bytes, not negative; rows of
 // an output must not fall on one another.
 la_status check_strides(const la_rope_desc& d, const la_strides& s, int H, bool output) {
@@ -233,7 +266,7 @@ la_status check_strides(const la_rope_desc& d, const la_strides& s, int H, bool 
         if (stride[i] < 0 || (output && stride[i] < d.d)) return LA_ERR_INVALID_ARG;
         if (stride[i] % unit != 0) return LA_ERR_MISALIGNED;
     }
-    return LA_OK;
+    return output && rows_overlap(d, s, H) ? LA_ERR_INVALID_ARG : LA_OK;
 }
 
 la_status check_rope_inputs(const la_rope_desc& d, const void* q, const la_strides* qs, const void* k,

@@ -15,7 +15,7 @@ namespace la {
 // take in the place of g.
 cudaError_t gated_gates(const Problem& p, const void* g, uint8_t* out, cudaStream_t st);
 size_t gated_gate_bytes(const Problem& p);
-// Outputs of every block of block_tokens tokens (a multiple of 64) from the
+// Outputs (not bf16 at d = 128: tc_gated_sweep) of every block of block_tokens tokens (a multiple of 64) from the
 // state in front of it: record (bh, blk) of `prefix`, or with prefix null (one
 // block) S_in / z_in, or zero. S_out / z_out (one block only): the state after
 // the last token.

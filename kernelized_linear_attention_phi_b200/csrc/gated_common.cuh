@@ -261,7 +261,7 @@ template <typename T, int D> struct State {
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[e] = fmaf(z[e], all, s[e]);
         }
-        if constexpr (!SH::F32) {
+        if constexpr (!SH::F32 && D != 128) {  // d = 128 bf16: a caller's state comes from tc_gated_states
             if (!exact) return;
             // a state that a caller gets: the last bits of w phi(x) too
 #pragma unroll 1

@@ -299,9 +299,13 @@ template <typename T>
 cudaError_t gated_sweep_t(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const float* prefix,
                           const float* S_in, const float* z_in, int block_tokens, int nblk, void* out, float* S_out,
                           float* z_out, cudaStream_t st) {
-    return gated::dispatch(p, [&](auto d, auto phi) {
-        return gated::launch_sweep<T, decltype(d)::value, decltype(phi)::value>(p, q, k, v, gates, prefix, S_in, z_in,
-                                                                               block_tokens, nblk, out, S_out, z_out, st);
+    return gated::dispatch(p, [&](auto d, auto phi) -> cudaError_t {
+        constexpr int D = decltype(d)::value;
+        if constexpr (sizeof(T) == 2 && D == 128)  // tc_gated_sweep's
+            return cudaErrorInvalidValue;
+        else
+            return gated::launch_sweep<T, D, decltype(phi)::value>(p, q, k, v, gates, prefix, S_in, z_in, block_tokens, nblk,
+                                                                   out, S_out, z_out, st);
     });
 }
 template <typename T>

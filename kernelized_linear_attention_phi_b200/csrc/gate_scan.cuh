@@ -2,7 +2,8 @@
 // fixed point (31 bits behind the point). Integer sums are exact: the decay
 // between two tokens depends on the gates between them and on nothing else,
 // however far the chunk has decayed before, and a closed gate drops out of every
-// difference behind it. A gate itself is held to 2^-32.
+// difference behind it. A gate itself is rounded to the nearest: 2^-32, or 2^-25
+// of its fraction where that is more.
 #pragma once
 
 #include "common.cuh"
@@ -32,7 +33,7 @@ __device__ __forceinline__ long long gate_bits(float g) {
     if (!(x >= kClosedBits)) return (long long)(int)kClosedBits << 31;  // -inf too (a NaN is dealt with by the caller)
     const float n = rintf(fminf(x, 16000.f));
     const float f = (fminf(x, 16000.f) - n) + rest;  // at most half, and a little
-    return ((long long)(int)n << 31) + (int)(f * 2147483648.f);
+    return ((long long)(int)n << 31) + __float2int_rn(f * 2147483648.f);
 }
 // The sum with a further chunk's b. It stops at 2^20 bits either way, where
 // fp32 has long reached 0 or infinity: without an end 150,000 closed gates

@@ -71,3 +71,17 @@ def test_a_long_row_of_closed_gates():
     out = la.la_gated_causal(x, x, x, g, S_out=S, z_out=z)
     assert bool((S == 2).all()) and bool((z == 2).all())
     assert torch.equal(out, x)
+
+
+def test_a_gate_is_rounded_to_the_nearest(probe):
+    """Slow gates, which a long row adds up by the thousand: no bias, and no more than half a unit each."""
+    gen = torch.Generator().manual_seed(2)
+    g = -torch.exp(torch.rand(1 << 16, generator=gen) * 7 - 18).cuda()  # 1.5e-8 .. 1.7e-5
+    got = torch.empty(len(g), dtype=torch.int64, device="cuda")
+    assert probe.gate_bits_probe(_ptr(g), _ptr(got), len(g)) == 0
+    # log2 e in two doubles: the product of a 24-bit g with 29 bits of it is exact
+    high = 1.44269504
+    off = got.double() - (g.double() * high + g.double() * (1.4426950408889634 - high)) * 2.0 ** 31
+    assert float(off.abs().max()) <= 0.5 + 2.0 ** -8
+    # errors within half a unit either way: their mean over 2^16 gates is some 0.29 / 2^8
+    assert abs(float(off.mean())) <= 6 * 0.29 / 2 ** 8

@@ -213,9 +213,9 @@ LA_API la_status la_decode_step(const la_desc* desc, const void* q, const void* 
  * gate included: masked products are multiplied by 0, not skipped, and a NaN
  * may reach its head up to 63 tokens in front of its own. A positive g
  * amplifies, within what fp32 can hold; a NaN or +inf gate makes NaN of its head
- * from there on. What lies in front of a chunk of 64 tokens reaches a query whose
- * gates have closed since with a weight of at most 2^-90 next to its own key's.
- * N is at most 2^30. Outputs must not overlap inputs, but for a state that is
+ * from there on. bf16 at d = 128: what lies in front of a chunk of 64 tokens reaches
+ * a query whose gates have closed since with a weight of at most 2^-60 next to its
+ * own key's. N is at most 2^30. Outputs must not overlap inputs, but for a state that is
  * updated in place. */
 
 /* Every output of a row, and optionally the state around it.

@@ -10,7 +10,7 @@
 // Sweep (tc_gated_sweep_kernel): the transposed layout of the ungated d = 128
 // sweep (tc_sweep_t.cu): S^T and O^T have d_v = 128 lanes. Per chunk, with
 // b_i = log2 of the product of the chunk's gates up to i:
-//   Q'   = 2^(n_i) phi(Q),  n_i = b_i rounded to a whole number within [-90, 0], or 0 (below)
+//   Q'   = 2^(n_i) phi(Q),  n_i = b_i rounded to a whole number within [-60, 0], or 0 (below)
 //   O^T  = S_prev^T Q'^T
 //   O^T += V^T P~^T,  P~_ij = (q'_i.phi(k_j)) 2^(-b_j)   j <= i
 //   out_i = 2^(b_i - n_i) O_i / den_i,  den_i likewise (q'_i.z_prev + sum_j P~_ij)
@@ -21,9 +21,10 @@
 // the weight: without it products of some 2^37 left fp32. A chunk whose b all
 // lie above -16 has no such factors and keeps n_i = 0, which spares the identity
 // map its pass over Q (1x16x131072x128: sweep 467 us with the pass in every
-// chunk, 433 with the choice; the other maps pass over Q anyway). Where b_i < -90,
-// P~_ij = (q'_i.phi(k_j)) 2^(b_i + 90 - b_j), which leaves the state in front a
-// weight of 2^(-90) next to the query's own key instead of the smaller true one.
+// chunk, 433 with the choice; the other maps pass over Q anyway). Where b_i < -60,
+// P~_ij = (q'_i.phi(k_j)) 2^(b_i + 60 - b_j), which leaves the state in front a
+// weight of 2^(-60) next to the query's own key instead of the smaller true one
+// (at 2^(-90) features below 2^(-36) would leave bf16's normal range).
 
 #include "tc_gated.cuh"
 

@@ -11,8 +11,8 @@ namespace tcg {
 
 using namespace tc;
 
-// The decays of queries below 2^-90 are taken apart from the state's (tc_gated.cu).
-constexpr float kDeep = -90.f;
+// The decays of queries below 2^-60 are taken apart from the state's (tc_gated.cu).
+constexpr float kDeep = -60.f;
 
 // Brings a box of a tensor map towards L2, ahead of its load.
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {

@@ -161,3 +161,15 @@ def test_a_nan_of_either_sign_reaches_prompt_step_and_gradients(dt, d, sign, phi
         one = [x[:, :, 150:151].clone() for x in a]
         S, z = torch.zeros(1, 1, d, d, device="cuda"), torch.zeros(1, 1, d, device="cuda")
         assert bool(la.la_gated_decode_step(*one, S, z, phi=phi, normalize=normalize).isnan().all())
+
+
+@pytest.mark.parametrize("dt,d", KINDS)
+@pytest.mark.parametrize("lowest", [-50.0, -88.0, -120.0])
+def test_small_features_under_fast_gates(dt, d, lowest):
+    """Queries whose features are all some 2^-45 (elu + 1 of -31): a decay next to them must not take them out
+    of their type's range."""
+    q, k, v, g, dout = inputs(1, 2, 200, d, dt, "elu1", seed=17)
+    g.fill_(rate(dt, d, lowest))
+    q = (q - 31).clamp(max=-28)
+    check_out(dt, q, k, v, g, "elu1", True)
+    check_gradients(dt, q, k, v, g, dout, "elu1", True)

@@ -238,7 +238,7 @@ LA_API la_status la_gated_causal(const la_desc* desc, const void* q, const void*
  *   dg_t = a_t (<S_{t-1}, G_t> + z_{t-1} . h_t)     (exactly 0 for a closed gate)
  * Sums are fp32; bf16 rounds the operands of its products once. ws: op
  * LA_OP_GATED_CAUSAL_BWD (it holds a state per chunk of 64, or in fp32 with
- * d >= 64 of 32, tokens: d d elements and d floats). */
+ * d >= 64 of 32, tokens: d d + d floats). */
 LA_API la_status la_gated_causal_backward(const la_desc* desc, const void* q, const void* k,
                                           const void* v, const void* g, const void* dout, void* dq,
                                           void* dk, void* dv, void* dg, void* ws, size_t ws_bytes,

@@ -237,7 +237,7 @@ size_t gated_gate_bytes(const Problem& p) {
 // fp32 d >= 64: chunks of 32 tokens (gated_common.cuh, Shape)
 int gated_chunk(const Problem& p) { return p.dtype == DT_F32 && p.d >= 64 ? 32 : 64; }
 size_t gated_chunk_state_bytes(const Problem& p) {
-    return (size_t)p.d * p.d * p.elem_bytes() + (size_t)p.d * sizeof(float);
+    return p.state_floats() * sizeof(float);
 }
 
 cudaError_t gated_sweep(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const float* prefix,

@@ -46,41 +46,34 @@ template <typename T, int D, int PARTS, int COPIES> struct BwdSmem {
 // positive (relu + 1, elu + 1) both are dominated by the part that all
 // channels share, and what is left would carry the rounding of the whole: S
 // goes in as two bf16 parts there (relative error of dq at 2 x 8 x 4096 x 64,
-// relu + 1: 6.1e-3 with one part).
+// relu + 1: 6.1e-3 with one part). Under the identity map dg needs them: the sums
+// over a chunk's queries of phi(q) . (S dout) all carry the same rounding of S
+// (1 x 16 x 32768 x 128: dg 2.2e-3 off with one part here and one in the records
+// below, 1.7e-3 with two and fp32; that costs the sweeps 440 -> 537 and 549 -> 592 us).
 template <typename T, int D, int PHI> struct BwdQ {
-    static constexpr int PARTS = sizeof(T) == 2 && shifted<PHI> ? 2 : 1;
+    static constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
     static constexpr int COPIES = D == 128 && PARTS == 2 ? 1 : Shape<T, D>::SB;
     using Smem = BwdSmem<T, D, PARTS, COPIES>;
 };
 template <typename T, int D> using BwdKvSmem = BwdSmem<T, D, 1, Shape<T, D>::SB>;
 
-// State records between the sweeps: per chunk, the fragments of S in the
-// element type in thread order (both sweeps hold S and G in the same lanes),
-// then z in fp32.
+// State records between the sweeps, in fp32: per chunk, the fragments of S in
+// thread order (both sweeps hold S and G in the same lanes), then z. dg takes
+// <S, G> from them.
 template <typename T, int D> struct ChunkState {
     using SH = Shape<T, D>;
     static constexpr int OWN = SH::SRT * SH::SCG * 32;             // threads that hold S
-    static constexpr int VEC = SH::SN * 4 / 8 * sizeof(T) / 16;    // 16-byte vectors per thread
-    static constexpr size_t BYTES = (size_t)D * D * sizeof(T) + D * sizeof(float);
-    static_assert((size_t)OWN * VEC * 16 == (size_t)D * D * sizeof(T), "record");
+    static constexpr int VEC = SH::SN / 8;                         // 16-byte vectors per thread
+    static constexpr size_t BYTES = (size_t)(D * D + D) * sizeof(float);
+    static_assert((size_t)OWN * VEC * 16 == (size_t)D * D * sizeof(float), "record");
 
     __device__ __forceinline__ static void write(uint8_t* rec, const State<T, D>& st, const float* zs) {
         if ((int)threadIdx.x < OWN) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                uint4 u;
-                if constexpr (SH::F32) {
-                    u = make_uint4(__float_as_uint(st.S[v][0]), __float_as_uint(st.S[v][1]), __float_as_uint(st.S[v][2]),
-                                   __float_as_uint(st.S[v][3]));
-                } else {
-                    u = make_uint4(pack_bf16(st.S[2 * v][0], st.S[2 * v][1]), pack_bf16(st.S[2 * v][2], st.S[2 * v][3]),
-                                   pack_bf16(st.S[2 * v + 1][0], st.S[2 * v + 1][1]),
-                                   pack_bf16(st.S[2 * v + 1][2], st.S[2 * v + 1][3]));
-                }
-                reinterpret_cast<uint4*>(rec)[v * OWN + threadIdx.x] = u;
-            }
+            for (int v = 0; v < VEC; ++v)
+                reinterpret_cast<float4*>(rec)[v * OWN + threadIdx.x] = make_float4(st.S[v][0], st.S[v][1], st.S[v][2], st.S[v][3]);
         }
-        float* z = reinterpret_cast<float*>(rec + (size_t)D * D * sizeof(T));
+        float* z = reinterpret_cast<float*>(rec) + D * D;
         for (int a = threadIdx.x; a < D; a += SH::THREADS) z[a] = zs[a];
     }
     // Asks for the next chunk's record (d = 128, where no other CTA covers for the
@@ -97,18 +90,11 @@ template <typename T, int D> struct ChunkState {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 const uint4 u = ldg_stream(reinterpret_cast<const uint4*>(rec) + v * OWN + threadIdx.x);
-                if constexpr (SH::F32) {
-                    sum += __uint_as_float(u.x) * st.S[v][0] + __uint_as_float(u.y) * st.S[v][1] +
-                           __uint_as_float(u.z) * st.S[v][2] + __uint_as_float(u.w) * st.S[v][3];
-                } else {
-                    sum += bf16_lo(u.x) * st.S[2 * v][0] + bf16_hi(u.x) * st.S[2 * v][1] + bf16_lo(u.y) * st.S[2 * v][2] +
-                           bf16_hi(u.y) * st.S[2 * v][3];
-                    sum += bf16_lo(u.z) * st.S[2 * v + 1][0] + bf16_hi(u.z) * st.S[2 * v + 1][1] +
-                           bf16_lo(u.w) * st.S[2 * v + 1][2] + bf16_hi(u.w) * st.S[2 * v + 1][3];
-                }
+                sum += __uint_as_float(u.x) * st.S[v][0] + __uint_as_float(u.y) * st.S[v][1] +
+                       __uint_as_float(u.z) * st.S[v][2] + __uint_as_float(u.w) * st.S[v][3];
             }
         }
-        const float* z = reinterpret_cast<const float*>(rec + (size_t)D * D * sizeof(T));
+        const float* z = reinterpret_cast<const float*>(rec) + D * D;
         for (int a = threadIdx.x; a < D; a += SH::THREADS) sum += z[a] * zs[a];
         return sum;
     }
@@ -348,7 +334,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 base_frag<PHI>(b[1]);
                 mma_step(acc[2 * n], ax, b[0]);
                 mma_step(acc[2 * n + 1], ax, b[1]);
-                if constexpr (LO) {
+                if constexpr (LO && shifted<PHI>) {
                     mma_step(acc[2 * n], xl, b[0]);
                     mma_step(acc[2 * n + 1], xl, b[1]);
                 }

@@ -53,8 +53,8 @@ def slope(x, kind):
 
 def chunked(q, k, v, g, dout=None, kind="relu1", normalize=True, S0=None, z0=None, rnd=exact, bf16=True, cross=True):
     """out, or with dout (dq, dk, dv, dg), of [..., N, d] in float64 tensors.
-    bf16: the state goes into products rounded once, and in two parts where the
-    gradient kernels take two. cross = False leaves out what the chunks give
+    bf16: the state goes into the outputs' products rounded once, and into those
+    of the gradients' first sweep in two parts. cross = False leaves out what the chunks give
     to one another."""
     lead, (N, d) = q.shape[:-2], q.shape[-2:]
     q, k, v = (x.reshape(-1, N, d) for x in (q, k, v))
@@ -82,7 +82,7 @@ def chunked(q, k, v, g, dout=None, kind="relu1", normalize=True, S0=None, z0=Non
             outs.append(rnd(num / den if normalize else num))
         else:
             do = dout[:, lo:hi]
-            Sr = S if bf16 and one else rnd(S)
+            Sr = S if bf16 else rnd(S)
             dp = prod(do @ vc.transpose(1, 2))
             Sd = f * (do @ Sr.transpose(1, 2))
             num = (P * dp).sum(-1, keepdim=True) + (phi(qc, kind) * Sd).sum(-1, keepdim=True)
@@ -97,7 +97,7 @@ def chunked(q, k, v, g, dout=None, kind="relu1", normalize=True, S0=None, z0=Non
             y = rnd(Y) @ base + one * Y.sum(-1, keepdim=True) + f * z[:, None]
             dq[:, lo:hi] = rnd(up * (x - delta * y) * slope(qc, kind))
             dgp = torch.zeros_like(b) if normalize else (up * num)[..., 0].flip(-1).cumsum(-1).flip(-1)
-            parts.append((D, f, end, pq, pk, up, -delta, dgp, rnd(S), z, b[:, -1]))
+            parts.append((D, f, end, pq, pk, up, -delta, dgp, S, z, b[:, -1]))
         all_ = torch.exp(b[:, -1])
         S = all_[:, None, None] * S * cross + (end * phi(kc, kind)).transpose(1, 2) @ vc
         z = all_[:, None] * z * cross + (end * phi(kc, kind)).sum(1)

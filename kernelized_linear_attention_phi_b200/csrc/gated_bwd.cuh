@@ -130,7 +130,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     using SH = Shape<T, D>;
     using BQ = BwdQ<T, D, PHI>;
     constexpr int C = SH::C, LD = SH::LD, NT = SH::NCOL / 8;
-    constexpr bool LO = BQ::PARTS == 2;
+    constexpr bool LO = BQ::PARTS == 2, APART = !SH::F32 && PHI == PHI_RELU1;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     auto& sm = *reinterpret_cast<typename BQ::Smem*>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
@@ -199,7 +199,8 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         ChunkState<T, D>::write(states + (size_t)c * ChunkState<T, D>::BYTES, st, zs);
 
         // dout S^T, and q . z
-        float acc[NT][4] = {}, oz[4] = {};
+        using PD = PhiDot<D, PHI>;
+        float acc[NT][4] = {}, oz[4] = {}, sq[4] = {};
 #pragma unroll(SH::F32 ? 1 : D / 16)
         for (int k0 = 0; k0 < D; k0 += 16) {
             FragA<T> a;
@@ -216,13 +217,24 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                     mma_step(acc[2 * n + 1], a, b[1]);
                 }
             }
+            if (normalize || APART) {
+                load_a<LD>(a, qt, i0, k0, lane);
+                PD::rows(sq, a);
+            }
             if (normalize) {
                 FragB<T> b;
-                load_a<LD>(a, qt, i0, k0, lane);
-                phi_frag<PHI>(a);
                 load_column(b, zs, k0, lane);
-                mma_step(oz, a, b);
+                PD::column(oz, a, b);
             }
+        }
+        if (APART && normalize) {  // the ones' part, in column 0 like oz
+            float sz = 0.f;
+#pragma unroll
+            for (int x = lane; x < D; x += 32) sz += zs[x];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sz += __shfl_xor_sync(0xffffffffu, sz, o);
+            oz[0] += sz;
+            oz[2] += sz;
         }
         // q . (S dout), over this warp's columns, then over the column groups
         float s0 = 0.f, s1 = 0.f;
@@ -264,18 +276,15 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         float yk[NT][4] = {};
 #pragma unroll 1
         for (int jt = 0; jt <= rg; ++jt) {
-            float p[2][4] = {}, dp[2][4] = {};
+            float p[2][4], dp[2][4] = {};
+            PD::template start<T>(p, sq);
 #pragma unroll(SH::F32 ? 1 : D / 16)
             for (int k0 = 0; k0 < D; k0 += 16) {
                 FragA<T> a;
                 FragB<T> b[2];
                 load_a<LD>(a, qt, i0, k0, lane);
-                phi_frag<PHI>(a);
                 load_bt<LD>(b, kt, jt * 16, k0, lane);
-                phi_frag<PHI>(b[0]);
-                phi_frag<PHI>(b[1]);
-                mma_step(p[0], a, b[0]);
-                mma_step(p[1], a, b[1]);
+                PD::step(p, a, b);
                 load_a<LD>(a, gt, i0, k0, lane);
                 load_bt<LD>(b, vt, jt * 16, k0, lane);
                 mma_step(dp[0], a, b[0]);
@@ -513,12 +522,14 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         if (lane == 0) sm.dot[s & 1][warp] = dot;
 
         // keys with the queries behind the chunk: phi(k) G and v G^T + h
-        float av[NT][4] = {}, ak[NT][4] = {};
+        using PD = PhiDot<D, PHI>;
+        float av[NT][4] = {}, ak[NT][4] = {}, sk[4] = {};
 #pragma unroll(SH::F32 ? 1 : D / 16)
         for (int k0 = 0; k0 < D; k0 += 16) {
             FragA<T> a;
             FragB<T> b[2];
             load_a<LD>(a, kt, j0, k0, lane);
+            PD::rows(sk, a);
             phi_frag<PHI>(a);
 #pragma unroll
             for (int n = 0; n < NT / 2; ++n) {
@@ -566,18 +577,15 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         float ws0 = 0.f, ws1 = 0.f;  // row sums of W
 #pragma unroll 1
         for (int it = rg; it < SH::RG; ++it) {
-            float p[2][4] = {}, dp[2][4] = {};
+            float p[2][4], dp[2][4] = {};
+            PD::template start<T>(p, sk);
 #pragma unroll(SH::F32 ? 1 : D / 16)
             for (int k0 = 0; k0 < D; k0 += 16) {
                 FragA<T> a;
                 FragB<T> b[2];
                 load_a<LD>(a, kt, j0, k0, lane);
-                phi_frag<PHI>(a);
                 load_bt<LD>(b, qt, it * 16, k0, lane);
-                phi_frag<PHI>(b[0]);
-                phi_frag<PHI>(b[1]);
-                mma_step(p[0], a, b[0]);
-                mma_step(p[1], a, b[1]);
+                PD::step(p, a, b);
                 load_a<LD>(a, vt, j0, k0, lane);
                 load_bt<LD>(b, gt, it * 16, k0, lane);
                 mma_step(dp[0], a, b[0]);

@@ -169,15 +169,14 @@ template <int PHI> __device__ __forceinline__ float base_f(float x) {
     if (PHI == PHI_ELU1) return x > 0.f ? x : exp_fast(x) - 1.f;
     return x;
 }
+template <int PHI> __device__ __forceinline__ uint32_t base_pair(uint32_t w) {
+    if (PHI == PHI_RELU1) return relu_nan_x2(w);
+    if (PHI == PHI_ELU1) return pack_bf16(base_f<PHI>(bf16_lo(w)), base_f<PHI>(bf16_hi(w)));
+    return w;
+}
 template <int PHI> __device__ __forceinline__ void base_frag(FragB<__nv_bfloat16>& b) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if constexpr (PHI == PHI_RELU1) {
-            b.r[i] = relu_nan_x2(b.r[i]);
-        } else if constexpr (PHI == PHI_ELU1) {
-            b.r[i] = pack_bf16(base_f<PHI>(bf16_lo(b.r[i])), base_f<PHI>(bf16_hi(b.r[i])));
-        }
-    }
+    for (int i = 0; i < 2; ++i) b.r[i] = base_pair<PHI>(b.r[i]);
 }
 template <int PHI> __device__ __forceinline__ void base_frag(FragB<float>& b) {
 #pragma unroll
@@ -199,6 +198,95 @@ template <int PHI> __device__ __forceinline__ void phi_frag(FragB<float>& b) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) b.r[i] = phi_f<PHI>(b.r[i]);
 }
+
+// ---- phi(x) . phi(y) without phi's rounding, for the gradients ---------------------------
+// What all channels share cancels in the gradients, and 1 + x rounded to bf16 has
+// lost most of a small x by then (sigma 0.02, 2 x 4 x 500 x 64, relu + 1: dq 1.6e-2
+// off with phi as the operand, 1.7e-3 as here). relu + 1: phi = 1 + base with base
+// exact in bf16, sum (1 + b_x)(1 + b_y) = D + sum b_x + sum b_y + sum b_x b_y, the
+// ones as an operand. elu + 1 (whose 1 + base would lose the small phi of far
+// negative x): phi in two bf16 parts. fp32 holds phi as it is.
+template <int D, int PHI> struct PhiDot {
+    // the rows' part, ones(phi(x)): added up by `rows` from every raw A operand of x; phi(x) . z with z a
+    // load_column and sz the sum of z
+    template <typename T> __device__ __forceinline__ static void rows(float (&s)[4], const FragA<T>& x) {
+        if constexpr (sizeof(T) == 2 && PHI == PHI_RELU1) {
+            FragA<T> a = x;
+            const FragB<T> ones{{0x3f803f80u, 0x3f803f80u}};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a.r[i] = base_pair<PHI>(a.r[i]);
+            mma_step(s, a, ones);
+        }
+    }
+    // p before the products: two accumulators of 8 columns
+    template <typename T> __device__ __forceinline__ static void start(float (&p)[2][4], const float (&s)[4]) {
+        constexpr bool APART = sizeof(T) == 2 && PHI == PHI_RELU1;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            p[n][0] = p[n][1] = APART ? s[0] + D : 0.f;
+            p[n][2] = p[n][3] = APART ? s[2] + D : 0.f;
+        }
+    }
+    // p += the products of one step's raw operands
+    __device__ __forceinline__ static void step(float (&p)[2][4], FragA<float> a, FragB<float> (&b)[2]) {
+        phi_frag<PHI>(a);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            phi_frag<PHI>(b[n]);
+            mma_step(p[n], a, b[n]);
+        }
+    }
+    __device__ __forceinline__ static void step(float (&p)[2][4], FragA<__nv_bfloat16> a, FragB<__nv_bfloat16> (&b)[2]) {
+        if constexpr (PHI == PHI_ELU1) {
+            FragA<__nv_bfloat16> lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_phi(a.r[i], a.r[i], lo.r[i]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                FragB<__nv_bfloat16> bl;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) split_phi(b[n].r[i], b[n].r[i], bl.r[i]);
+                mma_step(p[n], lo, b[n]);
+                mma_step(p[n], a, bl);
+                mma_step(p[n], a, b[n]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a.r[i] = base_pair<PHI>(a.r[i]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                base_frag<PHI>(b[n]);
+                if constexpr (PHI == PHI_RELU1) {
+                    const FragA<__nv_bfloat16> ones{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}};
+                    mma_step(p[n], ones, b[n]);
+                }
+                mma_step(p[n], a, b[n]);
+            }
+        }
+    }
+    // s += phi(x) z (relu + 1: without the ones' part, the sum of z)
+    __device__ __forceinline__ static void column(float (&s)[4], FragA<float> x, const FragB<float>& z) {
+        phi_frag<PHI>(x);
+        mma_step(s, x, z);
+    }
+    __device__ __forceinline__ static void column(float (&s)[4], FragA<__nv_bfloat16> x, const FragB<__nv_bfloat16>& z) {
+        if constexpr (PHI == PHI_ELU1) {
+            FragA<__nv_bfloat16> lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_phi(x.r[i], x.r[i], lo.r[i]);
+            mma_step(s, lo, z);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x.r[i] = base_pair<PHI>(x.r[i]);
+        }
+        mma_step(s, x, z);
+    }
+    __device__ __forceinline__ static void split_phi(uint32_t w, uint32_t& hi, uint32_t& lo) {
+        const float x = phi_f<PHI>(bf16_lo(w)), y = phi_f<PHI>(bf16_hi(w));
+        hi = pack_bf16(x, y);
+        lo = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+    }
+};
 
 // ---- operands from shared-memory tiles [rows][LD] --------------------------------------
 // LD is 16 bytes (bf16) or 32 bytes (fp32) more than the row, so the 8 rows an

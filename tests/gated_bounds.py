@@ -75,7 +75,11 @@ def chunked(q, k, v, g, dout=None, kind="relu1", normalize=True, S0=None, z0=Non
         D = torch.exp((b[:, :, None] - b[:, None, :]).tril()).tril()
         f, end = torch.exp(b)[..., None], torch.exp(b[:, -1:] - b)[..., None]
         pq, pk = rnd(phi(qc, kind)), rnd(phi(kc, kind))
-        P = D * prod(pq @ pk.transpose(1, 2))
+        if dout is not None and bf16:  # the gradients take phi in two parts here
+            pq = phi(qc, kind)
+            P = D * (pq @ phi(kc, kind).transpose(1, 2))
+        else:
+            P = D * prod(pq @ pk.transpose(1, 2))
         if dout is None:
             W, Sr = rnd(P), rnd(S)
             num, den = W @ vc + f * (pq @ Sr), W.sum(-1, keepdim=True) + f * (pq @ z[..., None])
@@ -112,7 +116,7 @@ def chunked(q, k, v, g, dout=None, kind="relu1", normalize=True, S0=None, z0=Non
         ak = end * (vc @ Gr.transpose(1, 2) + h[:, None])
         av = end * (pk @ Gr)
         W = D * up
-        qk = prod(pq @ pk.transpose(1, 2))
+        qk = pq @ phi(kc, kind).transpose(1, 2) if bf16 else prod(pq @ pk.transpose(1, 2))
         pw, dw = W * qk, W * (prod(do @ vc.transpose(1, 2)) + col)
         base = rnd(phi(qc, kind) - one) if kind != "relu1" or not bf16 else phi(qc, kind) - one
         dv[:, lo:hi] = rnd(av + rnd(pw).transpose(1, 2) @ do)

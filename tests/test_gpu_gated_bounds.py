@@ -188,3 +188,13 @@ def test_dg_does_not_carry_the_roundings_of_the_state(shape, span):
         got = la.la_gated_causal_backward(q, k, v, g, dout, phi="identity", normalize=False)
         off = float((got[3].double() - ref[3]).norm() / (like[3] - ref[3]).norm())
         assert off <= 1.25, (seed, off)
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("phi", ["relu1", "elu1"])
+@pytest.mark.parametrize("sigma", [0.1, 0.02])
+def test_small_queries_and_keys_keep_their_digits_in_dq(d, phi, sigma):
+    """Features next to 1: dq is what is left of sums that all channels share, and 1 + x rounded to bf16
+    would have lost most of x."""
+    q, k, v, g, dout = inputs(1, 4, 500, d, "bf16", phi, seed=19, sigma=sigma)
+    check_gradients("bf16", q, k, v, g, dout, phi, True)

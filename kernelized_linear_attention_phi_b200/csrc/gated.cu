@@ -253,16 +253,16 @@ cudaError_t gated_states(const Problem& p, bool reverse, const void* x, const vo
     return f(p, reverse, x, y, gates, up, col, block_tokens, nblk, blk0, count, exact, rec, dec, st);
 }
 cudaError_t gated_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                        const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+                        const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* own, float* dgp,
                         void* chunk_state, cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_bwd_q_t<float> : gated_bwd_q_t<__nv_bfloat16>;
-    return f(p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, up, col, dgp, chunk_state, st);
+    return f(p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, up, col, own, dgp, chunk_state, st);
 }
 cudaError_t gated_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates, const void* dout,
                          const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
-                         const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
+                         const float* own, const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     auto* f = p.dtype == DT_F32 ? gated_bwd_kv_t<float> : gated_bwd_kv_t<__nv_bfloat16>;
-    return f(p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, up, col, dgp, chunk_state, dk, dv, dg, st);
+    return f(p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, up, col, own, dgp, chunk_state, dk, dv, dg, st);
 }
 
 }  // namespace la

@@ -53,16 +53,17 @@ cudaError_t gated_decode(const Problem& p, const void* q, const void* k, const v
                          const float* z, float* S_out, float* z_out, void* out, cudaStream_t st);
 
 // Gradients, first sweep (chunks in order): dq, and per token (normalized only)
-// up = 1 / den and col = -(out . dout); dgp (what the chunk's queries give to
+// up = 1 / den, col = -(out . dout) and own = up (dout.v + col), the query's own
+// key's; dgp (what the chunk's queries give to
 // dg), and per chunk of gated_chunk(p) tokens the state in front of it
 // (chunk_state, gated_chunk_state_bytes(p) each).
 cudaError_t gated_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                        const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+                        const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* own, float* dgp,
                         void* chunk_state, cudaStream_t st);
 // Second sweep (chunks in reverse): dk, dv, dg from the states behind the blocks.
 cudaError_t gated_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates, const void* dout,
                          const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
-                         const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st);
+                         const float* own, const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st);
 int gated_chunk(const Problem& p);
 size_t gated_chunk_state_bytes(const Problem& p);
 
@@ -77,12 +78,12 @@ cudaError_t gated_states_t(const Problem& p, bool reverse, const void* x, const 
                            cudaStream_t st);
 template <typename T>
 cudaError_t gated_bwd_q_t(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                          const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+                          const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* own, float* dgp,
                           void* chunk_state, cudaStream_t st);
 template <typename T>
 cudaError_t gated_bwd_kv_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates, const void* dout,
                            const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
-                           const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st);
+                           const float* own, const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st);
 
 namespace gated {
 // Calls f(integral_constant<D>, integral_constant<PHI>) for p.

@@ -20,6 +20,12 @@
 // registers). delta_i comes out of the same pass over the keys as dq, since
 //   dq_i = phi'(q_i) up_i [ X_i + e^{b_i} S dout_i - delta_i (Y_i + e^{b_i} z) ],
 //   X_i = sum_j e^{b_i - b_j} (dout_i.v_j) phi(k_j),  Y_i = sum_j e^{b_i - b_j} phi(k_j).
+// A query's own key (j = i) is left out of these sums and of dg's and added in
+// fp32 as up_i (dout_i.v_i - delta_i) phi(k_i): under fast gates its weight is all
+// but 1, the difference is formed from the sums of the other keys, and what
+// would have to cancel in dg (W_ii, in the sum over i and in the one over j)
+// is in neither. A normalized output makes the row sum of W 0, so that the others'
+// is -W_ii.
 #pragma once
 
 #include "gated.h"
@@ -37,7 +43,7 @@ template <typename T, int D, int PARTS, int COPIES> struct BwdSmem {
     float zs[COPIES][D];
     Gates<SH::C> gates[2];
     float row[2][SH::CG][SH::C];     // per token sums for dg
-    float sum[2][SH::C];             // the keys' sums of W
+    float sum[2][SH::C];             // the keys' sums of W over the queries behind
     float part[SH::CG][SH::C];
     float dot[2][SH::NW];
 };
@@ -125,7 +131,7 @@ template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                    const uint8_t* __restrict__ gates, const T* __restrict__ dout, const float* prefix, int N, int block_tokens, int nblk, int normalize,
-                   T* __restrict__ dq, float* __restrict__ up, float* __restrict__ col, float* __restrict__ dgp,
+                   T* __restrict__ dq, float* __restrict__ up, float* __restrict__ col, float* __restrict__ own, float* __restrict__ dgp,
                    uint8_t* __restrict__ chunk_state) {
     using SH = Shape<T, D>;
     using BQ = BwdQ<T, D, PHI>;
@@ -146,7 +152,7 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 
     auto fetch = [&](int c) {
         const int row0 = first + c * C;
-        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, row0, N);
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, nullptr, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][2], v, row0, N);
@@ -265,9 +271,10 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         const bool deep = gs.deep;
         const float f0 = gs.from_start[i0 + g], f1 = gs.from_start[i0 + g + 8];
         const float hi0 = gs.hi[i0 + g], lo0 = gs.lo[i0 + g], hi1 = gs.hi[i0 + g + 8], lo1 = gs.lo[i0 + g + 8];
-        // per row, over all keys so far: den = q . z and so on, num = sum of weights times dout . v
+        // per row, over all keys in front: den = q . z and so on, num = sum of weights times dout . v
         float den0 = t == 0 ? f0 * (oz[0] + oz[1]) : 0.f, den1 = t == 0 ? f1 * (oz[2] + oz[3]) : 0.f;
         float num0 = 0.f, num1 = 0.f;
+        float pd0 = 0.f, pd1 = 0.f, dd0 = 0.f, dd1 = 0.f;  // the own key's weight and dout . v
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             acc[n][0] *= f0; acc[n][1] *= f0; acc[n][2] *= f1; acc[n][3] *= f1;
@@ -307,8 +314,10 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
                 if (jt == rg) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (jl + e > g) w[n][e] = 0.f;
-                        if (jl + e > g + 8) w[n][2 + e] = 0.f;
+                        if (jl + e == g) pd0 = p[n][e], dd0 = dp[n][e];
+                        if (jl + e == g + 8) pd1 = p[n][2 + e], dd1 = dp[n][2 + e];
+                        if (jl + e >= g) w[n][e] = 0.f;
+                        if (jl + e >= g + 8) w[n][2 + e] = 0.f;
                     }
                 }
 #pragma unroll
@@ -358,48 +367,61 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         // the state's part of num: q . (S dout)
         num0 = quad_sum(num0) + s0 * f0;
         num1 = quad_sum(num1) + s1 * f1;
+        pd0 = quad_sum(pd0);
+        pd1 = quad_sum(pd1);
+        dd0 = quad_sum(dd0);
+        dd1 = quad_sum(dd1);
         float up0 = 1.f, up1 = 1.f, de0 = 0.f, de1 = 0.f;
+        // dd - de, and the row sum of W over the keys in front
+        float df0 = dd0, df1 = dd1, rw0 = num0, rw1 = num1;
         const int row = first + c * C + i0 + g;
         if (normalize) {
-            up0 = 1.f / den0;
-            up1 = 1.f / den1;
-            de0 = num0 * up0;  // out . dout
-            de1 = num1 * up1;
+            up0 = 1.f / (den0 + pd0);
+            up1 = 1.f / (den1 + pd1);
+            de0 = fmaf(pd0, dd0, num0) * up0;  // out . dout
+            de1 = fmaf(pd1, dd1, num1) * up1;
+            df0 = pd0 > den0 ? (dd0 * den0 - num0) * up0 : dd0 - de0;
+            df1 = pd1 > den1 ? (dd1 * den1 - num1) * up1 : dd1 - de1;
+            rw0 = -pd0 * up0 * df0;
+            rw1 = -pd1 * up1 * df1;
             if (cg == 0 && t == 0) {
                 if (row < end) {
                     up[toff + row] = up0;
                     col[toff + row] = -de0;
+                    own[toff + row] = up0 * df0;
                 }
                 if (row + 8 < end) {
                     up[toff + row + 8] = up1;
                     col[toff + row + 8] = -de1;
+                    own[toff + row + 8] = up1 * df1;
                 }
             }
         }
         if (cg == 0 && t == 0) {
-            // the row sum of W with the part with earlier keys: phi(q) . dphi(q),
-            // which a normalized output makes 0
-            sm.row[c & 1][0][i0 + g] = !normalize && row < end ? up0 * num0 : 0.f;
-            sm.row[c & 1][0][i0 + g + 8] = !normalize && row + 8 < end ? up1 * num1 : 0.f;
+            sm.row[c & 1][0][i0 + g] = row < end ? rw0 : 0.f;
+            sm.row[c & 1][0][i0 + g + 8] = row + 8 < end ? rw1 : 0.f;
         }
         xs0 = shifted<PHI> ? quad_sum(xs0) - de0 * quad_sum(ys0) : 0.f;
         xs1 = shifted<PHI> ? quad_sum(xs1) - de1 * quad_sum(ys1) : 0.f;
         const float dz0 = de0 * f0, dz1 = de1 * f1;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float x, y;
+            float x, y, kx, ky;
             const float2 z = *reinterpret_cast<const float2*>(zs + col0 + 8 * n + 2 * t);
-            const T* qp = qt + (i0 + g) * LD + col0 + 8 * n + 2 * t;
+            const int at = (i0 + g) * LD + col0 + 8 * n + 2 * t;
+            const T *qp = qt + at, *kp = kt + at;
             T* o = dq + (size_t)row * D + col0 + 8 * n + 2 * t;
             if (row < end) {
                 load_pair(qp, x, y);
-                store_pair(o, up0 * (acc[n][0] + xs0 - de0 * yk[n][0] - dz0 * z.x) * slope_f<PHI>(x),
-                           up0 * (acc[n][1] + xs0 - de0 * yk[n][1] - dz0 * z.y) * slope_f<PHI>(y));
+                load_pair(kp, kx, ky);
+                store_pair(o, up0 * (acc[n][0] + xs0 - de0 * yk[n][0] - dz0 * z.x + df0 * phi_f<PHI>(kx)) * slope_f<PHI>(x),
+                           up0 * (acc[n][1] + xs0 - de0 * yk[n][1] - dz0 * z.y + df0 * phi_f<PHI>(ky)) * slope_f<PHI>(y));
             }
             if (row + 8 < end) {
                 load_pair(qp + 8 * LD, x, y);
-                store_pair(o + 8 * D, up1 * (acc[n][2] + xs1 - de1 * yk[n][2] - dz1 * z.x) * slope_f<PHI>(x),
-                           up1 * (acc[n][3] + xs1 - de1 * yk[n][3] - dz1 * z.y) * slope_f<PHI>(y));
+                load_pair(kp + 8 * LD, kx, ky);
+                store_pair(o + 8 * D, up1 * (acc[n][2] + xs1 - de1 * yk[n][2] - dz1 * z.x + df1 * phi_f<PHI>(kx)) * slope_f<PHI>(x),
+                           up1 * (acc[n][3] + xs1 - de1 * yk[n][3] - dz1 * z.y + df1 * phi_f<PHI>(ky)) * slope_f<PHI>(y));
             }
         }
         if (c + 1 < nch) {
@@ -420,7 +442,7 @@ template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,
                     const uint8_t* __restrict__ gates, const T* __restrict__ dout, const float* suffix, int N, int block_tokens, int nblk,
-                    const float* up, const float* col, const float* __restrict__ dgp,
+                    const float* up, const float* col, const float* own, const float* __restrict__ dgp,
                     const uint8_t* __restrict__ chunk_state, T* __restrict__ dk, T* __restrict__ dv, T* __restrict__ dg) {
     using SH = Shape<T, D>;
     constexpr int C = SH::C, LD = SH::LD, NT = SH::NCOL / 8;
@@ -439,6 +461,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     if (up) {
         up += toff;
         col += toff;
+        own += toff;
     }
     const uint8_t* states = chunk_state + ((size_t)bh * ((N + C - 1) / C) + first / C) * ChunkState<T, D>::BYTES;
     pdl_wait();
@@ -446,7 +469,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     // step s of the sweep is chunk nch - 1 - s
     auto fetch = [&](int s) {
         const int row0 = first + (nch - 1 - s) * C;
-        load_gates<C>(sm.gates[s & 1], gates + (size_t)(nch - 1 - s) * kGateBytes<C>, up, col, row0, N);
+        load_gates<C>(sm.gates[s & 1], gates + (size_t)(nch - 1 - s) * kGateBytes<C>, up, col, own, row0, N);
         load_tile<SH, T, D>(sm.tiles[s % SH::ST][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[s % SH::ST][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[s % SH::ST][2], v, row0, N);
@@ -548,6 +571,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
         const bool deep = gs.deep;
         const float e0 = gs.to_end[j0 + g], e1 = gs.to_end[j0 + g + 8];
         const float inv0 = gs.inv[j0 + g], inv1 = gs.inv[j0 + g + 8];
+        const float own0 = up ? gs.own[j0 + g] : 0.f, own1 = up ? gs.own[j0 + g + 8] : 0.f;
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -574,7 +598,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 
         const float hi0 = gs.hi[j0 + g], lo0 = gs.lo[j0 + g], hi1 = gs.hi[j0 + g + 8], lo1 = gs.lo[j0 + g + 8];
         float rs0 = 0.f, rs1 = 0.f;  // row sums of the pairs' gradients, for the shift of phi(q)
-        float ws0 = 0.f, ws1 = 0.f;  // row sums of W
+        float ws0 = 0.f, ws1 = 0.f;  // row sums of W, own queries apart
 #pragma unroll 1
         for (int it = rg; it < SH::RG; ++it) {
             float p[2][4], dp[2][4] = {};
@@ -620,8 +644,10 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
+                    const bool self = it == rg && il + (e & 1) == (e < 2 ? g : g + 8);  // the key's own query
                     dp[n][e] = w[e] * (dp[n][e] + (e & 1 ? cl.y : cl.x));
-                    (e < 2 ? ws0 : ws1) += p[n][e] * dp[n][e];
+                    if (self && up) dp[n][e] = e < 2 ? own0 : own1;
+                    (e < 2 ? ws0 : ws1) += self ? 0.f : p[n][e] * dp[n][e];
                     (e < 2 ? rs0 : rs1) += dp[n][e];
                     p[n][e] *= w[e];
                 }
@@ -682,7 +708,7 @@ gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
 
 template <typename T, int D, int PHI>
 cudaError_t launch_bwd_q(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                         const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+                         const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* own, float* dgp,
                          void* chunk_state, cudaStream_t st) {
     constexpr size_t smem = sizeof(typename BwdQ<T, D, PHI>::Smem);
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -691,20 +717,20 @@ cudaError_t launch_bwd_q(const Problem& p, const void* q, const void* k, const v
     return launch_pdl(gated_bwd_q_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
                       smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
                       gates, static_cast<const T*>(dout), prefix, p.N, block_tokens, nblk,
-                      p.normalize, static_cast<T*>(dq), up, col, dgp, static_cast<uint8_t*>(chunk_state));
+                      p.normalize, static_cast<T*>(dq), up, col, own, dgp, static_cast<uint8_t*>(chunk_state));
 }
 
 template <typename T, int D, int PHI>
 cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates,
                           const void* dout, const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
-                          const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
+                          const float* own, const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     constexpr size_t smem = sizeof(BwdKvSmem<T, D>);
     static_assert(smem <= 227 * 1024, "shared memory");
     const cudaError_t e = ensure_smem<gated_bwd_kv_kernel<T, D, PHI>>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(gated_bwd_kv_kernel<T, D, PHI>, dim3((unsigned)nblk, (unsigned)p.bh()), dim3(Shape<T, D>::THREADS),
                       smem, st, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-                      static_cast<const T*>(g), gates, static_cast<const T*>(dout), suffix, p.N, block_tokens, nblk, up, col, dgp,
+                      static_cast<const T*>(g), gates, static_cast<const T*>(dout), suffix, p.N, block_tokens, nblk, up, col, own, dgp,
                       static_cast<const uint8_t*>(chunk_state), static_cast<T*>(dk), static_cast<T*>(dv),
                       static_cast<T*>(dg));
 }
@@ -713,20 +739,20 @@ cudaError_t launch_bwd_kv(const Problem& p, const void* q, const void* k, const 
 
 template <typename T>
 cudaError_t gated_bwd_q_t(const Problem& p, const void* q, const void* k, const void* v, const uint8_t* gates, const void* dout,
-                          const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* dgp,
+                          const float* prefix, int block_tokens, int nblk, void* dq, float* up, float* col, float* own, float* dgp,
                           void* chunk_state, cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
         return gated::launch_bwd_q<T, decltype(d)::value, decltype(phi)::value>(
-            p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, up, col, dgp, chunk_state, st);
+            p, q, k, v, gates, dout, prefix, block_tokens, nblk, dq, up, col, own, dgp, chunk_state, st);
     });
 }
 template <typename T>
 cudaError_t gated_bwd_kv_t(const Problem& p, const void* q, const void* k, const void* v, const void* g, const uint8_t* gates,
                            const void* dout, const float* suffix, int block_tokens, int nblk, const float* up, const float* col,
-                           const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
+                           const float* own, const float* dgp, const void* chunk_state, void* dk, void* dv, void* dg, cudaStream_t st) {
     return gated::dispatch(p, [&](auto d, auto phi) {
         return gated::launch_bwd_kv<T, decltype(d)::value, decltype(phi)::value>(
-            p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, up, col, dgp, chunk_state, dk, dv, dg, st);
+            p, q, k, v, g, gates, dout, suffix, block_tokens, nblk, up, col, own, dgp, chunk_state, dk, dv, dg, st);
     });
 }
 

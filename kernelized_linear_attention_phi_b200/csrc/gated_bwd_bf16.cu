@@ -6,9 +6,9 @@ namespace la {
 
 template cudaError_t gated_bwd_q_t<__nv_bfloat16>(
     const Problem&, const void*, const void*, const void*, const uint8_t*, const void*, const float*, int, int, void*, float*,
-    float*, float*, void*, cudaStream_t);
+    float*, float*, float*, void*, cudaStream_t);
 template cudaError_t gated_bwd_kv_t<__nv_bfloat16>(
     const Problem&, const void*, const void*, const void*, const void*, const uint8_t*, const void*, const float*, int, int,
-    const float*, const float*, const float*, const void*, void*, void*, void*, cudaStream_t);
+    const float*, const float*, const float*, const float*, const void*, void*, void*, void*, cudaStream_t);
 
 }  // namespace la

@@ -68,17 +68,18 @@ template <int C> struct alignas(16) Gates {
     float to_end[C];      // 2^(b_last - b_j); 0 past the last token
     float all;            // 2^b_last
     int deep, pad[2];
-    float up[C], col[C];  // second sweep, normalized: 1 / den_i and -(out_i . dout_i); 0 past the last token
+    // second sweep, normalized: 1 / den_i, -(out_i . dout_i) and (dout_i.v_i + col_i) / den_i; 0 past the last token
+    float up[C], col[C], own[C];
 };
 template <int C> constexpr int kGateBytes = (5 * C + 4) * 4;  // of a chunk's record in global memory
 constexpr float kDeep = 90.f;
-// Starts the copy of a chunk's gates; with up (the second sweep of a normalized
-// call: up, col of the head, from row0 on) those too.
+// Starts the copy of a chunk's gates; with up (a normalized call: up, col and,
+// where the second sweep takes it, own of the head, from row0 on) those too.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 template <int C>
-__device__ __forceinline__ void load_gates(Gates<C>& s, const uint8_t* rec, const float* up, const float* col, int row0, int N) {
+__device__ __forceinline__ void load_gates(Gates<C>& s, const uint8_t* rec, const float* up, const float* col, const float* own, int row0, int N) {
     static_assert(offsetof(Gates<C>, up) == kGateBytes<C>, "record");
     const int u = threadIdx.x;
     if (u < kGateBytes<C> / 16) cp_async16(reinterpret_cast<uint8_t*>(&s) + u * 16, rec + u * 16, true);
@@ -87,6 +88,7 @@ __device__ __forceinline__ void load_gates(Gates<C>& s, const uint8_t* rec, cons
         const int i = in ? row0 + u : 0;
         cp_async4(s.up + u, up + i, in);
         cp_async4(s.col + u, col + i, in);
+        if (own) cp_async4(s.own + u, own + i, in);
     }
 }
 

@@ -54,7 +54,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 
     auto fetch = [&](int c) {
         const int row0 = first + c * C;
-        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, row0, N);
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)c * kGateBytes<C>, nullptr, nullptr, nullptr, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], q, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], k, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][2], v, row0, N);
@@ -230,7 +230,7 @@ gated_state_kernel(const T* __restrict__ x, const T* __restrict__ y, const uint8
     auto chunk = [&](int c) { return REVERSE ? nch - 1 - c : c; };
     auto fetch = [&](int c) {
         const int row0 = first + chunk(c) * C;
-        load_gates<C>(sm.gates[c & 1], gates + (size_t)chunk(c) * kGateBytes<C>, up, col, row0, N);
+        load_gates<C>(sm.gates[c & 1], gates + (size_t)chunk(c) * kGateBytes<C>, up, col, nullptr, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][0], x, row0, N);
         load_tile<SH, T, D>(sm.tiles[c % SH::ST][1], y, row0, N);
         cp_async_commit();

@@ -92,7 +92,7 @@ int prefix_nbins(const Problem& p, int kchunk) { return p.N / kchunk + 1; }
 struct WsLayout {
     size_t part = 0, sz = 0, perm = 0, msort = 0, bins = 0, total = 0;
     size_t grec = 0, gtot = 0, gn = 0, gden = 0;  // gradients
-    size_t dec = 0, gates = 0, up = 0, col = 0, dgp = 0, chunks = 0;  // gated forms
+    size_t dec = 0, gates = 0, up = 0, col = 0, own = 0, dgp = 0, chunks = 0;  // gated forms
 };
 
 WsLayout ws_layout(const Problem& p, int op) {
@@ -173,6 +173,8 @@ WsLayout ws_layout(const Problem& p, int op) {
             L.up = off;
             off = round_up(off + tokens, kAlign);
             L.col = off;
+            off = round_up(off + tokens, kAlign);
+            L.own = off;
             off = round_up(off + tokens, kAlign);
             L.dgp = off;
             off = round_up(off + tokens, kAlign);
@@ -669,6 +671,7 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
     LA_TRY(cuda_status(gated_gates(p, g, gates, st)));
     float* up = p.normalize ? at<float>(ws, L.up) : nullptr;
     float* col = p.normalize ? at<float>(ws, L.col) : nullptr;
+    float* own = p.normalize ? at<float>(ws, L.own) : nullptr;
     float* dgp = at<float>(ws, L.dgp);
     void* chunks = at<char>(ws, L.chunks);
     float *part = nullptr, *dec = nullptr;
@@ -687,7 +690,7 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
                                         bp.nblk - 1, false, part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, false, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
-    LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, gates, dout, part, bp.block_tokens, bp.nblk, dq, up, col, dgp, chunks,
+    LA_TRY(cuda_status(gated_bwd_q(p, q, k, v, gates, dout, part, bp.block_tokens, bp.nblk, dq, up, col, own, dgp, chunks,
                                    st)));
     if (bp.nblk > 1) {  // the same records, from the other end
         if (tcs)
@@ -698,7 +701,7 @@ la_status la_gated_causal_backward(const la_desc* desc, const void* q, const voi
                                         part, dec, st)));
         LA_TRY(cuda_status(gated_scan(p, true, part, dec, bp.nblk, nullptr, nullptr, nullptr, nullptr, st)));
     }
-    return cuda_status(gated_bwd_kv(p, q, k, v, g, gates, dout, part, bp.block_tokens, bp.nblk, up, col, dgp, chunks,
+    return cuda_status(gated_bwd_kv(p, q, k, v, g, gates, dout, part, bp.block_tokens, bp.nblk, up, col, own, dgp, chunks,
                                     dk, dv, dg, st));
 }
 

@@ -89,19 +89,25 @@ def chunked(q, k, v, g, dout=None, kind="relu1", normalize=True, S0=None, z0=Non
             Sr = S if bf16 else rnd(S)
             dp = prod(do @ vc.transpose(1, 2))
             Sd = f * (do @ Sr.transpose(1, 2))
-            num = (P * dp).sum(-1, keepdim=True) + (phi(qc, kind) * Sd).sum(-1, keepdim=True)
-            up, delta = torch.ones_like(num), torch.zeros_like(num)
+            # a query's own key apart: with fast gates its weight is all but 1, and what counts is the rest
+            own, val = (x.diagonal(dim1=1, dim2=2)[..., None] for x in (P, dp))
+            Px, Dx = P.tril(-1), D.tril(-1)
+            num = (Px * dp).sum(-1, keepdim=True) + (phi(qc, kind) * Sd).sum(-1, keepdim=True)
+            den = Px.sum(-1, keepdim=True) + f * (pq @ z[..., None])
+            up, delta, diff, row = torch.ones_like(num), torch.zeros_like(num), val, num
             if normalize:
-                up = 1 / (P.sum(-1, keepdim=True) + f * (pq @ z[..., None]))
-                delta = num * up
+                up = 1 / (den + own)
+                delta = (num + own * val) * up
+                diff = torch.where(own * up > 0.5, (val * den - num) * up, val - delta)
+                row = -own * up * diff
             base = rnd(phi(kc, kind) - one) if kind != "relu1" or not bf16 else phi(kc, kind) - one
-            X, Y = D * dp, D
+            X, Y = Dx * dp, Dx
             Xr = X if bf16 and one else rnd(X)
             x = Xr @ base + one * X.sum(-1, keepdim=True) + Sd
             y = rnd(Y) @ base + one * Y.sum(-1, keepdim=True) + f * z[:, None]
-            dq[:, lo:hi] = rnd(up * (x - delta * y) * slope(qc, kind))
-            dgp = torch.zeros_like(b) if normalize else (up * num)[..., 0].flip(-1).cumsum(-1).flip(-1)
-            parts.append((D, f, end, pq, pk, up, -delta, dgp, S, z, b[:, -1]))
+            dq[:, lo:hi] = rnd(up * (x - delta * y + diff * phi(kc, kind)) * slope(qc, kind))
+            dgp = row[..., 0].flip(-1).cumsum(-1).flip(-1)
+            parts.append((D, f, end, pq, pk, up, -delta, up * diff, dgp, S, z, b[:, -1]))
         all_ = torch.exp(b[:, -1])
         S = all_[:, None, None] * S * cross + (end * phi(kc, kind)).transpose(1, 2) @ vc
         z = all_[:, None] * z * cross + (end * phi(kc, kind)).sum(1)
@@ -110,7 +116,7 @@ def chunked(q, k, v, g, dout=None, kind="relu1", normalize=True, S0=None, z0=Non
     if dout is None:
         return torch.cat(outs, 1).reshape(*lead, N, d)
     G, h = torch.zeros_like(S), torch.zeros_like(z)
-    for (lo, hi), (D, f, end, pq, pk, up, col, dgp, Sf, zf, last) in zip(spans[::-1], parts[::-1]):
+    for (lo, hi), (D, f, end, pq, pk, up, col, own, dgp, Sf, zf, last) in zip(spans[::-1], parts[::-1]):
         qc, kc, vc, do = q[:, lo:hi], k[:, lo:hi], v[:, lo:hi], dout[:, lo:hi]
         Gr, all_ = rnd(G), torch.exp(last)
         ak = end * (vc @ Gr.transpose(1, 2) + h[:, None])
@@ -118,10 +124,11 @@ def chunked(q, k, v, g, dout=None, kind="relu1", normalize=True, S0=None, z0=Non
         W = D * up
         qk = pq @ phi(kc, kind).transpose(1, 2) if bf16 else prod(pq @ pk.transpose(1, 2))
         pw, dw = W * qk, W * (prod(do @ vc.transpose(1, 2)) + col)
+        dw = dw.tril(-1) + torch.diag_embed(own[..., 0])
         base = rnd(phi(qc, kind) - one) if kind != "relu1" or not bf16 else phi(qc, kind) - one
         dv[:, lo:hi] = rnd(av + rnd(pw).transpose(1, 2) @ do)
         dk[:, lo:hi] = rnd((ak + rnd(dw).transpose(1, 2) @ base + one * dw.sum(1)[..., None]) * slope(kc, kind))
-        inside = (dw * qk).sum(1)
+        inside = (dw * qk).tril(-1).sum(1)
         earlier = (phi(kc, kind) * ak).sum(-1)
         outside = all_ * ((Sf * G).sum((1, 2)) + (zf * h).sum(1))
         x = dgp - inside.flip(-1).cumsum(-1).flip(-1) + (earlier.cumsum(-1) - earlier) + outside[:, None]

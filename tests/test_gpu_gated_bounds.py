@@ -198,3 +198,14 @@ def test_small_queries_and_keys_keep_their_digits_in_dq(d, phi, sigma):
     would have lost most of x."""
     q, k, v, g, dout = inputs(1, 4, 500, d, "bf16", phi, seed=19, sigma=sigma)
     check_gradients("bf16", q, k, v, g, dout, phi, True)
+
+
+@pytest.mark.parametrize("dt,d", KINDS)
+@pytest.mark.parametrize("phi,normalize", MODES)
+@pytest.mark.parametrize("gate", [-4.0, -8.0, -14.0])
+def test_gradients_under_gates_that_keep_little(dt, d, phi, normalize, gate):
+    """Every gate lets through 2 % to a millionth: dg (and dq, dk of a normalized output) are small next to
+    what each token has with itself, and come from the pairs of different tokens alone."""
+    q, k, v, g, dout = inputs(1, 2, 150, d, dt, phi, seed=20)
+    g.fill_(gate)
+    check_gradients(dt, q, k, v, g, dout, phi, normalize)

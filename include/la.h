@@ -236,7 +236,8 @@ LA_API la_status la_gated_causal(const la_desc* desc, const void* q, const void*
  *   dq_i = phi'(q_i) * (S_i gn_i + z_i gden_i)
  *   dk_j = phi'(k_j) * (G_j v_j + h_j),  dv_j = G_j^T phi(k_j)
  *   dg_t = a_t (<S_{t-1}, G_t> + z_{t-1} . h_t)     (exactly 0 for a closed gate)
- * Sums are fp32; bf16 rounds the operands of its products once. ws: op
+ * Sums and states are fp32; bf16 rounds the operands of its products once, but for
+ * phi(q).phi(k) and the state in front of a chunk, which go in whole or in two parts. ws: op
  * LA_OP_GATED_CAUSAL_BWD (it holds a state per chunk of 64, or in fp32 with
  * d >= 64 of 32, tokens: d d + d floats). */
 LA_API la_status la_gated_causal_backward(const la_desc* desc, const void* q, const void* k,
@@ -286,7 +287,8 @@ LA_API la_status la_qk_norm_rope(const la_rope_desc* desc, const void* q, const 
                                  const int32_t* positions, void* q_out, void* k_out, void* stream);
 
 /* Gradients: dq, dk by strides (they may lie in one packed buffer; different
- * rows must not overlap) for dq_out, dk_out = dL/dq_out, dL/dk_out (contiguous),
+ * rows must not overlap: strides that lay rows of dq, or of dk, on one another are
+ * refused) for dq_out, dk_out = dL/dq_out, dL/dk_out (contiguous),
  * and dwq, dwk float32 [d] (both NULL: not wanted), all overwritten.
  * ws: la_qk_norm_rope_workspace_size bytes. */
 LA_API la_status la_qk_norm_rope_backward(const la_rope_desc* desc, const void* q,

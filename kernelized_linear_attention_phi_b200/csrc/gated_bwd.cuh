@@ -55,7 +55,7 @@ template <typename T, int D, int PARTS, int COPIES> struct BwdSmem {
 // relu + 1: 6.1e-3 with one part). Under the identity map dg needs them: the sums
 // over a chunk's queries of phi(q) . (S dout) all carry the same rounding of S
 // (1 x 16 x 32768 x 128: dg 2.2e-3 off with one part here and one in the records
-// below, 1.7e-3 with two and fp32; that costs the sweeps 440 -> 537 and 549 -> 592 us).
+// below, 1.7e-3 with two and fp32; 4 x 16 x 8192 x 128: sweeps 440 -> 537 and 549 -> 592 us).
 template <typename T, int D, int PHI> struct BwdQ {
     static constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
     static constexpr int COPIES = D == 128 && PARTS == 2 ? 1 : Shape<T, D>::SB;
@@ -122,11 +122,11 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16(a, b);
 }
 
-// First sweep. 4x16x8192x64 bf16: 209 us for 201 MB of rows and 71 MB of chunk
-// states (1.3 TB/s), fp32 650 us; 1x16x32768x128 bf16, identity: 390 us, 7.5 us
+// First sweep. 4x16x8192x64 bf16: 234 us for 336 MB of rows and 136 MB of chunk
+// states (2.0 TB/s), fp32 660 us; 1x16x32768x128 bf16, identity: 494 us, 9.5 us
 // for a chunk of 64 tokens. A chunk's products follow from one another over four
 // barriers, and registers and shared memory leave an SM 8 warps at d = 128 (12 at 64)
-// to cover for it: shared memory 60 % busy, the tensor pipe 32 %, issue 25 %.
+// to cover for it: shared memory 62 % busy, the tensor pipe 33 %, issue 27 %.
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
@@ -436,8 +436,8 @@ gated_bwd_q_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     finish(nch - 1);
 }
 
-// Second sweep, bound like the first. 4x16x8192x64 bf16: 219 us, fp32 745 us;
-// 1x16x32768x128 bf16, identity: 488 us (shared memory 65 % busy, the tensor pipe 29 %).
+// Second sweep, bound like the first. 4x16x8192x64 bf16: 235 us, fp32 744 us;
+// 1x16x32768x128 bf16, identity: 541 us (shared memory 64 % busy, the tensor pipe 30 %).
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? 3 : 1)
 gated_bwd_kv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ gate,

@@ -31,8 +31,8 @@ template <typename T, int D> struct StateSmem {
 
 // The outputs of one block of a head's chunks, from the state in front of the
 // block (a record of `prefix`, or S_in / z_in, or nothing). 4x16x8192x64 bf16:
-// 110 us for 268 MB (2.4 TB/s; shared memory 69 % busy with operands, the tensor
-// pipe 32 %, DRAM 29 %), fp32 455 us (three products for one). A short block is
+// 109 us for 268 MB (2.5 TB/s; shared memory 68 % busy with operands, the tensor
+// pipe 33 %, DRAM 29 %), fp32 451 us (three products for one). A short block is
 // the latency of its chunks: 2x8x4096x64 in blocks of four chunks 19 us.
 template <typename T, int D, int PHI>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, D == 64 ? (sizeof(T) == 2 ? 4 : 3) : 1)
@@ -202,7 +202,7 @@ gated_sweep_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 }
 
 // One block's own state (from zero) and the product of its gates. 4x16x8192x64
-// bf16: 49 us for 134 MB, fp32 137 us.
+// bf16: 51 us for 134 MB, fp32 139 us.
 //   REVERSE = false: X = k, Y = v, weights e^{b_last - b_j}, chunks in order;
 //   REVERSE = true (gradients): X = q, Y = dout, weights e^{b_i} / den_i, the
 //   z part weighted by col_i = -(out_i . dout_i), chunks from the last to the first.

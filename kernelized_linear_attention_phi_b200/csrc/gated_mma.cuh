@@ -1,4 +1,4 @@
-// Warp-level matrix tiles of the gated kernels (gated.cu, gated_bwd.cu).
+// Warp-level matrix tiles of the gated kernels (gated_fwd.cuh, gated_bwd.cuh).
 //
 // One 16 x 16 x 8 step of C += A B on the warp's matrix instructions, for two
 // element types with one lane layout. With g = lane / 4, t = lane % 4:
@@ -14,12 +14,13 @@
 //     the sums are fp32 sums. The order of k inside a step is free, so logical
 //     k = 2t, 2t + 1 take the instruction's k = t, t + 4 and both types share
 //     the layout.
-// These are not the tensor cores' fastest instructions, but at the intensity of
-// this method (about 60 flop per byte) they would keep up with memory: 8 cycles
-// for 16 x 8 x 16 on a quarter of an SM, 1300 cycles for a chunk at d = 64. The
-// state and the decayed products stay in registers between them, where the
-// decay changes them every chunk. d = 128 in bf16, where they would not keep up,
-// runs on tcgen05 going forward (tc_gated.cu).
+// These are not the tensor cores' fastest instructions. Their rate alone would do
+// at the intensity of this method (about 60 flop per byte: 8 cycles for
+// 16 x 8 x 16 on a quarter of an SM, 1300 cycles for a chunk at d = 64), but every
+// operand comes out of shared memory, and that is what the kernels wait for (68 %
+// busy at 38 % of a copy's rate, 4x16x8192x64 forward). The state and the decayed
+// products stay in registers between them, where the decay changes them every
+// chunk. d = 128 in bf16 runs on tcgen05 going forward (tc_gated.cu).
 #pragma once
 
 #include "common.cuh"

@@ -12,9 +12,9 @@
 // written), 16 bytes per lane, d / 8 (bf16) or d / 4 (fp32) lanes per row. The
 // lanes of a token keep its cosines and sines in registers and run over
 // several heads, so the tables (fp32, as wide as the rows) are read once per
-// head group and not once per row. Forward, 4x16384x(16+16)x64 bf16: 92 us for
-// 541 MB, 90 % of a copy's rate. Backward, 3x1777x(12+4)x128 fp32: 35 us for
-// 132 MB (57 %); 2x4096x(8+8)x64 bf16: 25 us for 51 MB, of which some 6 are
+// head group and not once per row. Forward, 4x16384x(16+16)x64 bf16: 95 us for
+// 541 MB, 87 % of a copy's rate. Backward, 3x1777x(12+4)x128 fp32: 34 us for
+// 132 MB (60 %); 2x4096x(8+8)x64 bf16: 23 us for 51 MB, of which some 6 are
 // the launch; registers (two rows and the sums of dw) hold it to 5 CTAs an SM.
 
 #include "common.cuh"

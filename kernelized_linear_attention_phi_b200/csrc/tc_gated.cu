@@ -21,7 +21,7 @@
 // the weight: without it products of some 2^37 left fp32. A chunk whose b all
 // lie above -16 has no such factors and keeps n_i = 0, which spares the identity
 // map its pass over Q (1x16x131072x128: sweep 467 us with the pass in every
-// chunk, 433 with the choice; the other maps pass over Q anyway). Where b_i < -60,
+// chunk, 433 - 440 with the choice; the other maps pass over Q anyway). Where b_i < -60,
 // P~_ij = (q'_i.phi(k_j)) 2^(b_i + 60 - b_j), which leaves the state in front a
 // weight of 2^(-60) next to the query's own key instead of the smaller true one
 // (at 2^(-90) features below 2^(-36) would leave bf16's normal range).
@@ -284,8 +284,8 @@ tc_gated_state_kernel(const __grid_constant__ CUtensorMap mK, const __grid_const
 // "state" (phi on Q; S^T: the bf16 operand, and its decay in place), warps 14..17 "mask"
 // (P~, denominators), warps 18..21 "out" (O^T to the outputs). The transforms run a chunk ahead: the loop
 // from one S^T update to the next holds only the state warps' pass over S^T
-// and that update's products. 1x16x131072x128, relu + 1: 445 us for 2147 MB, 4.8
-// TB/s, 73 % of a copy's rate; the rest is that loop, about 3,750 cycles a chunk.
+// and that update's products. 1x16x131072x128, relu + 1: 463 us for 2147 MB, 4.6
+// TB/s, 71 % of a copy's rate; the rest is that loop, about 3,900 cycles a chunk.
 struct GtCfg {
     static constexpr int D = 128, C = 64, NB = 2;
     static constexpr int BOX = C * 128;            // one 64-row x 64-column box (8 KB)
